@@ -33,7 +33,8 @@
  *   - Work is enqueued on `stream` (NULL = the legacy default stream); the
  *     calls return before it completes.  te_q8_linear, te_q8_gated_linear,
  *     te_attn_varlen_fwd,
- *     the row ops and te_encoder_block_fwd are capturable in a CUDA graph
+ *     the row ops, te_i8_linear, te_i8_gated_linear, te_qk_rope_axes and
+ *     te_encoder_block_fwd are capturable in a CUDA graph
  *     (no host synchronisation, no allocation).
  */
 #ifndef TEFWD_H
@@ -295,6 +296,124 @@ te_status te_gate_act(const void *gu, int64_t ld, int32_t u_off, int32_t act, vo
 te_status te_pool_mean(const float *x, int32_t d, const int32_t *cu_host,
                        const int32_t *cu_dev, int32_t nseq, const float *w_final, float eps,
                        float *out, te_stream stream);
+
+/* ---- activations in 8 bits -------------------------------------------- */
+
+/* quant_rows: each row in 8 bits with a scale of its own.
+ *   a = max_j |x[r, j]|;  scale[r] = a / 127;  q[r, j] = rint(x[r, j] * (127 / a))
+ * in f32 (each operation rounded once, rint to nearest even), so that
+ * x ~ scale * q with |q| <= 127.  A row with a < 2^-120 (all zeros included)
+ * gets scale 0 and q 0; a row that holds an infinity or a NaN gets scale NaN
+ * and q 0, so that its products are NaN and no other row's are.
+ * x [t, ldx] of xdt (f32/bf16), q int8 [t, ldq], scale f32 [t].
+ * d % 8 == 0, 8 <= d <= 16384; ldq a multiple of 16.  q may not overlap x.
+ * The pages hold activations in f16 only; this and te_i8_linear are the same
+ * projections with the activation narrowed like the weights. */
+te_status te_quant_rows(const void *x, int32_t xdt, int64_t ldx, int8_t *q, int64_t ldq,
+                        float *scale, int32_t t, int32_t d, te_stream stream);
+
+/* rownorm_quant: the pre-norm and the quantisation in one pass: quant_rows of
+ *   v = Norm(pre * x) * w (+ b), times (1 + mod_scale) when given
+ * (te_rownorm_mod's arithmetic; v stays f32, it is not rounded to bf16
+ * between).  x may be f32 or bf16; b: LN only, or NULL; mod_scale f32 [d] or
+ * NULL.  Sizes and the other arguments as te_quant_rows. */
+te_status te_rownorm_quant(const void *x, int32_t xdt, int64_t ldx, const float *w, const float *b,
+                           const float *mod_scale, int32_t kind, float eps, float pre, int8_t *q,
+                           int64_t ldq, float *scale, int32_t t, int32_t d, te_stream stream);
+
+/* i8_linear: te_q8_linear with the activation in 8 bits and a scale a token:
+ *   y_i[t, o] = (x_scale[t] * sum_j x[t, j] * q_i[o, j]) * scale_i[o]  (+ bias_i[o])  (+ residual_i[t, o])
+ * x: int8 [m, k] (leading dimension ldx, a multiple of 16), x_scale f32 [m]
+ * (4-byte aligned).  Items as te_q8_linear, q8_row weights only (block_scale
+ * and col NULL); an item's epilogue activation is applied to the f32 value.
+ * The sum runs over exact integer products in 32 bits: exact whenever no
+ * partial sum reaches 2^24 in magnitude (any k <= 1040, and in practice sums
+ * of both signs at every k), else rounded like an f32 sum.
+ * Sizes: m >= 0, 64 <= k <= 65536, k % 64 == 0, 1 <= z <= 4.
+ * workspace: te_i8_workspace(m, k, n) bytes or more with n the sum of the
+ * items' n, 256-byte aligned (may be NULL when that is 0).  It holds nothing
+ * between calls; calls that may run at the same time need one each.
+ * Capturable in a CUDA graph. */
+te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_scale, int32_t m, int32_t k,
+                       const te_q8_item *items, int32_t z, void *workspace, size_t ws_bytes,
+                       te_stream stream);
+
+/* i8_gated_linear: the gate|up projections and the gate from 8-bit
+ * activations, m[t, f] = act(g[t, f]) * u[t, f] (stored bf16), with g and u
+ * as te_i8_linear computes them.  Unlike te_q8_gated_linear g and u are not
+ * rounded to bf16 before the gate: the f32 product is rounded once.
+ * workspace: te_i8_workspace(m, k, 2 f) bytes.  Otherwise as
+ * te_q8_gated_linear and te_i8_linear. */
+te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const float *x_scale, int32_t m,
+                             int32_t k, const te_q8w *wg, const te_q8w *wu, int32_t act, void *out,
+                             int64_t ldm, void *workspace, size_t ws_bytes, te_stream stream);
+
+/* Workspace bytes of te_i8_linear / te_i8_gated_linear for m tokens of k
+ * values and n output features in all (0 for sizes they do not take). */
+size_t te_i8_workspace(int32_t m, int32_t k, int32_t n);
+
+/* ---- rotary positions with several axes -------------------------------- */
+
+/* Which two channels of a head turn together.  The first rot = sum of the
+ * sections channels of a head rotate, the rest pass unrotated.
+ *   TE_ROPE_SECTION_HALVES  within the section of an axis: channel i of its
+ *                           first half with channel i of its second half
+ *                           (te_qk_prep_rope's convention)
+ *   TE_ROPE_HEAD_HALVES     channel i with channel i + rot/2; the pairs
+ *                           i = 0..rot/2-1 go to the axes in runs of
+ *                           sections[a]/2
+ *   TE_ROPE_ADJACENT        channel 2i with channel 2i + 1 (sections in runs) */
+typedef enum {
+    TE_ROPE_SECTION_HALVES = 0,
+    TE_ROPE_HEAD_HALVES = 1,
+    TE_ROPE_ADJACENT = 2
+} te_rope_pairing;
+
+#define TE_ROPE_MAX_AXES 4
+#define TE_ROPE_MAX_PAIRS 128
+
+/* The layout of a multi-axis rotation, filled by te_rope_axes_init and kept
+ * by the caller (host memory; plain data).  turn[p] is pair p's angle a unit
+ * of position in units of 2^-64 of a full turn, axis[p] its axis. */
+typedef struct {
+    int32_t hd, axes, pairs, pairing;
+    int32_t sections[TE_ROPE_MAX_AXES];
+    uint8_t axis[TE_ROPE_MAX_PAIRS];
+    uint64_t turn[TE_ROPE_MAX_PAIRS];
+} te_rope_axes;
+
+/* rope_axes_init: fills *plan for heads of hd channels (hd % 8 == 0,
+ * 8 <= hd <= 256) and `axes` sections (1..4; each even and >= 2; their sum
+ * rot <= hd).  The angle of pair p at position t is t * f_p radians with
+ *   freq != NULL: f_p = freq[p], p = 0..rot/2-1 in section order (finite, >= 0)
+ *   whole == 0:   f = theta^(-2i/sections[a]) for pair i of axis a
+ *   whole != 0:   f = theta^(-2p/rot), p counted over the whole head
+ * (theta > 0).  Host only; no device is touched. */
+te_status te_rope_axes_init(te_rope_axes *plan, int32_t hd, int32_t axes, const int32_t *sections,
+                            double theta, int32_t whole, int32_t pairing, const double *freq);
+
+/* qk_rope_axes: q/k norm and rotary positions with several axes (time, height,
+ * width, ...), for the q heads (nq heads of hd channels from column q_off)
+ * and k heads (nkv from k_off) of src [rows, ld_src], written at the same
+ * columns of dst [rows, ld_dst]; both of dtype dt (f32 or bf16).  dst may be
+ * src itself with ld_dst == ld_src (in place); otherwise they may not
+ * overlap, and columns of dst that hold no q or k head are left as they are.
+ * Per row r and head: if qn/kn != NULL, x = x / sqrt(mean(x^2) + eps) * w
+ * (f32 [hd]); pair p then turns by pos[r, axis[p]] * f_p; q heads are
+ * multiplied by q_mul.  f32 arithmetic, rounded once.
+ * pos: int32 [rows, ldp] (device, ldp >= axes), any value, negative too: the
+ * angle is reduced exactly (64-bit fixed point), so far positions lose
+ * nothing.  It generalises te_qk_prep_rope ([EG2] EgQkv.sec, [ZI] Enc::block)
+ * to sections of different widths, with no tables.
+ * Rows (ld_src, ld_dst) and head offsets must be multiples of 16 bytes. */
+te_status te_qk_rope_axes(const void *src, int64_t ld_src, void *dst, int64_t ld_dst, int32_t dt,
+                          int32_t q_off, int32_t k_off, int32_t nq, int32_t nkv, int32_t hd,
+                          const float *qn, const float *kn, float eps, const te_rope_axes *plan,
+                          const int32_t *pos, int64_t ldp, float q_mul, int32_t rows,
+                          te_stream stream);
+
+/* sizeof(te_rope_axes) as this library was compiled (for a binding). */
+size_t te_rope_axes_size(void);
 
 /* One encoder block ([EG2] TextGpu::forward layer loop; [ZI] Enc::block;
  * [VIT] encode_image_gpu block loop). */

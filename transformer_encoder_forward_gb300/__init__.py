@@ -20,6 +20,8 @@ TE_NORM_RMS, TE_NORM_LN = 0, 1
 TE_ACT_GELU_TANH, TE_ACT_SILU = 0, 1
 TE_RESID_PLAIN, TE_RESID_SANDWICH = 0, 1
 TE_EPI_NONE, TE_EPI_GELU_TANH, TE_EPI_SILU = 0, 1, 2
+TE_ROPE_SECTION_HALVES, TE_ROPE_HEAD_HALVES, TE_ROPE_ADJACENT = 0, 1, 2
+TE_ROPE_MAX_AXES, TE_ROPE_MAX_PAIRS = 4, 128
 # TE_STATIC_SCRATCH_BYTES of tefwd.h: the scratch array of te_encoder_block_fwd_static
 TE_STATIC_SCRATCH_BYTES = 32 << 20
 # TE_BLOCK_PROF_EVENTS of tefwd.h: the step-boundary events of te_block_desc.prof_events
@@ -66,6 +68,12 @@ class te_block_desc(ctypes.Structure):
                 ("prof_events", c_p)]
 
 
+class te_rope_axes(ctypes.Structure):
+    _fields_ = [("hd", c_i32), ("axes", c_i32), ("pairs", c_i32), ("pairing", c_i32),
+                ("sections", c_i32 * TE_ROPE_MAX_AXES), ("axis", ctypes.c_uint8 * TE_ROPE_MAX_PAIRS),
+                ("turn", ctypes.c_uint64 * TE_ROPE_MAX_PAIRS)]
+
+
 _lib = None
 
 EXPORTS = {
@@ -96,6 +104,22 @@ EXPORTS = {
     "te_cast_bf16": (ctypes.c_int, [c_p, c_i64, c_p, c_i64, c_i32, c_i32, c_p]),
     "te_gate_act": (ctypes.c_int, [c_p, c_i64, c_i32, c_i32, c_p, c_i64, c_i32, c_i32, c_p]),
     "te_pool_mean": (ctypes.c_int, [c_p, c_i32, c_p, c_p, c_i32, c_p, c_f32, c_p, c_p]),
+    "te_quant_rows": (ctypes.c_int, [c_p, c_i32, c_i64, c_p, c_i64, c_p, c_i32, c_i32, c_p]),
+    "te_rownorm_quant": (ctypes.c_int, [c_p, c_i32, c_i64, c_p, c_p, c_p, c_i32, c_f32, c_f32, c_p,
+                                        c_i64, c_p, c_i32, c_i32, c_p]),
+    "te_i8_linear": (ctypes.c_int, [c_p, c_i64, c_p, c_i32, c_i32, ctypes.POINTER(te_q8_item), c_i32,
+                                    c_p, ctypes.c_size_t, c_p]),
+    "te_i8_gated_linear": (ctypes.c_int, [c_p, c_i64, c_p, c_i32, c_i32, ctypes.POINTER(te_q8w),
+                                          ctypes.POINTER(te_q8w), c_i32, c_p, c_i64, c_p,
+                                          ctypes.c_size_t, c_p]),
+    "te_i8_workspace": (ctypes.c_size_t, [c_i32, c_i32, c_i32]),
+    "te_rope_axes_init": (ctypes.c_int, [ctypes.POINTER(te_rope_axes), c_i32, c_i32,
+                                         ctypes.POINTER(c_i32), ctypes.c_double, c_i32, c_i32,
+                                         ctypes.POINTER(ctypes.c_double)]),
+    "te_rope_axes_size": (ctypes.c_size_t, []),
+    "te_qk_rope_axes": (ctypes.c_int, [c_p, c_i64, c_p, c_i64, c_i32, c_i32, c_i32, c_i32, c_i32,
+                                       c_i32, c_p, c_p, c_f32, ctypes.POINTER(te_rope_axes), c_p,
+                                       c_i64, c_f32, c_i32, c_p]),
     "te_encoder_block_workspace": (ctypes.c_size_t, [ctypes.POINTER(te_block_desc), c_i32]),
     "te_encoder_block_fwd": (ctypes.c_int, [ctypes.POINTER(te_block_desc), c_p, c_p, c_p, c_p, c_i32,
                                             c_p, ctypes.c_size_t, c_p]),
@@ -298,6 +322,141 @@ def pool_mean(x, cu_host, cu_dev, w_final, eps, out, stream=None):
     arr, hp = _host_i32(cu_host)
     _ok(lib().te_pool_mean(x.data_ptr(), x.shape[1], hp, cu_dev.data_ptr(), len(arr) - 1,
                            _ptr(w_final), eps, out.data_ptr(), _stream(stream)))
+
+
+# --------------------------------------------------- activations in 8 bits
+
+def _want(what: str, t, dtypes, *shape):
+    """Address of a tensor argument of the operators below, once it is seen to
+    lie on the current device with one of `dtypes`, the given shape (None: any
+    size) and a contiguous last axis."""
+    import torch
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: dtype {t.dtype}, not one of {dtypes}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: a tensor on the current CUDA device, not on {t.device}")
+    have = t.shape
+    if len(have) != len(shape) or any(n is not None and n != h for n, h in zip(shape, have)):
+        raise ValueError(f"{what}: shape {tuple(have)}, not {shape}")
+    if have[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: its last axis must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(what: str, t, dtypes, *shape):
+    return None if t is None else _want(what, t, dtypes, *shape)
+
+
+def _ld(t) -> int:
+    """Leading dimension of a matrix; a single row's stride says nothing."""
+    return t.stride(0) if t.shape[0] != 1 else max(t.stride(0), -(-t.shape[1] // 16) * 16)
+
+
+def _types():
+    import torch
+    return (torch.float32,), (torch.float32, torch.bfloat16), (torch.int8,), (torch.int32,)
+
+
+def _scratch(what: str, t):
+    """Address and size of a workspace (None: no workspace)."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: the workspace must be a contiguous CUDA tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def quant_rows(x, q, scale, stream=None):
+    """q (int8 [t, d]), scale (f32 [t]) = each row of x (f32 or bf16) in 8 bits."""
+    f32, real, i8, _ = _types()
+    t, d = x.shape
+    _ok(lib().te_quant_rows(_want("quant_rows: x", x, real, t, d), _dt(x), _ld(x),
+                            _want("quant_rows: q", q, i8, t, d), _ld(q),
+                            _want("quant_rows: scale", scale, f32, t), t, d, _stream(stream)))
+
+
+def rownorm_quant(x, w, b, kind, eps, q, scale, pre=1.0, mod_scale=None, stream=None):
+    """quant_rows of Norm(pre x) w (+b), times (1 + mod_scale) when given."""
+    f32, real, i8, _ = _types()
+    t, d = x.shape
+    _ok(lib().te_rownorm_quant(_want("rownorm_quant: x", x, real, t, d), _dt(x), _ld(x),
+                               _want("rownorm_quant: w", w, f32, d), _opt("rownorm_quant: b", b, f32, d),
+                               _opt("rownorm_quant: mod_scale", mod_scale, f32, d), kind, eps, pre,
+                               _want("rownorm_quant: q", q, i8, t, d), _ld(q),
+                               _want("rownorm_quant: scale", scale, f32, t), t, d, _stream(stream)))
+
+
+def i8_workspace(m: int, k: int, n: int) -> int:
+    """Workspace bytes of i8_linear (n: the items' features in all) and of
+    i8_gated_linear (n = 2 f)."""
+    return int(lib().te_i8_workspace(m, k, n))
+
+
+def i8_linear(xq, x_scale, items: Sequence[dict], workspace, stream=None):
+    """Grouped GEMM of int8 tokens xq (int8 [m, k], x_scale f32 [m]) with q8_row
+    weights; items as q8_linear (y [m, n] with leading dimension ldy).
+    workspace: a uint8 device tensor of i8_workspace(m, k, sum of n) bytes, or
+    None when that is 0."""
+    f32, real, i8, _ = _types()
+    m, k = xq.shape
+    arr = (te_q8_item * len(items))()
+    for i, it in enumerate(items):
+        y, w, r = it["y"], it["w"], it.get("residual")
+        arr[i] = te_q8_item(w, _want("i8_linear: y", y, real, m, w.n), it["ldy"], _dt(y),
+                            it.get("epilogue", TE_EPI_NONE),
+                            _opt("i8_linear: residual", r, f32, m, None), it.get("ldr", 0))
+    ws, nb = _scratch("i8_linear", workspace)
+    _ok(lib().te_i8_linear(_want("i8_linear: xq", xq, i8, m, k), _ld(xq),
+                           _want("i8_linear: x_scale", x_scale, f32, m), m, k, arr, len(items), ws, nb,
+                           _stream(stream)))
+
+
+def i8_gated_linear(xq, x_scale, wg: te_q8w, wu: te_q8w, act, out, workspace, stream=None):
+    """out (bf16) = act(x Wg^T) * (x Wu^T) from int8 tokens, rounded once;
+    workspace of i8_workspace(m, k, 2 f) bytes."""
+    import torch
+    f32, _, i8, _ = _types()
+    m, k = xq.shape
+    ws, nb = _scratch("i8_gated_linear", workspace)
+    _ok(lib().te_i8_gated_linear(_want("i8_gated_linear: xq", xq, i8, m, k), _ld(xq),
+                                 _want("i8_gated_linear: x_scale", x_scale, f32, m), m, k,
+                                 ctypes.byref(wg), ctypes.byref(wu), act,
+                                 _want("i8_gated_linear: out", out, (torch.bfloat16,), m, wg.n), _ld(out),
+                                 ws, nb, _stream(stream)))
+
+
+# ---------------------------------------- rotary positions with several axes
+
+def rope_axes_plan(hd, sections, theta=10000.0, pairing=TE_ROPE_SECTION_HALVES, whole=False,
+                   freq=None) -> te_rope_axes:
+    """The layout of a multi-axis rotation: `sections` channels a head for each
+    axis; frequencies theta^(-2i/section) (whole: theta^(-2p/rot) over the
+    whole head) or `freq`, radians a unit of position for each pair."""
+    plan = te_rope_axes()
+    sec = (c_i32 * len(sections))(*[int(s) for s in sections])
+    f = None
+    if freq is not None:
+        if 2 * len(freq) != sum(int(s) for s in sections):
+            raise ValueError("rope_axes_plan: one frequency for each pair of the sections")
+        f = (ctypes.c_double * len(freq))(*[float(v) for v in freq])
+    _ok(lib().te_rope_axes_init(ctypes.byref(plan), hd, len(sections), sec, theta, 1 if whole else 0,
+                                pairing, f))
+    return plan
+
+
+def qk_rope_axes(src, ld_src, dst, ld_dst, q_off, k_off, nq, nkv, hd, qn, kn, eps,
+                 plan: te_rope_axes, pos, q_mul, rows, stream=None):
+    """q/k norm + rotation of the q and k heads of src into the same columns of
+    dst (dst may be src); pos int32 [rows, axes] on the device."""
+    f32, real, _, i32 = _types()
+    if src.dtype != dst.dtype:
+        raise TypeError(f"qk_rope_axes: src is {src.dtype}, dst {dst.dtype}")
+    _ok(lib().te_qk_rope_axes(_want("qk_rope_axes: src", src, real, rows, None), ld_src,
+                              _want("qk_rope_axes: dst", dst, real, rows, None), ld_dst, _dt(src),
+                              q_off, k_off, nq, nkv, hd, _opt("qk_rope_axes: qn", qn, f32, hd),
+                              _opt("qk_rope_axes: kn", kn, f32, hd), eps, ctypes.byref(plan),
+                              _want("qk_rope_axes: pos", pos, i32, rows, plan.axes), _ld(pos), q_mul,
+                              rows, _stream(stream)))
 
 
 def block_workspace(desc: te_block_desc, t: int) -> int:
