@@ -35,6 +35,13 @@ te_status make_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base
                       uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                       CUtensorMapSwizzle sw);
 
+// The tensor-core products of 8-bit activations (q8_linear.cu): xh is the
+// activation widened to f16 [m, k], ts its token scales; arguments checked.
+te_status i8_gemm_linear(const void *xh, const float *ts, int32_t m, int32_t k, const te_q8_item *items, int32_t z,
+                         cudaStream_t s);
+te_status i8_gemm_gated(const void *xh, const float *ts, int32_t m, int32_t k, const te_q8w *wg, const te_q8w *wu,
+                        int32_t act, void *out, int64_t ldm, cudaStream_t s);
+
 // Bounded-wait error words: each translation unit with bounded waits owns one
 // and exposes a reader that returns and clears it (0 = nothing happened).
 int read_clear_gemm_error();
@@ -507,6 +514,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
     return (1u << 4)                              // D format f32
            | (1u << 7)                            // A format bf16
            | (1u << 10)                           // B format bf16
+           | ((uint32_t)(N >> 3) << 17)           // N / 8
+           | ((uint32_t)(M >> 4) << 24);          // M / 16
+}
+
+// The same for f16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+    return (1u << 4)                              // D format f32; A and B format 0: f16
            | ((uint32_t)(N >> 3) << 17)           // N / 8
            | ((uint32_t)(M >> 4) << 24);          // M / 16
 }

@@ -89,6 +89,43 @@ __global__ void __launch_bounds__(256) i8_tile_kernel(const __grid_constant__ I8
     }
 }
 
+// x int8 [m, k] (rows ldx apart) widened to f16 [m, k], exactly: 16 values a
+// thread, 16 bytes in and 32 out.  q + 128 as the low byte of the f16 pattern
+// 0x64xx reads 1024 + q + 128; subtracting 1152 leaves q.
+__global__ void __launch_bounds__(256) widen_kernel(const int8_t *__restrict__ x, long long ldx,
+                                                    __half *__restrict__ y, long long total, int chunks) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= total) return;
+    const long long r = i / chunks;
+    const int c = (int)(i - r * chunks);
+    const uint4 v = *reinterpret_cast<const uint4 *>(x + r * ldx + 16 * c);
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    uint32_t out[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t u = in[j] ^ 0x80808080u;
+        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+        out[2 * j] = *reinterpret_cast<const uint32_t *>(&l);
+        out[2 * j + 1] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(y + 16 * i);
+    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+te_status widen(const int8_t *x, int64_t ldx, void *y, int m, int k, cudaStream_t s) {
+    const int chunks = k / 16;
+    const long long total = (long long)m * chunks, blocks = (total + 255) / 256;
+    if (blocks > 0x7FFFFFFFll) return fail(TE_ESHAPE, "i8_linear: m * k too large");
+    widen_kernel<<<(unsigned)blocks, 256, 0, s>>>(x, ldx, static_cast<__half *>(y), total, chunks);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear: widen launch");
+}
+
+constexpr int SMALL_M = 8;
 constexpr int MAX_K = 65536;
 
 te_status check_x(const char *what, const void *x, int64_t ldx, const float *xs, int32_t m, int32_t k) {
@@ -131,10 +168,8 @@ te_status launched(const char *what) {
 using namespace tefwd;
 
 extern "C" size_t te_i8_workspace(int32_t m, int32_t k, int32_t n) {
-    (void)m;
-    (void)k;
-    (void)n;
-    return 0;
+    if (m <= SMALL_M || k < 64 || k > MAX_K || k % 64 || n < 32) return 0;
+    return ((size_t)m * k * 2 + 255) & ~(size_t)255;
 }
 
 extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_scale, int32_t m,
@@ -191,6 +226,11 @@ extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_s
     if (n > 0x7FFFFFFFll) return fail(TE_ESHAPE, "i8_linear: too many output features");
     if ((st = check_ws("i8_linear", workspace, ws_bytes, te_i8_workspace(m, k, (int32_t)n))) != TE_OK) return st;
     if (m == 0) return TE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (m > SMALL_M) {
+        if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
+        return i8_gemm_linear(workspace, x_scale, m, k, items, z, s);
+    }
     i8_tile_kernel<false><<<dim3(tiles, (m + 63) / 64), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     return launched("i8_linear launch");
 }
@@ -212,6 +252,11 @@ extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const floa
     if (!aligned16(out)) return fail(TE_EALIGN, "i8_gated_linear: out not 16-byte aligned");
     if ((st = check_ws("i8_gated_linear", workspace, ws_bytes, te_i8_workspace(m, k, 2 * f))) != TE_OK) return st;
     if (m == 0) return TE_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (m > SMALL_M) {
+        if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
+        return i8_gemm_gated(workspace, x_scale, m, k, wg, wu, act, out, ldm, s);
+    }
     I8Params p;
     memset(&p, 0, sizeof(p));
     p.x = x;

@@ -39,6 +39,11 @@
 //     blocks go out in chunks, one shared-memory fence a chunk.  In
 //     the gated form each lane quadrant holds 16 gate rows and the same
 //     features' up rows, paired by register shuffles.
+// Products of 8-bit activations (I8: te_i8_linear, te_i8_gated_linear) run
+// through the same pipeline on f16 operands: the activation arrives widened to
+// f16 (i8_linear.cu; |x| <= 128 is exact), the weights are widened to f16 in
+// two instructions a pair, and the drain multiplies each token by its scale,
+// which a draining warp keeps in shared memory for its token tile.
 // The issuing thread's instruction rate bounds the MMA rate at N <= 192 (one
 // thread issues a 2-SM MMA every ~45 cycles at best), so its loop is kept
 // lean.  With long K a unit can hold two token tiles: each widened weight
@@ -102,11 +107,12 @@ struct Params {
     int tgroup;               // token tiles per group of the unit order
     int kb32;                 // k / 32: the row stride of the block scales
     int res;                  // resident weights (see q8_gemm_kernel)
+    const float *ts;          // 8-bit activations: the token scales [m]
 };
 
 __device__ int g_gemm_err;
 
-template <int BN, int TPA>
+template <int BN, int TPA, bool I8 = false>
 struct Layout {
     static constexpr int HALF = BN / 2;                 // token rows each CTA of the pair holds
     // shared-memory load stages (a stage holds TPA token tiles)
@@ -131,8 +137,12 @@ struct Layout {
     // else 4 KB; 128-byte aligned (TMA sources).  q8_2f: each stage's 128 column-field values
     // (f32), for the gate and the up weight in the gated form
     static constexpr int COL_OFF = W_OFF + NST * WBYTES;
-    static constexpr int COL_BYTES = 2 * BK * 4;
-    static constexpr int STG_OFF = COL_OFF + NST * COL_BYTES;
+    static constexpr int COL_BYTES = I8 ? 0 : 2 * BK * 4;
+    // 8-bit activations: each of the (up to eight) draining warps' token
+    // scales of one token tile
+    static constexpr int TS_OFF = COL_OFF + NST * COL_BYTES;
+    static constexpr int TS_BYTES = I8 ? 8 * BN * 4 : 0;
+    static constexpr int STG_OFF = TS_OFF + TS_BYTES;
     static constexpr int STG_WARP = TPA == 1 && BN <= 128 ? 8192 : 4096;
     static constexpr int STG_BYTES = 4 * STG_WARP;
     // one-tile units at N = 128: 4 KB a warp for four converter warps that
@@ -169,6 +179,19 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
     const float f3 = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7653)) - magic;
     lo = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
     hi = __byte_perm(__float_as_uint(f2), __float_as_uint(f3), 0x7632);
+}
+
+// int8 x4 -> two f16x2 words, exactly.  u = q + 128 as the low byte of the f16
+// pattern 0x64xx reads 1024 + q + 128; one paired subtraction of 1152 leaves
+// q, which needs 8 of f16's 11 significant bits.
+__device__ __forceinline__ void widen4_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // As widen4, value e multiplied by its own factor c[e] (the q8_2f column
@@ -280,10 +303,110 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
                  : "memory");
 }
 
-template <int BN, bool GATED, int TPA>
+// One 32-token block of the gated form, in a draining warp whose lanes 0-15
+// hold the gate rows and 16-31 the up rows of its 16 features: v becomes the
+// outputs yv, lane l's for tokens 0-15 of feature l and lane l + 16's for
+// tokens 16-31.  Scale and bias, then gate lane l and up lane l + 16 swap half
+// their tokens, then m = act(g) * u, in f32 pairs.  bf16 activations: both
+// halves are rounded to bf16 before the gate, as a stored g|u panel would be,
+// and the activation takes the hardware tanh (error below that rounding).
+// 8-bit activations (ts: the block's 32 token scales in shared memory): g and
+// u stay f32 and the activation is exact to f32 rounding, so that the output
+// is rounded once.
+template <bool I8, int ACT>
+__device__ __forceinline__ void gate_block(const uint32_t (&v)[32], float sc, float bi, const float *ts, bool upper,
+                                           float (&yv)[16]) {
+    const uint64_t sc2 = f2_pack(sc, sc), bi2 = f2_pack(bi, bi), half2 = f2_pack(0.5f, 0.5f);
+    float gv[16], uv[16];
+    float4 ta, tb;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        uint64_t v2 = f2_pack(__uint_as_float(v[j]), __uint_as_float(v[16 + j]));
+        if constexpr (I8) {
+            if ((j & 3) == 0) {
+                ta = *reinterpret_cast<const float4 *>(ts + j);
+                tb = *reinterpret_cast<const float4 *>(ts + 16 + j);
+            }
+            const float t0 = (j & 3) == 0 ? ta.x : ((j & 3) == 1 ? ta.y : ((j & 3) == 2 ? ta.z : ta.w));
+            const float t1 = (j & 3) == 0 ? tb.x : ((j & 3) == 1 ? tb.y : ((j & 3) == 2 ? tb.z : tb.w));
+            v2 = f2_mul(v2, f2_pack(t0, t1));
+        }
+        float lo, hi;
+        f2_unpack(f2_fma(v2, sc2, bi2), lo, hi);
+        if constexpr (!I8) {
+            const uint32_t b2 = pack_bf16x2(lo, hi);
+            lo = bf16_lo(b2);
+            hi = bf16_hi(b2);
+        }
+        // the gate lane sends its token 16 + j, the up lane its token j
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, upper ? lo : hi, 16);
+        // operands selected first: one activation per lane, no branch
+        gv[j] = upper ? got : lo;
+        uv[j] = upper ? hi : got;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        if constexpr (I8) {
+            yv[j] = apply_act(gv[j], ACT) * uv[j];
+            yv[j + 1] = apply_act(gv[j + 1], ACT) * uv[j + 1];
+        } else {
+            const uint64_t g2 = f2_pack(gv[j], gv[j + 1]);
+            // GELU-tanh: z = g (0.79788456 + 0.035677408 g^2); SiLU: z = g / 2
+            uint64_t z2;
+            if constexpr (ACT == TE_ACT_GELU_TANH)
+                z2 = f2_mul(g2, f2_fma(f2_pack(0.035677408f, 0.035677408f), f2_mul(g2, g2),
+                                       f2_pack(0.79788456f, 0.79788456f)));
+            else
+                z2 = f2_mul(half2, g2);
+            float z0, z1;
+            f2_unpack(z2, z0, z1);
+            const uint64_t h2 = f2_mul(half2, g2);
+            const uint64_t a2 = f2_fma(h2, f2_pack(hw_tanh(z0), hw_tanh(z1)), h2);
+            f2_unpack(f2_mul(a2, f2_pack(uv[j], uv[j + 1])), yv[j], yv[j + 1]);
+        }
+    }
+}
+
+// s*acc + b of one 32-token block in place (f32 bits), two tokens an
+// instruction; 8-bit activations: (acc * ts) * s + b with the block's 32 token
+// scales ts in shared memory.
+template <bool I8>
+__device__ __forceinline__ void scale_block(uint32_t (&v)[32], float sc, float bi, const float *ts) {
+    const uint64_t sc2 = f2_pack(sc, sc), bi2 = f2_pack(bi, bi);
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        uint64_t a2 = f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+        uint64_t b2 = f2_pack(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+        if constexpr (I8) {
+            const float4 t = *reinterpret_cast<const float4 *>(ts + j);
+            a2 = f2_mul(a2, f2_pack(t.x, t.y));
+            b2 = f2_mul(b2, f2_pack(t.z, t.w));
+        }
+        float y0, y1, y2, y3;
+        f2_unpack(f2_fma(a2, sc2, bi2), y0, y1);
+        f2_unpack(f2_fma(b2, sc2, bi2), y2, y3);
+        v[j] = __float_as_uint(y0);
+        v[j + 1] = __float_as_uint(y1);
+        v[j + 2] = __float_as_uint(y2);
+        v[j + 3] = __float_as_uint(y3);
+    }
+}
+
+// The ungated MLP's activation of one block, act(bf16(y)); 8-bit activations:
+// act(y) of the f32 value.
+template <bool I8>
+__device__ __forceinline__ void act_block(uint32_t (&v)[32], int act) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float y = __uint_as_float(v[j]);
+        v[j] = __float_as_uint(I8 ? apply_act(y, act) : apply_act_tanh(round_bf16(y), act));
+    }
+}
+
+template <int BN, bool GATED, int TPA, bool I8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     q8_gemm_kernel(const __grid_constant__ Params p) {
-    using L = Layout<BN, TPA>;
+    using L = Layout<BN, TPA, I8>;
     constexpr int NST = L::NST;
     constexpr int NA = L::NA;
     constexpr int HALF = L::HALF;
@@ -360,6 +483,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     auto fills = [&](int i) {
         return !res || i == 0 || unit_at(i) / p.ttiles != unit_at(i - 1) / p.ttiles;
     };
+    // 8-bit activations: this draining warp's token scales of the token tile
+    // from token t0 on (zero past m), staged before the tile's drain; warps
+    // 2-5 and 10-13 drain
+    float *tsw = reinterpret_cast<float *>(smem + L::TS_OFF) + (warp >= 10 ? warp - 6 : (warp - 2) & 3) * BN;
+    auto stage_ts = [&](int t0) {
+        if constexpr (I8) {
+            float t[BN / 32];
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) t[c] = t0 + 32 * c + lane < p.m ? p.ts[t0 + 32 * c + lane] : 0.f;
+            __syncwarp();                       // the previous tile's scales have been read
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) tsw[32 * c + lane] = t[c];
+            __syncwarp();
+        }
+    };
     // With helpers: the drain of unit lt's accumulator (one token tile), blocks
     // [cb, ce), by the calling warp (lane quadrant warp & 3), in chunks of two
     // blocks through its own 4-block ring at shared address hstg (gslot: the
@@ -380,6 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const float *bias = upper ? p.it[tc.zi].bias2 : p.it[tc.zi].bias;
         const float sc = ov ? (scale ? scale[o] : 1.f) : 0.f;
         const float bi = (ov && bias) ? bias[o] : 0.f;
+        stage_ts(tc.t0 * BN);
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_accfull + 8 * b, ph))) return false;
         tc_fence_after();
         const int act = p.it[tc.zi].act;
@@ -391,7 +530,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const int cend = ce < cn ? ce : cn;
         const int fo = tc.o0 + 16 * q;
         const int jb = upper ? 16 : 0;
-        const uint64_t sc2 = f2_pack(sc, sc), bi2 = f2_pack(bi, bi), half2 = f2_pack(0.5f, 0.5f);
         for (int c0 = cb; c0 < cend && fo < n; c0 += 2) {
             const int ceb = c0 + 2 < cend ? c0 + 2 : cend;
             if (lane < 2) bulk_wait_read_n<1>();
@@ -400,31 +538,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 uint32_t v[32];
                 tmem_ld32(tbase + tl + acol + 32 * c, v);
                 tmem_wait_ld();
-                float gv[16], uv[16], yv[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float lo, hi;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[16 + j])), sc2, bi2), lo, hi);
-                    const uint32_t b2 = pack_bf16x2(lo, hi);
-                    lo = bf16_lo(b2);
-                    hi = bf16_hi(b2);
-                    const float got = __shfl_xor_sync(0xFFFFFFFFu, upper ? lo : hi, 16);
-                    gv[j] = upper ? got : lo;
-                    uv[j] = upper ? hi : got;
-                }
-                const bool gelu = act == TE_ACT_GELU_TANH;
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const uint64_t g2 = f2_pack(gv[j], gv[j + 1]);
-                    const uint64_t z2 = gelu ? f2_mul(g2, f2_fma(f2_pack(0.035677408f, 0.035677408f), f2_mul(g2, g2),
-                                                                 f2_pack(0.79788456f, 0.79788456f)))
-                                             : f2_mul(half2, g2);
-                    float z0, z1;
-                    f2_unpack(z2, z0, z1);
-                    const uint64_t h2 = f2_mul(half2, g2);
-                    const uint64_t a2 = f2_fma(h2, f2_pack(hw_tanh(z0), hw_tanh(z1)), h2);
-                    f2_unpack(f2_mul(a2, f2_pack(uv[j], uv[j + 1])), yv[j], yv[j + 1]);
-                }
+                float yv[16];
+                if (act == TE_ACT_GELU_TANH)
+                    gate_block<I8, TE_ACT_GELU_TANH>(v, sc, bi, tsw + 32 * c, upper, yv);
+                else
+                    gate_block<I8, TE_ACT_SILU>(v, sc, bi, tsw + 32 * c, upper, yv);
                 const uint32_t so = hstg + (uint32_t)(((gslot + c - c0) & 3) * 1024);
                 uint16_t *ostg_h = reinterpret_cast<uint16_t *>(smem + (so - sb));
 #pragma unroll
@@ -476,50 +594,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const float *bias = upper ? it.bias2 : it.bias;
         const float sc = ov ? (scale ? scale[o] : 1.f) : 0.f;
         const float bi = (ov && bias) ? bias[o] : 0.f;
+        const int t0 = (tc.t0 * 2 + 1) * BN;
+        stage_ts(t0);
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_accfull, lt & 1))) return false;
         tc_fence_after();
-        const int t0 = (tc.t0 * 2 + 1) * BN;
         const int cn = t0 >= p.m ? 0 : ((p.m - t0 + 31) / 32 < BN / 32 ? (p.m - t0 + 31) / 32 : BN / 32);
         const int fo = tc.o0 + (GATED ? 16 : 32) * q;
         const void *ymap = &p.ty[tc.zi];
         const bool f32out = it.ydt == TE_F32;
         const bool inplace = it.resid != nullptr && it.resid == it.y;
-        const uint64_t sc2 = f2_pack(sc, sc), bi2 = f2_pack(bi, bi);
         for (int c = e_blocks2(tc.zi, cn); c < cn && fo < it.n; ++c) {
             uint32_t v[32];
             tmem_ld32(tbase + tl + BN + 32 * c, v);
             tmem_wait_ld();
             const int tb = t0 + 32 * c;
             if constexpr (GATED) {
-                // the epilogue's gated form: scale and bias, both halves
-                // rounded to bf16, gate and up lanes swap half their tokens,
-                // m = act(g) * u in f32 pairs
-                const uint64_t half2 = f2_pack(0.5f, 0.5f);
-                float gv[16], uv[16], yv[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float lo, hi;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[16 + j])), sc2, bi2), lo, hi);
-                    const uint32_t b2 = pack_bf16x2(lo, hi);
-                    lo = bf16_lo(b2);
-                    hi = bf16_hi(b2);
-                    const float got = __shfl_xor_sync(0xFFFFFFFFu, upper ? lo : hi, 16);
-                    gv[j] = upper ? got : lo;
-                    uv[j] = upper ? hi : got;
-                }
-                const bool gelu = it.act == TE_ACT_GELU_TANH;
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const uint64_t g2 = f2_pack(gv[j], gv[j + 1]);
-                    const uint64_t z2 = gelu ? f2_mul(g2, f2_fma(f2_pack(0.035677408f, 0.035677408f), f2_mul(g2, g2),
-                                                                 f2_pack(0.79788456f, 0.79788456f)))
-                                             : f2_mul(half2, g2);
-                    float z0, z1;
-                    f2_unpack(z2, z0, z1);
-                    const uint64_t h2 = f2_mul(half2, g2);
-                    const uint64_t a2 = f2_fma(h2, f2_pack(hw_tanh(z0), hw_tanh(z1)), h2);
-                    f2_unpack(f2_mul(a2, f2_pack(uv[j], uv[j + 1])), yv[j], yv[j + 1]);
-                }
+                float yv[16];
+                if (it.act == TE_ACT_GELU_TANH)
+                    gate_block<I8, TE_ACT_GELU_TANH>(v, sc, bi, tsw + 32 * c, upper, yv);
+                else
+                    gate_block<I8, TE_ACT_SILU>(v, sc, bi, tsw + 32 * c, upper, yv);
                 // the store two blocks back, which used this slot, has read it
                 if (lane == 0) bulk_wait_read_n<1>();
                 __syncwarp();
@@ -537,18 +631,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 }
                 ++hslot;
             } else {
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    float a, b2;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2, bi2), a, b2);
-                    v[j] = __float_as_uint(a);
-                    v[j + 1] = __float_as_uint(b2);
-                }
-                if (it.act) {   // the ungated MLP: act(bf16(s*acc + b))
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = __float_as_uint(apply_act_tanh(round_bf16(__uint_as_float(v[j])), it.act - 1));
-                }
+                scale_block<I8>(v, sc, bi, tsw + 32 * c);
+                if (it.act) act_block<I8>(v, it.act - 1);   // the ungated MLP
                 if (f32out) {
                     // 16-token halves (the two-tile units' f32 maps have
                     // 16-row boxes), each after the previous has been read
@@ -604,8 +688,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const bool fl = fills(i);   // weights (and column field) only when widened
             const TileCoord tc = tile_coord<GATED>(p, u, rank);
             const void *wmap = &p.tw[tc.zi];
-            const float *cg = fl ? p.it[tc.zi].col : nullptr;
-            const float *cu2 = GATED && fl ? p.it[tc.zi].col2 : nullptr;
+            const float *cg = !I8 && fl ? p.it[tc.zi].col : nullptr;
+            const float *cu2 = !I8 && GATED && fl ? p.it[tc.zi].col2 : nullptr;
             for (int kb = 0; kb < nkb; ++kb, ++kbg) {
                 const int s = kbg % NST;
                 const uint32_t fb = bar_full + 8 * s;
@@ -647,7 +731,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         // one divergent lane cost about 84 cycles an MMA).
         if (leader) {
             const uint32_t e = elect_one();
-            constexpr uint32_t idesc = idesc_bf16_f32(2 * BM, BN);
+            constexpr uint32_t idesc = I8 ? idesc_f16_f32(2 * BM, BN) : idesc_bf16_f32(2 * BM, BN);
             // the loop keeps its indices incremental: ring slot s and A stage
             // ar with their phases
             int nfill = 0, s = 0, ar = 0;
@@ -790,8 +874,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             {
                 const TileCoord tc = tile_coord<GATED>(p, u, rank);
                 const int o = tc.o0 + frow;
-                const uint16_t *b = upper ? p.it[tc.zi].bsc2 : p.it[tc.zi].bsc;
-                colp = upper ? p.it[tc.zi].col2 : p.it[tc.zi].col;
+                const uint16_t *b = I8 ? nullptr : (upper ? p.it[tc.zi].bsc2 : p.it[tc.zi].bsc);
+                colp = I8 ? nullptr : (upper ? p.it[tc.zi].col2 : p.it[tc.zi].col);
                 blk = b != nullptr;
                 if (blk && o < p.it[tc.zi].n) bsr = b + (long long)o * p.kb32;
             }
@@ -822,7 +906,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 const uint8_t *wrow = smem + L::W_OFF + s * L::WBYTES + h * L::WBOX + srow * 64;
                 const int sw = (srow >> 1) & 3;
                 uint32_t r[32];
-                if (colp) {
+                if constexpr (I8) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(wrow + ((c ^ sw) << 4));
+                        widen4_f16(v.x, r[8 * c + 0], r[8 * c + 1]);
+                        widen4_f16(v.y, r[8 * c + 2], r[8 * c + 3]);
+                        widen4_f16(v.z, r[8 * c + 4], r[8 * c + 5]);
+                        widen4_f16(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    }
+                } else if (colp) {
                     // column field of K = kb*128 + h*64 + 16c + e, staged with the
                     // weight tile (zero past k: the weight reads zeros there too)
                     const int k0 = kb * BK + h * BOX;
@@ -925,6 +1018,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const float *bias = upper ? p.it[tc.zi].bias2 : p.it[tc.zi].bias;
             const float sc = ov ? (scale ? scale[o] : 1.f) : 0.f;
             const float bi = (ov && bias) ? bias[o] : 0.f;
+            stage_ts(tc.t0 * TPA * BN);
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_accfull + 8 * b, ph));
             if (!ok) break;
             tc_fence_after();
@@ -971,23 +1065,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                         tmem_wait_ld();
                         {
                             // v[] becomes the output values in place (f32 bits)
-                            // s*acc + b in f32 pairs (two tokens an instruction)
-                            {
-                                const uint64_t sc2 = f2_pack(sc, sc), bi2 = f2_pack(bi, bi);
-#pragma unroll
-                                for (int j = 0; j < 32; j += 2) {
-                                    float a, b2;
-                                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2, bi2),
-                                              a, b2);
-                                    v[j] = __float_as_uint(a);
-                                    v[j + 1] = __float_as_uint(b2);
-                                }
-                            }
-                            if (act) {   // the ungated MLP: act(bf16(s*acc + b)), no residual
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    v[j] = __float_as_uint(apply_act_tanh(round_bf16(__uint_as_float(v[j])), act - 1));
-                            }
+                            scale_block<I8>(v, sc, bi, tsw + 32 * c);
+                            if (act) act_block<I8>(v, act - 1);   // the ungated MLP, no residual
                             if constexpr (BYTES == 4096) {
                                 float *ostg_f = reinterpret_cast<float *>(smem + (so - sb));
 #pragma unroll
@@ -1046,7 +1125,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             // its predecessor's store every time)
             auto drain_f32_halves = [&](int acol, int t0, int cn, int fo) {
                 constexpr int HB = 2048;
-                const uint64_t sc2 = f2_pack(sc, sc), bi2 = f2_pack(bi, bi);
                 auto half_out = [&](const uint32_t (&v)[32], int h, int tb) {
                     const bool resize = slot_bytes != HB + 1;   // HB + 1: this form's mark
                     if (resize) {
@@ -1076,19 +1154,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     uint32_t v[32];
                     tmem_ld32(tbase + tl + acol + 32 * c, v);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float a, b2;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2, bi2), a,
-                                  b2);
-                        v[j] = __float_as_uint(a);
-                        v[j + 1] = __float_as_uint(b2);
-                    }
-                    if (act) {   // the ungated MLP with an f32 output: act(bf16(s*acc + b))
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = __float_as_uint(apply_act_tanh(round_bf16(__uint_as_float(v[j])), act - 1));
-                    }
+                    scale_block<I8>(v, sc, bi, tsw + 32 * c);
+                    if (act) act_block<I8>(v, act - 1);   // the ungated MLP with an f32 output
                     const int tb = t0 + 32 * c;
                     half_out(v, 0, tb);
                     if (tb + 16 < p.m) half_out(v, 1, tb + 16);
@@ -1102,6 +1169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             // drained by converter warps 2-5 (see e_blocks2)
             const int cn0 = t0 >= p.m ? 0 : ((p.m - t0 + 31) / 32 < BN / 32 ? (p.m - t0 + 31) / 32 : BN / 32);
             const int cn = L::HELP2 && tt == 1 ? e_blocks2(tc.zi, cn0) : cn0;
+            if (tt == 1 && cn > 0) stage_ts(t0);
             // this warp's first output feature: a warp whose features all lie
             // past n (a phantom tile) has nothing to drain
             const int fo = tc.o0 + (GATED ? 16 : 32) * q;
@@ -1112,49 +1180,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                     // Before a chunk, all but the previous chunk's GBSZ groups
                     // have finished reading - after a chunk of fewer stores
                     // (a ragged last tile), all of them.
-                    // one 32-token block: scale and bias, both halves rounded
-                    // to bf16 (one conversion for the pair); gate lane l and up
-                    // lane l + 16 swap half their tokens, so that lane l
-                    // computes m = act(g) * u for tokens 0-15 and lane l + 16
-                    // for tokens 16-31 of feature 16 q + l; the arithmetic in
-                    // f32 pairs (two tokens an instruction, each rounded as
-                    // the scalar form), the tanh one token at a time
-                    auto gated_math = [&](auto act_c, const uint32_t (&v)[32], float (&yv)[16]) {
-                        constexpr int ACT = decltype(act_c)::value;
-                        const uint64_t sc2 = f2_pack(sc, sc), bi2 = f2_pack(bi, bi);
-                        const uint64_t half2 = f2_pack(0.5f, 0.5f);
-                        float gv[16], uv[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float lo, hi;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[16 + j])), sc2, bi2),
-                                      lo, hi);
-                            const uint32_t b2 = pack_bf16x2(lo, hi);
-                            lo = bf16_lo(b2);
-                            hi = bf16_hi(b2);
-                            // the gate lane sends its token 16 + j, the up lane its token j
-                            const float got = __shfl_xor_sync(0xFFFFFFFFu, upper ? lo : hi, 16);
-                            // operands selected first: one activation per lane, no branch
-                            gv[j] = upper ? got : lo;
-                            uv[j] = upper ? hi : got;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const uint64_t g2 = f2_pack(gv[j], gv[j + 1]);
-                            // GELU-tanh: z = g (0.79788456 + 0.035677408 g^2); SiLU: z = g / 2
-                            uint64_t z2;
-                            if constexpr (ACT == TE_ACT_GELU_TANH)
-                                z2 = f2_mul(g2, f2_fma(f2_pack(0.035677408f, 0.035677408f), f2_mul(g2, g2),
-                                                       f2_pack(0.79788456f, 0.79788456f)));
-                            else
-                                z2 = f2_mul(half2, g2);
-                            float z0, z1;
-                            f2_unpack(z2, z0, z1);
-                            const uint64_t h2 = f2_mul(half2, g2);
-                            const uint64_t a2 = f2_fma(h2, f2_pack(hw_tanh(z0), hw_tanh(z1)), h2);
-                            f2_unpack(f2_mul(a2, f2_pack(uv[j], uv[j + 1])), yv[j], yv[j + 1]);
-                        }
-                    };
                     constexpr int GNB = L::STG_WARP / 1024;
                     constexpr int GBSZ = GNB / 2 < BN / 32 ? GNB / 2 : BN / 32;
                     static_assert(GBSZ == 2 || GBSZ == 4, "a ring of 2 GBSZ blocks indexed by a mask");
@@ -1173,9 +1198,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             tmem_wait_ld();
                             float yv[16];
                             if (act == TE_ACT_GELU_TANH)
-                                gated_math(std::integral_constant<int, TE_ACT_GELU_TANH>{}, v, yv);
+                                gate_block<I8, TE_ACT_GELU_TANH>(v, sc, bi, tsw + 32 * c, upper, yv);
                             else
-                                gated_math(std::integral_constant<int, TE_ACT_SILU>{}, v, yv);
+                                gate_block<I8, TE_ACT_SILU>(v, sc, bi, tsw + 32 * c, upper, yv);
                             const uint32_t so = stg + (uint32_t)(((gslot + c) & (2 * GBSZ - 1)) * 1024);
                             uint16_t *ostg_h = reinterpret_cast<uint16_t *>(smem + (so - sb));
 #pragma unroll
@@ -1434,9 +1459,9 @@ int split_rows(int m, int k, int ftiles, const TilePlan &t) {
     return split < plan_time(m, ftiles, t) ? m1 : m;
 }
 
-template <int BN, bool GATED, int TPA>
+template <int BN, bool GATED, int TPA, bool I8>
 te_status launch(Params &p, int ftiles, cudaStream_t stream) {
-    const int smem = Layout<BN, TPA>::BYTES + 1024;
+    const int smem = Layout<BN, TPA, I8>::BYTES + 1024;
     // per instantiation and device: dynamic shared memory size, and how many
     // 2-CTA clusters can be resident at once (the persistent grid's size)
     static int max_clusters[64] = {};
@@ -1445,7 +1470,7 @@ te_status launch(Params &p, int ftiles, cudaStream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, "q8_linear: cudaGetDevice");
     if (dev < 0 || dev >= 64) return fail(TE_EINVAL, "q8_linear: device %d out of range", dev);
     if (!max_clusters[dev]) {
-        e = cudaFuncSetAttribute(q8_gemm_kernel<BN, GATED, TPA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(q8_gemm_kernel<BN, GATED, TPA, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return cuda_fail(e, "q8_linear: set shared memory size");
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * sm_count(), 1, 1);
@@ -1459,7 +1484,7 @@ te_status launch(Params &p, int ftiles, cudaStream_t stream) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, q8_gemm_kernel<BN, GATED, TPA>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, q8_gemm_kernel<BN, GATED, TPA, I8>, &cfg);
         if (e != cudaSuccess || n < 1) n = sm_count() / 2;
         max_clusters[dev] = n;
     }
@@ -1472,7 +1497,7 @@ te_status launch(Params &p, int ftiles, cudaStream_t stream) {
     const long long tg = p.res ? p.ttiles : XGROUP_BYTES / xtile;
     p.tgroup = tg < 1 ? 1 : (tg > p.ttiles ? p.ttiles : (int)tg);
     const int clusters = p.nunits < max_clusters[dev] ? p.nunits : max_clusters[dev];
-    q8_gemm_kernel<BN, GATED, TPA><<<2 * clusters, NTHREADS, smem, stream>>>(p);
+    q8_gemm_kernel<BN, GATED, TPA, I8><<<2 * clusters, NTHREADS, smem, stream>>>(p);
     e = cudaGetLastError();
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "q8_linear launch");
 }
@@ -1512,6 +1537,146 @@ te_status make_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(TE_ECUDA, "q8_linear: cuTensorMapEncodeTiled failed (%d)", (int)r);
     return TE_OK;
+}
+
+// The rows of a grouped product in one launch, or in two with a tile each (see
+// split_rows).  p holds everything but the maps and the row-dependent
+// pointers; x: bf16 [p.m, p.k] (I8: f16).
+template <bool I8>
+static te_status linear_parts(const Params &p, const void *x, int64_t ldx, const te_q8_item *items, int ftiles,
+                              cudaStream_t s) {
+    const int m = p.m, k = p.k, z = p.z;
+    const TilePlan t1 = tile_for(m, k, ftiles);
+    const int m1 = split_rows(m, k, ftiles, t1);
+    // rows [r0, r0 + mr) with tile t: the maps and item pointers start at row r0
+    auto part = [&](int r0, int mr, const TilePlan &t) -> te_status {
+        Params q = p;
+        q.m = mr;
+        q.res = t.res;
+        if (I8) q.ts = p.ts + r0;
+        const char *xb = static_cast<const char *>(x) + (size_t)r0 * ldx * 2;
+        // each CTA of a cluster pair TMA-loads its own half of the token tile
+        te_status st = make_map_2d(&q.tx, I8 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, xb,
+                                   (uint64_t)k, (uint64_t)mr, (uint64_t)ldx * 2, BOX, t.bn / 2,
+                                   CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != TE_OK) return st;
+        for (int i = 0; i < z; ++i) {
+            const bool f32 = items[i].y_dtype == TE_F32;
+            Item &d = q.it[i];
+            d.y = static_cast<char *>(items[i].y) + (size_t)r0 * items[i].ldy * (f32 ? 4 : 2);
+            if (items[i].residual) d.resid = items[i].residual + (size_t)r0 * items[i].ldr;
+            st = make_map_2d(&q.tw[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, items[i].w.q, (uint64_t)k,
+                             (uint64_t)items[i].w.n, (uint64_t)k, BOX, BM, CU_TENSOR_MAP_SWIZZLE_64B);
+            if (st != TE_OK) return st;
+            // f32 outputs without a separate residual go out in 16-token halves
+            // where a warp's staging holds one 32-token f32 block (every tile
+            // but the one-tile units at N <= 128): the kernel's own condition
+            const bool halves = f32 && !(t.tpa == 1 && t.bn <= 128) &&
+                                !(items[i].residual && items[i].residual != items[i].y);
+            st = make_map_2d(&q.ty[i], f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                             d.y, (uint64_t)items[i].w.n, (uint64_t)mr, (uint64_t)items[i].ldy * (f32 ? 4 : 2), 32,
+                             halves ? 16 : 32, CU_TENSOR_MAP_SWIZZLE_NONE);
+            if (st != TE_OK) return st;
+        }
+        if (t.bn == 192) return t.tpa == 2 ? launch<192, false, 2, I8>(q, ftiles, s) : launch<192, false, 1, I8>(q, ftiles, s);
+        if (t.bn == 128) return t.tpa == 2 ? launch<128, false, 2, I8>(q, ftiles, s) : launch<128, false, 1, I8>(q, ftiles, s);
+        return launch<64, false, 1, I8>(q, ftiles, s);
+    };
+    te_status st = part(0, m1, t1);
+    if (st == TE_OK && m1 < m) st = part(m1, m - m1, tail_tile(m - m1, k, ftiles));
+    return st;
+}
+
+// The gated form's rows, likewise; wg, wu: int8 [p.it[0].n, p.k].
+template <bool I8>
+static te_status gated_parts(const Params &p, const void *x, int64_t ldx, const int8_t *wg, const int8_t *wu,
+                             void *out, int64_t ldm, cudaStream_t s) {
+    const int m = p.m, k = p.k, f = p.it[0].n;
+    const int ftiles = p.it[0].ntiles;
+    const TilePlan t1 = tile_for(m, k, ftiles);
+    const int m1 = split_rows(m, k, ftiles, t1);
+    auto part = [&](int r0, int mr, const TilePlan &t) -> te_status {
+        Params q = p;
+        q.m = mr;
+        q.res = t.res;
+        if (I8) q.ts = p.ts + r0;
+        const char *xb = static_cast<const char *>(x) + (size_t)r0 * ldx * 2;
+        char *ob = static_cast<char *>(out) + (size_t)r0 * ldm * 2;
+        q.it[0].y = ob;
+        te_status st = make_map_2d(&q.tx, I8 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, xb,
+                                   (uint64_t)k, (uint64_t)mr, (uint64_t)ldx * 2, BOX, t.bn / 2,
+                                   CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != TE_OK) return st;
+        if ((st = make_map_2d(&q.tw[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, wg, (uint64_t)k, (uint64_t)f,
+                              (uint64_t)k, BOX, BM / 2, CU_TENSOR_MAP_SWIZZLE_64B)) != TE_OK)
+            return st;
+        if ((st = make_map_2d(&q.tw[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, wu, (uint64_t)k, (uint64_t)f,
+                              (uint64_t)k, BOX, BM / 2, CU_TENSOR_MAP_SWIZZLE_64B)) != TE_OK)
+            return st;
+        // each epilogue warp stores 16 features x 32 tokens of a block
+        if ((st = make_map_2d(&q.ty[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ob, (uint64_t)f, (uint64_t)mr,
+                              (uint64_t)ldm * 2, 16, 32, CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_OK)
+            return st;
+        if (t.bn == 192)
+            return t.tpa == 2 ? launch<192, true, 2, I8>(q, ftiles, s) : launch<192, true, 1, I8>(q, ftiles, s);
+        if (t.bn == 128)
+            return t.tpa == 2 ? launch<128, true, 2, I8>(q, ftiles, s) : launch<128, true, 1, I8>(q, ftiles, s);
+        return launch<64, true, 1, I8>(q, ftiles, s);
+    };
+    te_status st = part(0, m1, t1);
+    if (st == TE_OK && m1 < m) st = part(m1, m - m1, tail_tile(m - m1, k, ftiles));
+    return st;
+}
+
+// The products of 8-bit activations for i8_linear.cu, which has checked the
+// arguments: xh is the activation widened to f16 [m, k], ts its token scales.
+te_status i8_gemm_linear(const void *xh, const float *ts, int32_t m, int32_t k, const te_q8_item *items, int32_t z,
+                         cudaStream_t s) {
+    Params p;
+    memset(&p, 0, sizeof(p));
+    p.z = z;
+    p.m = m;
+    p.k = k;
+    p.ts = ts;
+    int ftiles = 0;
+    for (int i = 0; i < z; ++i) {
+        Item &d = p.it[i];
+        d.scale = items[i].w.scale;
+        d.bias = items[i].w.bias;
+        d.y = items[i].y;
+        d.resid = items[i].residual;
+        d.ldy = items[i].ldy;
+        d.ldr = items[i].ldr;
+        d.n = items[i].w.n;
+        d.ydt = items[i].y_dtype;
+        d.act = items[i].epilogue;
+        d.tile0 = ftiles;
+        d.ntiles = (d.n + BM - 1) / BM;
+        ftiles += d.ntiles;
+    }
+    return linear_parts<true>(p, xh, k, items, ftiles, s);
+}
+
+te_status i8_gemm_gated(const void *xh, const float *ts, int32_t m, int32_t k, const te_q8w *wg, const te_q8w *wu,
+                        int32_t act, void *out, int64_t ldm, cudaStream_t s) {
+    Params p;
+    memset(&p, 0, sizeof(p));
+    p.z = 1;
+    p.m = m;
+    p.k = k;
+    p.ts = ts;
+    Item &d = p.it[0];
+    d.scale = wg->scale;
+    d.bias = wg->bias;
+    d.scale2 = wu->scale;
+    d.bias2 = wu->bias;
+    d.y = out;
+    d.ldy = ldm;
+    d.n = wg->n;
+    d.ydt = TE_BF16;
+    d.act = act;
+    d.ntiles = (wg->n + BM / 2 - 1) / (BM / 2);
+    return gated_parts<true>(p, xh, k, wg->q, wu->q, out, ldm, s);
 }
 
 int read_clear_gemm_error() {
@@ -1591,44 +1756,7 @@ extern "C" te_status te_q8_linear(const void *x, int64_t ldx, int32_t m, int32_t
         ftiles += d.ntiles;
     }
     if (m == 0) return TE_OK;
-    const TilePlan t1 = tile_for(m, k, ftiles);
-    const int m1 = split_rows(m, k, ftiles, t1);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // rows [r0, r0 + mr) with tile t: the maps and item pointers start at row r0
-    auto part = [&](int r0, int mr, const TilePlan &t) -> te_status {
-        Params q = p;
-        q.m = mr;
-        q.res = t.res;
-        const char *xb = static_cast<const char *>(x) + (size_t)r0 * ldx * 2;
-        // each CTA of a cluster pair TMA-loads its own half of the token tile
-        te_status st = make_map_2d(&q.tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, xb, (uint64_t)k, (uint64_t)mr,
-                                   (uint64_t)ldx * 2, BOX, t.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B);
-        if (st != TE_OK) return st;
-        for (int i = 0; i < z; ++i) {
-            const bool f32 = items[i].y_dtype == TE_F32;
-            Item &d = q.it[i];
-            d.y = static_cast<char *>(items[i].y) + (size_t)r0 * items[i].ldy * (f32 ? 4 : 2);
-            if (items[i].residual) d.resid = items[i].residual + (size_t)r0 * items[i].ldr;
-            st = make_map_2d(&q.tw[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, items[i].w.q, (uint64_t)k,
-                             (uint64_t)items[i].w.n, (uint64_t)k, BOX, BM, CU_TENSOR_MAP_SWIZZLE_64B);
-            if (st != TE_OK) return st;
-            // f32 outputs without a separate residual go out in 16-token halves
-            // where a warp's staging holds one 32-token f32 block (every tile
-            // but the one-tile units at N <= 128): the kernel's own condition
-            const bool halves = f32 && !(t.tpa == 1 && t.bn <= 128) &&
-                                !(items[i].residual && items[i].residual != items[i].y);
-            st = make_map_2d(&q.ty[i], f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                             d.y, (uint64_t)items[i].w.n, (uint64_t)mr, (uint64_t)items[i].ldy * (f32 ? 4 : 2), 32,
-                             halves ? 16 : 32, CU_TENSOR_MAP_SWIZZLE_NONE);
-            if (st != TE_OK) return st;
-        }
-        if (t.bn == 192) return t.tpa == 2 ? launch<192, false, 2>(q, ftiles, s) : launch<192, false, 1>(q, ftiles, s);
-        if (t.bn == 128) return t.tpa == 2 ? launch<128, false, 2>(q, ftiles, s) : launch<128, false, 1>(q, ftiles, s);
-        return launch<64, false, 1>(q, ftiles, s);
-    };
-    te_status st = part(0, m1, t1);
-    if (st == TE_OK && m1 < m) st = part(m1, m - m1, tail_tile(m - m1, k, ftiles));
-    return st;
+    return linear_parts<false>(p, x, ldx, items, ftiles, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" te_status te_q8_gated_linear(const void *x, int64_t ldx, int32_t m, int32_t k,
@@ -1680,38 +1808,7 @@ extern "C" te_status te_q8_gated_linear(const void *x, int64_t ldx, int32_t m, i
     d.tile0 = 0;
     d.ntiles = (f + BM / 2 - 1) / (BM / 2);
     if (m == 0) return TE_OK;
-    const int ftiles = d.ntiles;
-    const TilePlan t1 = tile_for(m, k, ftiles);
-    const int m1 = split_rows(m, k, ftiles, t1);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // rows [r0, r0 + mr) with tile t (see te_q8_linear)
-    auto part = [&](int r0, int mr, const TilePlan &t) -> te_status {
-        Params q = p;
-        q.m = mr;
-        q.res = t.res;
-        const char *xb = static_cast<const char *>(x) + (size_t)r0 * ldx * 2;
-        char *ob = static_cast<char *>(out) + (size_t)r0 * ldm * 2;
-        q.it[0].y = ob;
-        te_status st = make_map_2d(&q.tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, xb, (uint64_t)k, (uint64_t)mr,
-                                   (uint64_t)ldx * 2, BOX, t.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B);
-        if (st != TE_OK) return st;
-        if ((st = make_map_2d(&q.tw[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, wg->q, (uint64_t)k, (uint64_t)f,
-                              (uint64_t)k, BOX, BM / 2, CU_TENSOR_MAP_SWIZZLE_64B)) != TE_OK)
-            return st;
-        if ((st = make_map_2d(&q.tw[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, wu->q, (uint64_t)k, (uint64_t)f,
-                              (uint64_t)k, BOX, BM / 2, CU_TENSOR_MAP_SWIZZLE_64B)) != TE_OK)
-            return st;
-        // each epilogue warp stores 16 features x 32 tokens of a block
-        if ((st = make_map_2d(&q.ty[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ob, (uint64_t)f, (uint64_t)mr,
-                              (uint64_t)ldm * 2, 16, 32, CU_TENSOR_MAP_SWIZZLE_NONE)) != TE_OK)
-            return st;
-        if (t.bn == 192) return t.tpa == 2 ? launch<192, true, 2>(q, ftiles, s) : launch<192, true, 1>(q, ftiles, s);
-        if (t.bn == 128) return t.tpa == 2 ? launch<128, true, 2>(q, ftiles, s) : launch<128, true, 1>(q, ftiles, s);
-        return launch<64, true, 1>(q, ftiles, s);
-    };
-    te_status st = part(0, m1, t1);
-    if (st == TE_OK && m1 < m) st = part(m1, m - m1, tail_tile(m - m1, k, ftiles));
-    return st;
+    return gated_parts<false>(p, x, ldx, wg->q, wu->q, out, ldm, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" te_status te_mma_peak(int32_t bn, int32_t stages, float *ms, te_stream stream) {
