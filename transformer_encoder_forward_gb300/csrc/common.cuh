@@ -46,6 +46,9 @@ te_status i8_gemm_gated(const void *xh, const float *ts, int32_t m, int32_t k, c
 // and exposes a reader that returns and clears it (0 = nothing happened).
 int read_clear_gemm_error();
 int read_clear_attn_error();
+// Device address of the products' error word, for kernels of other
+// translation units that report there.
+te_status gemm_error_word(int **word);
 
 // ---------------------------------------------------------------- device side
 

@@ -14,13 +14,15 @@ namespace tefwd {
 namespace {
 
 constexpr int MAXZ = 4;
+constexpr int SMS = 152;      // GB300
 
 struct I8Item {
     const int8_t *w, *w2;          // w2: the up projection of the gated form
     const float *scale, *bias, *scale2, *bias2, *resid;
     void *y;
     long long ldy, ldr;
-    int n, ydt, act, tile0;
+    int n, ydt, act;
+    int tile0;                // first row group
 };
 
 struct I8Params {
@@ -31,67 +33,540 @@ struct I8Params {
     I8Item it[MAXZ];
 };
 
-// 64 tokens x 64 features a CTA, 4 x 4 a thread, exact 32-bit integer sums by
-// the 4-way byte dot product.
-template <bool GATED>
-__global__ void __launch_bounds__(256) i8_tile_kernel(const __grid_constant__ I8Params p) {
-    __shared__ int xs[64][17], ws[GATED ? 128 : 64][17];
+// int8 x4 -> two f16x2 words, exactly: q + 128 as the low byte of the f16
+// pattern 0x64xx reads 1024 + q + 128; subtracting 1152 leaves q.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t word(const uint4 &v, int j) { return j == 0 ? v.x : (j == 1 ? v.y : (j == 2 ? v.z : v.w)); }
+
+// Few tokens: bound by the weights' bytes, which go from global memory
+// straight into tensor-core fragments (the register form mma.sync: at this
+// intensity a TMEM pipeline would only add latency).  A CTA takes MT x 16
+// weight rows; its ks warps each take every ks-th 128 bytes of k.  The order
+// of k inside a product is free as long as both operands share it, so lane
+// 4 g + t loads 16 consecutive bytes of rows g and g + 8 at k + 16 t, and of
+// tokens g, g + 8, ..., and word j of each is its share of the j-th 16-deep
+// product.  Rows and tokens are widened to f16 in registers (exact), five
+// instructions a word; D slots of 128 bytes are in flight meanwhile, and
+// alternate products add into separate sums (a chain of dependent products
+// would wait for each one's latency).  The warps' sums meet in shared memory,
+// always in the same order.
+// Gated: tile 0 is 16 gate rows, tile 1 the same features' up rows.
+template <int NT, int MT, bool GATED, int D>
+__global__ void __launch_bounds__(256) i8_small_kernel(const __grid_constant__ I8Params p) {
+    static_assert(!GATED || MT == 2, "a gate tile and an up tile");
+    extern __shared__ float part[];             // [ks][MT * 16 rows][NT * 8 tokens]
+    constexpr int ROWS = MT * 16, TOK = NT * 8, F = GATED ? 16 : ROWS, PW = ROWS * TOK;
+    constexpr int AS = 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ks = blockDim.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
     int zi = 0;
     while (zi + 1 < p.z && (int)blockIdx.x >= p.it[zi + 1].tile0) ++zi;
     const I8Item &it = p.it[zi];
-    const int o0 = ((int)blockIdx.x - it.tile0) * 64;
-    const long long t0 = (long long)blockIdx.y * 64;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int acc[4][4] = {}, acc2[4][4] = {};
-    for (int k0 = 0; k0 < p.k; k0 += 64) {
-        const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 4;
-        int4 v = make_int4(0, 0, 0, 0);
-        if (t0 + r < p.m) v = *reinterpret_cast<const int4 *>(p.x + (t0 + r) * p.ldx + k0 + 4 * c);
-        xs[r][c] = v.x; xs[r][c + 1] = v.y; xs[r][c + 2] = v.z; xs[r][c + 3] = v.w;
-        v = make_int4(0, 0, 0, 0);
-        if (o0 + r < it.n) v = *reinterpret_cast<const int4 *>(it.w + (long long)(o0 + r) * p.k + k0 + 4 * c);
-        ws[r][c] = v.x; ws[r][c + 1] = v.y; ws[r][c + 2] = v.z; ws[r][c + 3] = v.w;
-        if (GATED) {
-            v = make_int4(0, 0, 0, 0);
-            if (o0 + r < it.n) v = *reinterpret_cast<const int4 *>(it.w2 + (long long)(o0 + r) * p.k + k0 + 4 * c);
-            ws[GATED ? 64 + r : 0][c] = v.x; ws[GATED ? 64 + r : 0][c + 1] = v.y;
-            ws[GATED ? 64 + r : 0][c + 2] = v.z; ws[GATED ? 64 + r : 0][c + 3] = v.w;
+    const int o0 = ((int)blockIdx.x - it.tile0) * F;
+    const int8_t *wp[MT], *xp = p.x + (long long)g * p.ldx + 16 * t;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        wp[i] = (GATED && i == 1 ? it.w2 + (long long)(o0 + g) * p.k : it.w + (long long)(o0 + 16 * i + g) * p.k) + 16 * t;
+    uint4 w[D][MT][2][2], x[D][NT][2];
+    auto load = [&](uint4 (&wr)[MT][2][2], uint4 (&xr)[NT][2], int k0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool in = k0 + 64 * h < p.k;  // k is a multiple of 64
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    wr[i][r][h] = in ? __ldcs(reinterpret_cast<const uint4 *>(wp[i] + (long long)(8 * r) * p.k + k0 + 64 * h))
+                                     : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                xr[n][h] = in && g + 8 * n < p.m
+                               ? __ldg(reinterpret_cast<const uint4 *>(xp + (long long)(8 * n) * p.ldx + k0 + 64 * h))
+                               : make_uint4(0u, 0u, 0u, 0u);
         }
-        __syncthreads();
+    };
+    float acc[AS][MT][NT][4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+    for (int s = 0; s < AS; ++s)
 #pragma unroll
-            for (int a = 0; a < 4; ++a)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    acc[a][b] = __dp4a(xs[ty + 16 * a][j], ws[tx + 16 * b][j], acc[a][b]);
-                    if (GATED)
-                        acc2[a][b] = __dp4a(xs[ty + 16 * a][j], ws[(GATED ? 64 : 0) + tx + 16 * b][j], acc2[a][b]);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[s][i][n][e] = 0.f;
+    const int step = 128 * ks;
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(w[d], x[d], 128 * warp + d * step);
+    for (int k0 = 128 * warp; k0 < p.k; k0 += D * step) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {           // a slot past k holds zeros
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t a[MT][4];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        widen4(word(w[d][i][0][h], j), a[i][0], a[i][2]);
+                        widen4(word(w[d][i][1][h], j), a[i][1], a[i][3]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t b0, b1;
+                        widen4(word(x[d][n][h], j), b0, b1);
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) mma_16x8x16(acc[j % AS][i][n], a[i], b0, b1);
+                    }
                 }
-        __syncthreads();
+            if (k0 + (D + d) * step < p.k) load(w[d], x[d], k0 + (D + d) * step);
+            else if (k0 + D * step < p.k) {     // the next pass runs, without this slot
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) w[d][i][0][h] = w[d][i][1][h] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        }
     }
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        const long long t = t0 + ty + 16 * a;
-        if (t >= p.m) continue;
-        const float sx = p.xs[t];
+    for (int s = 1; s < AS; ++s)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int o = o0 + tx + 16 * b;
-            if (o >= it.n) continue;
-            float y = fmaf((float)acc[a][b] * sx, it.scale[o], it.bias ? it.bias[o] : 0.f);
-            if (GATED) y = apply_act(y, it.act) * fmaf((float)acc2[a][b] * sx, it.scale2[o], it.bias2 ? it.bias2[o] : 0.f);
-            else if (it.act != TE_EPI_NONE) y = apply_act(y, it.act - 1);
-            if (it.resid) y += it.resid[t * it.ldr + o];
-            if (it.ydt == TE_F32) static_cast<float *>(it.y)[t * it.ldy + o] = y;
-            else static_cast<__nv_bfloat16 *>(it.y)[t * it.ldy + o] = __float2bfloat16_rn(y);
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[0][i][n][e] += acc[s][i][n][e];
+    // lane 4 g + t holds rows g and g + 8 of each tile for tokens 2 t, 2 t + 1
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                *reinterpret_cast<float2 *>(part + warp * PW + (16 * i + 8 * r + g) * TOK + 8 * n + 2 * t) =
+                    make_float2(acc[0][i][n][2 * r], acc[0][i][n][2 * r + 1]);
+    __syncthreads();
+    // outputs, features fastest
+    for (int e = threadIdx.x; e < F * p.m; e += blockDim.x) {
+        const int f = e % F, tk = e / F, o = o0 + f;
+        float a = 0.f, a2 = 0.f;
+        for (int i = 0; i < ks; ++i) {
+            a += part[i * PW + f * TOK + tk];
+            if (GATED) a2 += part[i * PW + (16 + f) * TOK + tk];
         }
+        const float sx = p.xs[tk];
+        float y = fmaf(a * sx, it.scale[o], it.bias ? it.bias[o] : 0.f);
+        if (GATED)
+            y = apply_act(y, it.act) * fmaf(a2 * sx, it.scale2[o], it.bias2 ? it.bias2[o] : 0.f);
+        else if (it.act != TE_EPI_NONE)
+            y = apply_act(y, it.act - 1);
+        if (it.resid) y += it.resid[tk * it.ldr + o];
+        if (it.ydt == TE_F32)
+            static_cast<float *>(it.y)[tk * it.ldy + o] = y;
+        else
+            static_cast<__nv_bfloat16 *>(it.y)[tk * it.ldy + o] = __float2bfloat16_rn(y);
     }
 }
 
+// One CTA a group of MT x 16 rows, with as many warps as fill the device (16
+// an SM) while each still has 128 bytes of k.
+template <int NT, int MT, bool GATED>
+te_status small_launch(I8Params &p, cudaStream_t s) {
+    constexpr int F = GATED ? 16 : MT * 16;
+    constexpr int D = NT * MT == 1 ? 2 : 1;
+    int groups = 0;
+    for (int i = 0; i < p.z; ++i) {
+        p.it[i].tile0 = groups;
+        groups += p.it[i].n / F;
+    }
+    int ks = 1;
+    while (ks < 8 && (long long)groups * ks < SMS * 16 && 128 * ks < p.k) ks *= 2;
+    i8_small_kernel<NT, MT, GATED, D><<<groups, 32 * ks, ks * MT * 16 * NT * 8 * 4, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
+}
+// --------------------------------------------------- a middling token count
+//
+// Up to a few hundred tokens the products are still bound by the weights'
+// bytes or by latency: the wide tiles of the large pipeline (q8_linear.cu) leave
+// SMs idle there, and its activation needs a widening pass of its own.  Here a
+// CTA takes 128 weight rows (TMEM lanes) x N tokens x a share of k, in one
+// launch and without a workspace:
+//   * warp 0 streams stages of 128 k by TMA: the int8 weight rows and tokens
+//     (128-byte swizzle);
+//   * groups of four warps from warp 2 on, a lane quadrant a warp, take the stages in turn and
+//     widen them to f16, exactly: the weights into TMEM (the MMA's A operand),
+//     the tokens into shared memory in the MMA's 128-byte-swizzled layout (its
+//     B operand); several groups, because one stage's chain of load, widening,
+//     TMEM store and fence takes longer than its issue slots;
+//   * warp 1 issues the MMAs (kind::f16, M = 128, N, K = 16; f32 sums in TMEM);
+//   * the CTAs of a cluster share a tile and split k; at the end each sends
+//     its partial sums for a run of tokens to the CTA that owns the run (through
+//     distributed shared memory), which adds them in the order of k, scales
+//     and stores.
+// The split makes enough CTAs to fill the SMs, the ring (NS stages, two CTAs
+// an SM up to N = 32) keeps enough bytes in flight for HBM.  Every wait is
+// bounded; a wait that gives up sets the error word that te_check reads.
+template <int N>
+struct Mid {
+    static constexpr int G = N <= 32 ? 2 : (N <= 64 ? 4 : 3);       // converter groups of 4 warps
+    static constexpr int THREADS = 64 + 128 * G;
+    static constexpr int NS = N <= 64 ? 4 : 3;              // int8 stages
+    static constexpr int NA = N <= 32 ? 3 : G;              // widened stages
+    static constexpr int CTAS = N <= 32 ? 2 : 1;            // an SM
+    static constexpr int TMEM = 512 / CTAS;
+    // A wait for a phase must know that the phase before it is over.  Slots
+    // pass between the producer and one group only (NS a multiple of G), and a
+    // widened stage's MMAs are complete in order, G of them a turn.
+    static_assert(NS % G == 0 && NA >= G, "rings in phase with the groups");
+    static constexpr int WBYTES = 128 * 128;                // int8 weights of a stage
+    static constexpr int XBYTES = N * 128;                  // int8 tokens of a stage
+    static constexpr int SBYTES = WBYTES + XBYTES;
+    static constexpr int BBOX = N * 128;                    // 64 k of the widened tokens
+    static constexpr int B_OFF = NS * SBYTES;
+    static constexpr int BAR_OFF = B_OFF + NA * 2 * BBOX;
+    static constexpr int NBAR = 2 * NS + 2 * NA + 1;
+    static constexpr int BYTES = BAR_OFF + 8 * NBAR + 16;
+    static_assert(SBYTES % 1024 == 0 && BBOX % 1024 == 0, "swizzled tiles stay 1024-byte aligned");
+    static_assert(N * 128 * 4 <= B_OFF, "the partial sums reuse the ring");
+    static_assert(N + 64 * NA <= TMEM, "TMEM columns");
+    static_assert(BYTES + 1024 <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
+};
+
+struct MidParams {
+    CUtensorMap tx;                             // x int8 [m, k]
+    CUtensorMap tw[MAXZ];                       // weights int8 [n, k]
+    I8Item it[MAXZ];
+    const float *xs;
+    int *err;
+    int m, k, z;
+};
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int N, bool GATED>
+__global__ void __launch_bounds__(Mid<N>::THREADS) i8_mid_kernel(const __grid_constant__ MidParams p) {
+    using L = Mid<N>;
+    constexpr int NA = L::NA, NS = L::NS;
+    constexpr int F = GATED ? 64 : 128;         // features a tile
+    extern __shared__ uint8_t smem_raw[];
+    // the same offset in every CTA of a cluster: remote addresses agree
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem);
+    const uint32_t bar_full = sb + L::BAR_OFF, bar_empty = bar_full + 8 * NS, bar_afull = bar_empty + 8 * NS,
+                   bar_aempty = bar_afull + 8 * NA, bar_done = bar_aempty + 8 * NA;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFF + 8 * L::NBAR);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank, csize;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
+    const int S = (int)csize;
+    const int tile = (int)blockIdx.x / S;
+    const int t0 = (int)blockIdx.y * N;
+    int zi = 0;
+    while (zi + 1 < p.z && tile >= p.it[zi + 1].tile0) ++zi;
+    const I8Item &it = p.it[zi];
+    const int o0 = (tile - it.tile0) * F;
+    const int nkb = (p.k + 127) / 128;
+    const int kb0 = (int)((long long)nkb * rank / S), cnt = (int)((long long)nkb * (rank + 1) / S) - kb0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 4);    // a group of converter warps
+        }
+        for (int i = 0; i < NA; ++i) {
+            mbar_init(bar_afull + 8 * i, 4);
+            mbar_init(bar_aempty + 8 * i, 1);   // the MMAs' commit
+        }
+        mbar_init(bar_done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), L::TMEM);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+    bool ok = true;
+
+    if (warp == 0) {
+        const uint32_t e = elect_one();
+        for (int i = 0; i < cnt; ++i) {
+            const int s = i % NS;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_empty + 8 * s, ((i / NS) & 1) ^ 1));
+            if (!ok) break;
+            const uint32_t fb = bar_full + 8 * s, dst = sb + s * L::SBYTES;
+            const int k0 = (kb0 + i) * 128;
+            mbar_arrive_expect_tx_e(fb, L::SBYTES, e);
+            if (GATED) {                        // rows 0-63 gate, 64-127 up
+                tma_load_2d_e(dst, &p.tw[0], fb, k0, o0, e);
+                tma_load_2d_e(dst + L::WBYTES / 2, &p.tw[1], fb, k0, o0, e);
+            } else {
+                tma_load_2d_e(dst, &p.tw[zi], fb, k0, o0, e);
+            }
+            tma_load_2d_e(dst + L::WBYTES, &p.tx, fb, k0, t0, e);
+        }
+        // no copy of ours may land after the ring changes its use
+        for (int j = cnt - NS < 0 ? 0 : cnt - NS; j < cnt; ++j)
+            if (!mbar_wait(bar_full + 8 * (j % NS), (j / NS) & 1, 20000000ull)) ok = false;
+    } else if (warp == 1) {
+        const uint32_t e = elect_one();
+        constexpr uint32_t idesc = idesc_f16_f32(128, N);
+        for (int i = 0; i < cnt; ++i) {
+            const int a = i % NA;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_afull + 8 * a, (i / NA) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t d0 = smem_desc_sw128(sb + L::B_OFF + a * 2 * L::BBOX);
+            const uint32_t a0 = tbase + N + 64 * a;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                mma_ts_bf16_e(tbase, a0 + 8 * j, d0 + (uint64_t)(((j >> 2) * L::BBOX + (j & 3) * 32) >> 4), idesc,
+                              (uint32_t)(i != 0 || j != 0), e);
+            mma_commit_e(bar_aempty + 8 * a, e);
+        }
+        mma_commit_e(bar_done, e);              // every MMA issued above
+        if (!mbar_wait(bar_done, 0, 20000000ull)) ok = false;
+    } else {
+        const int q = warp & 3, row = 32 * q + lane;
+        for (int i = (warp - 2) >> 2; i < cnt; i += L::G) {
+            const int s = i % NS, a = i % NA;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * s, (i / NS) & 1) &&
+                                             mbar_wait(bar_aempty + 8 * a, ((i / NA) & 1) ^ 1));
+            if (!ok) break;
+            tc_fence_after();
+            const uint8_t *st = smem + s * L::SBYTES;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(st + row * 128 + (((4 * h + c) ^ (row & 7)) << 4));
+                    widen4(v.x, r[8 * c + 0], r[8 * c + 1]);
+                    widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+                    widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+                    widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+                }
+                tmem_st32(tbase + ((uint32_t)(32 * q) << 16) + N + 64 * a + 32 * h, r);
+            }
+            // tokens: 16-byte piece c of row r becomes pieces 2c, 2c + 1 of
+            // 128-byte rows, in the box of its half of k; the two halves' lanes
+            // store in opposite order, so that no two hit one bank
+#pragma unroll
+            for (int j = 0; j < N / 16; ++j) {
+                const int id = q * 2 * N + lane + 32 * j;
+                const int xr = id >> 3, c = id & 7;
+                const uint4 v = *reinterpret_cast<const uint4 *>(st + L::WBYTES + xr * 128 + ((c ^ (xr & 7)) << 4));
+                uint4 lo, hi;
+                widen4(v.x, lo.x, lo.y);
+                widen4(v.y, lo.z, lo.w);
+                widen4(v.z, hi.x, hi.y);
+                widen4(v.w, hi.z, hi.w);
+                uint8_t *box = smem + L::B_OFF + a * 2 * L::BBOX + (c >> 2) * L::BBOX + xr * 128;
+                const int p0 = 2 * (c & 3), first = c >> 2;
+                *reinterpret_cast<uint4 *>(box + (((p0 + first) ^ (xr & 7)) << 4)) = first ? hi : lo;
+                *reinterpret_cast<uint4 *>(box + (((p0 + 1 - first) ^ (xr & 7)) << 4)) = first ? lo : hi;
+            }
+            fence_async_smem();                 // the B tile, visible to the MMA
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar_afull + 8 * a);
+                mbar_arrive(bar_empty + 8 * s);
+            }
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar_done, 0));
+        tc_fence_after();
+    }
+    if (!ok && lane == 0) atomicExch(p.err, 1);
+    __syncwarp();
+
+    // Partial sums to the owners: token run d of TC tokens goes to CTA d, as
+    // [source CTA][token][128 rows].  All pipelines are done with their rings first.
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const int tn = p.m - t0 < N ? p.m - t0 : N; // tokens of this tile
+    const int TC = (tn + S - 1) / S;
+    if (warp >= 2 && warp < 10 && cnt > 0) {
+        const int q = warp & 3, h = (warp - 2) >> 2;
+        int d = h * (N / 2) / TC, tl = h * (N / 2) - d * TC;    // owner and place of the next token
+        const uint32_t mine = sb + (uint32_t)(((int)rank * TC * 128 + 32 * q + lane) * 4);
+        uint32_t to = mapa_shared(mine, d < S ? d : 0);
+#pragma unroll
+        for (int c8 = 0; c8 < N / 16; ++c8) {
+            const int c = h * (N / 2) + 8 * c8;
+            if (c >= tn) break;                 // warp-uniform
+            uint32_t v[8];
+            tmem_ld8(tbase + ((uint32_t)(32 * q) << 16) + c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (c + j < tn) st_cluster_f32(to + 512 * tl, __uint_as_float(v[j]));
+                if (++tl == TC) {
+                    tl = 0;
+                    to = mapa_shared(mine, ++d < S ? d : 0);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tbase, L::TMEM);
+    }
+    // Sums, scales and stores: a lane keeps 4 features (their scales and biases
+    // in registers), a warp takes a token (gated: two) at a time.
+    const int own = tn - (int)rank * TC < TC ? tn - (int)rank * TC : TC;
+    constexpr int LPT = F / 4;                  // lanes a token
+    const int f = 4 * (lane % LPT), o = o0 + f;
+    if (o >= it.n) return;                      // n is a multiple of 32
+    float4 sc, bi = make_float4(0.f, 0.f, 0.f, 0.f), sc2 = bi, bi2 = bi;
+    sc = make_float4(it.scale[o], it.scale[o + 1], it.scale[o + 2], it.scale[o + 3]);
+    if (it.bias) bi = make_float4(it.bias[o], it.bias[o + 1], it.bias[o + 2], it.bias[o + 3]);
+    if (GATED) {
+        sc2 = make_float4(it.scale2[o], it.scale2[o + 1], it.scale2[o + 2], it.scale2[o + 3]);
+        if (it.bias2) bi2 = make_float4(it.bias2[o], it.bias2[o + 1], it.bias2[o + 2], it.bias2[o + 3]);
+    }
+    for (int tl = warp * (32 / LPT) + lane / LPT; tl < own; tl += (L::THREADS / 32) * (32 / LPT)) {
+        const long long t = t0 + (int)rank * TC + tl;
+        const float sx = p.xs[t];
+        const float *b = reinterpret_cast<const float *>(smem) + tl * 128 + f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), u = a;
+        for (int i = 0; i < S; ++i, b += TC * 128) {
+            const float4 v = *reinterpret_cast<const float4 *>(b);
+            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+            if (GATED) {
+                const float4 v2 = *reinterpret_cast<const float4 *>(b + 64);
+                u.x += v2.x; u.y += v2.y; u.z += v2.z; u.w += v2.w;
+            }
+        }
+        float y[4] = {fmaf(a.x * sx, sc.x, bi.x), fmaf(a.y * sx, sc.y, bi.y), fmaf(a.z * sx, sc.z, bi.z),
+                      fmaf(a.w * sx, sc.w, bi.w)};
+        if (GATED) {
+            const float w[4] = {fmaf(u.x * sx, sc2.x, bi2.x), fmaf(u.y * sx, sc2.y, bi2.y),
+                                fmaf(u.z * sx, sc2.z, bi2.z), fmaf(u.w * sx, sc2.w, bi2.w)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = apply_act(y[j], it.act) * w[j];
+        } else if (it.act != TE_EPI_NONE) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = apply_act(y[j], it.act - 1);
+        }
+        if (it.resid) {
+            const float4 r = *reinterpret_cast<const float4 *>(it.resid + t * it.ldr + o);
+            y[0] += r.x; y[1] += r.y; y[2] += r.z; y[3] += r.w;
+        }
+        if (it.ydt == TE_F32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(it.y) + t * it.ldy + o) =
+                make_float4(y[0], y[1], y[2], y[3]);
+        else
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(it.y) + t * it.ldy + o) =
+                make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    }
+}
+
+// The split of k: the least of whole waves of CTAs times a CTA's stages, with
+// four stages' time for a CTA's start and end.  Returns the time in stages.
+double mid_split(int tiles, int nkb, int slots, int &split) {
+    double best = 1e30;
+    for (int s = 1; s <= 8 && s <= nkb; s *= 2) {
+        const int waves = (int)(((long long)tiles * s + slots - 1) / slots), stages = (nkb + s - 1) / s;
+        if ((double)waves * (stages + 4) < best - 1e-9) {
+            best = (double)waves * (stages + 4);
+            split = s;
+        }
+    }
+    return best - 4;
+}
+
+template <int N, bool GATED>
+te_status mid_launch(const I8Params &q, cudaStream_t s) {
+    constexpr int F = GATED ? 64 : 128, smem = Mid<N>::BYTES + 1024;
+    static bool ready[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return cuda_fail(e, "i8_linear: device");
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(i8_mid_kernel<N, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return cuda_fail(e, "i8_linear: set shared memory size");
+        ready[dev] = true;
+    }
+    MidParams p;
+    memset(&p, 0, sizeof(p));
+    te_status st = make_map_2d(&p.tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x, (uint64_t)q.k, (uint64_t)q.m, (uint64_t)q.ldx,
+                               128, N, CU_TENSOR_MAP_SWIZZLE_128B);
+    int tiles = 0;
+    for (int i = 0; i < q.z && st == TE_OK; ++i) {
+        p.it[i] = q.it[i];
+        p.it[i].tile0 = tiles;
+        tiles += (q.it[i].n + F - 1) / F;
+        st = make_map_2d(&p.tw[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q.it[i].w, (uint64_t)q.k, (uint64_t)q.it[i].n,
+                         (uint64_t)q.k, 128, F, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    if (GATED && st == TE_OK)
+        st = make_map_2d(&p.tw[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, q.it[0].w2, (uint64_t)q.k, (uint64_t)q.it[0].n,
+                         (uint64_t)q.k, 128, F, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != TE_OK) return st;
+    p.xs = q.xs;
+    p.m = q.m;
+    p.k = q.k;
+    p.z = q.z;
+    if ((st = gemm_error_word(&p.err)) != TE_OK) return st;
+    const int ttiles = (q.m + N - 1) / N;
+    int S = 1;
+    mid_split(tiles * ttiles, (q.k + 127) / 128, SMS * Mid<N>::CTAS, S);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles * S, ttiles, 1);
+    cfg.blockDim = dim3(Mid<N>::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = S;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, i8_mid_kernel<N, GATED>, p);
+    return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
+}
+template <bool GATED>
+te_status mid(const I8Params &p, cudaStream_t s) {
+    if (p.m <= 16) return mid_launch<16, GATED>(p, s);
+    if (p.m <= 32) return mid_launch<32, GATED>(p, s);
+    return p.m <= 64 ? mid_launch<64, GATED>(p, s) : mid_launch<128, GATED>(p, s);
+}
+
 // x int8 [m, k] (rows ldx apart) widened to f16 [m, k], exactly: 16 values a
-// thread, 16 bytes in and 32 out.  q + 128 as the low byte of the f16 pattern
-// 0x64xx reads 1024 + q + 128; subtracting 1152 leaves q.
+// thread, 16 bytes in and 32 out.
 __global__ void __launch_bounds__(256) widen_kernel(const int8_t *__restrict__ x, long long ldx,
                                                     __half *__restrict__ y, long long total, int chunks) {
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -99,18 +574,11 @@ __global__ void __launch_bounds__(256) widen_kernel(const int8_t *__restrict__ x
     const long long r = i / chunks;
     const int c = (int)(i - r * chunks);
     const uint4 v = *reinterpret_cast<const uint4 *>(x + r * ldx + 16 * c);
-    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
     uint32_t out[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t u = in[j] ^ 0x80808080u;
-        const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
-        out[2 * j] = *reinterpret_cast<const uint32_t *>(&l);
-        out[2 * j + 1] = *reinterpret_cast<const uint32_t *>(&h);
-    }
+    widen4(v.x, out[0], out[1]);
+    widen4(v.y, out[2], out[3]);
+    widen4(v.z, out[4], out[5]);
+    widen4(v.w, out[6], out[7]);
     uint4 *dst = reinterpret_cast<uint4 *>(y + 16 * i);
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
     dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
@@ -125,8 +593,45 @@ te_status widen(const int8_t *x, int64_t ldx, void *y, int m, int k, cudaStream_
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear: widen launch");
 }
 
-constexpr int SMALL_M = 8;
 constexpr int MAX_K = 65536;
+
+// Which kernel takes a call.  The measured device times (us, back to back in a
+// graph, weights not in L2; n the output features in all):
+//                      small    mid   large (with its widening pass)
+//   m = 8   k 3840 n 11520     10.5   14.5
+//   m = 16  k 512  n 1536       2.9    4.6    7.9
+//   m = 16  k 3840 n 3840       7.7    9.2   18.2
+//   m = 16  k 10240 n 3840     15.6   12.7   35.9
+//   m = 32  k 768  n 2304       4.6    5.6    8.8
+//   m = 32  k 3840 n 3840      11.3   10.2   18.4
+//   m = 64  k 3840 n 11520            23.9   19.6
+//   m = 128 k 3840 n 3840             14.7   19.7
+//   m = 128 k 10240 n 3840            22.2   38.5
+//   m = 384 k 3840 n 11520            54.5   32.7
+// Small: to 8 tokens; to 16 (32) tokens while the weights are under 16 M (4 M)
+// values, beyond which its warps' widening of the tokens costs more than the
+// TMEM pipeline's start.  Between mid and large, by their stage counts: mid
+// 5.5 us and 0.62 us a stage (0.8 at 128 tokens a tile), large 7 us (the
+// widening pass and a second launch) and 0.39 us a stage of each wave of
+// 256 x 128 units; both fit what was measured to about 15 %.
+enum Path { SMALL, MID, LARGE };
+Path path_of(int m, int k, const int *n, int z, bool gated) {
+    long long total = 0;
+    int tiles = 0;                              // 128 weight rows (gated: 64 gate and 64 up)
+    for (int i = 0; i < z; ++i) {
+        total += n[i];
+        tiles += gated ? (n[i] + 63) / 64 : (n[i] + 127) / 128;
+    }
+    if (gated) total *= 2;
+    if (m <= 8 || (m <= 16 && total * k <= (16 << 20)) || (m <= 32 && total * k <= (4 << 20))) return SMALL;
+    if (m <= 32) return MID;
+    if (m > 1024) return LARGE;
+    const int nkb = (k + 127) / 128, N = m <= 64 ? 64 : 128;
+    int split = 1;
+    const double mid_us = 5.5 + (N == 64 ? 0.62 : 0.8) * mid_split(tiles * ((m + N - 1) / N), nkb, SMS, split);
+    const int units = (tiles + 1) / 2 * ((m + 127) / 128), waves = (units + SMS / 2 - 1) / (SMS / 2);
+    return mid_us < 7.0 + 0.39 * nkb * waves ? MID : LARGE;
+}
 
 te_status check_x(const char *what, const void *x, int64_t ldx, const float *xs, int32_t m, int32_t k) {
     if (!x || !xs) return fail(TE_EINVAL, "%s: NULL x or x_scale", what);
@@ -157,18 +662,13 @@ te_status check_ws(const char *what, const void *ws, size_t have, size_t need) {
     return TE_OK;
 }
 
-te_status launched(const char *what) {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? TE_OK : cuda_fail(e, what);
-}
-
 }  // namespace
 }  // namespace tefwd
 
 using namespace tefwd;
 
 extern "C" size_t te_i8_workspace(int32_t m, int32_t k, int32_t n) {
-    if (m <= SMALL_M || k < 64 || k > MAX_K || k % 64 || n < 32) return 0;
+    if (m <= 8 || k < 64 || k > MAX_K || k % 64 || n < 32) return 0;
     return ((size_t)m * k * 2 + 255) & ~(size_t)255;
 }
 
@@ -187,7 +687,6 @@ extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_s
     p.m = m;
     p.k = k;
     p.z = z;
-    int tiles = 0;
     int64_t n = 0;
     for (int i = 0; i < z; ++i) {
         const te_q8_item &src = items[i];
@@ -219,20 +718,22 @@ extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_s
         d.n = src.w.n;
         d.ydt = src.y_dtype;
         d.act = src.epilogue;
-        d.tile0 = tiles;
-        tiles += (src.w.n + 63) / 64;
         n += src.w.n;
     }
     if (n > 0x7FFFFFFFll) return fail(TE_ESHAPE, "i8_linear: too many output features");
     if ((st = check_ws("i8_linear", workspace, ws_bytes, te_i8_workspace(m, k, (int32_t)n))) != TE_OK) return st;
     if (m == 0) return TE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (m > SMALL_M) {
+    int ns[MAXZ];
+    for (int i = 0; i < z; ++i) ns[i] = p.it[i].n;
+    const Path path = path_of(m, k, ns, z, false);
+    if (path == MID) return mid<false>(p, s);
+    if (path == LARGE) {
         if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
         return i8_gemm_linear(workspace, x_scale, m, k, items, z, s);
     }
-    i8_tile_kernel<false><<<dim3(tiles, (m + 63) / 64), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return launched("i8_linear launch");
+    if (m <= 8) return small_launch<1, 1, false>(p, s);
+    return m <= 16 ? small_launch<2, 1, false>(p, s) : small_launch<4, 1, false>(p, s);
 }
 
 extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const float *x_scale, int32_t m,
@@ -253,7 +754,8 @@ extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const floa
     if ((st = check_ws("i8_gated_linear", workspace, ws_bytes, te_i8_workspace(m, k, 2 * f))) != TE_OK) return st;
     if (m == 0) return TE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (m > SMALL_M) {
+    const Path path = path_of(m, k, &f, 1, true);
+    if (path == LARGE) {
         if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
         return i8_gemm_gated(workspace, x_scale, m, k, wg, wu, act, out, ldm, s);
     }
@@ -277,6 +779,7 @@ extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const floa
     d.n = f;
     d.ydt = TE_BF16;
     d.act = act;
-    i8_tile_kernel<true><<<dim3((f + 63) / 64, (m + 63) / 64), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return launched("i8_gated_linear launch");
+    if (path == MID) return mid<true>(p, s);
+    if (m <= 8) return small_launch<1, 2, true>(p, s);
+    return m <= 16 ? small_launch<2, 2, true>(p, s) : small_launch<4, 2, true>(p, s);
 }

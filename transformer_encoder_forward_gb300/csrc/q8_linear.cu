@@ -1679,6 +1679,11 @@ te_status i8_gemm_gated(const void *xh, const float *ts, int32_t m, int32_t k, c
     return gated_parts<true>(p, xh, k, wg->q, wu->q, out, ldm, s);
 }
 
+te_status gemm_error_word(int **word) {
+    const cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_gemm_err);
+    return e == cudaSuccess ? TE_OK : cuda_fail(e, "gemm error word");
+}
+
 int read_clear_gemm_error() {
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_gemm_err, sizeof(int)) != cudaSuccess) return -1;
