@@ -1,6 +1,7 @@
 """Python binding of libtefwd (the C-ABI in include/tefwd.h).
 
-Argument marshalling only: every step of the forward pass runs in the CUDA
+Argument marshalling only (ctypes; csrc/marshal.cpp for the calls of a few
+microseconds): every step of the forward pass runs in the CUDA
 kernels of libtefwd.so.  PyTorch supplies device memory and the current CUDA
 stream.  There is no CPU or library fallback: if the shared library is
 missing or fails to load, every call raises.
@@ -9,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional, Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -49,10 +49,6 @@ class te_q8w(ctypes.Structure):
 class te_q8_item(ctypes.Structure):
     _fields_ = [("w", te_q8w), ("y", c_p), ("ldy", c_i64), ("y_dtype", c_i32),
                 ("epilogue", c_i32), ("residual", c_p), ("ldr", c_i64)]
-
-
-# the fields of te_q8_item after w, as i8_linear packs them
-_ITEM_TAIL = struct.Struct("@qqiiqq")
 
 
 class te_block_desc(ctypes.Structure):
@@ -112,8 +108,8 @@ EXPORTS = {
     "te_quant_rows": (ctypes.c_int, [c_p, c_i32, c_i64, c_p, c_i64, c_p, c_i32, c_i32, c_p]),
     "te_rownorm_quant": (ctypes.c_int, [c_p, c_i32, c_i64, c_p, c_p, c_p, c_i32, c_f32, c_f32, c_p,
                                         c_i64, c_p, c_i32, c_i32, c_p]),
-    "te_i8_linear": (ctypes.c_int, [c_p, c_i64, c_p, c_i32, c_i32, c_p, c_i32, c_p, ctypes.c_size_t,
-                                    c_p]),
+    "te_i8_linear": (ctypes.c_int, [c_p, c_i64, c_p, c_i32, c_i32, ctypes.POINTER(te_q8_item), c_i32,
+                                    c_p, ctypes.c_size_t, c_p]),
     "te_i8_gated_linear": (ctypes.c_int, [c_p, c_i64, c_p, c_i32, c_i32, ctypes.POINTER(te_q8w),
                                           ctypes.POINTER(te_q8w), c_i32, c_p, c_i64, c_p,
                                           ctypes.c_size_t, c_p]),
@@ -334,75 +330,32 @@ def pool_mean(x, cu_host, cu_dev, w_final, eps, out, stream=None):
 
 # --------------------------------------------------- activations in 8 bits
 
-_T = None
+_m = None
 
 
-def _types():
-    """torch, its current device and the dtype groups the operators below take
-    (f32, f32 or bf16, int8, int32)."""
-    global _T
-    if _T is None:
-        import torch
-        _T = (torch, (torch.float32,), (torch.float32, torch.bfloat16), (torch.int8,), (torch.int32,))
-    return (_T[0].cuda.current_device(), *_T[1:])
-
-
-def _want(what: str, t, dev: int, dtypes, shape):
-    """Address of a tensor argument of the operators below, once it is seen to
-    lie on the current device with one of `dtypes`, the given shape and a
-    contiguous last axis.  These checks run in every call, so the passing path
-    is one line."""
-    if t.dtype in dtypes and t.get_device() == dev and t.shape == shape and t.stride(-1) == 1:
-        return t.data_ptr()
-    if t.dtype not in dtypes:
-        raise TypeError(f"{what}: dtype {t.dtype}, not one of {dtypes}")
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: a tensor on the current CUDA device, not on {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, not {tuple(shape)}")
-    if shape[-1] > 1:
-        raise ValueError(f"{what}: its last axis must be contiguous")
-    return t.data_ptr()
-
-
-def _opt(what: str, t, dev, dtypes, shape):
-    return None if t is None else _want(what, t, dev, dtypes, shape)
-
-
-def _ld(t) -> int:
-    """Leading dimension of a matrix; a single row's stride says nothing."""
-    return t.stride(0) if t.shape[0] != 1 else max(t.stride(0), -(-t.shape[1] // 16) * 16)
-
-
-def _scratch(what: str, t, dev):
-    """Address and size of a workspace (None: no workspace)."""
-    if t is None:
-        return None, 0
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{what}: the workspace must be a contiguous tensor on the current CUDA device")
-    return t.data_ptr(), t.numel() * t.element_size()
+def _marshalling():
+    """The marshalling module next to libtefwd.so (raises if it has not been built)."""
+    global _m
+    if _m is None:
+        import torch  # noqa: F401  (its libraries first)
+        lib()
+        try:
+            from . import _marshal as mod
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is not built; run "
+                               "python -m transformer_encoder_forward_gb300.build") from e
+        _m = mod
+    return _m
 
 
 def quant_rows(x, q, scale, stream=None):
     """q (int8 [t, d]), scale (f32 [t]) = each row of x (f32 or bf16) in 8 bits."""
-    dev, f32, real, i8, _ = _types()
-    t, d = x.shape
-    _ok(lib().te_quant_rows(_want("quant_rows: x", x, dev, real, (t, d)), _dt(x), _ld(x),
-                            _want("quant_rows: q", q, dev, i8, (t, d)), _ld(q),
-                            _want("quant_rows: scale", scale, dev, f32, (t,)), t, d, _stream(stream)))
+    _ok((_m or _marshalling()).quant_rows(x, q, scale, stream))
 
 
 def rownorm_quant(x, w, b, kind, eps, q, scale, pre=1.0, mod_scale=None, stream=None):
     """quant_rows of Norm(pre x) w (+b), times (1 + mod_scale) when given."""
-    dev, f32, real, i8, _ = _types()
-    t, d = x.shape
-    _ok(lib().te_rownorm_quant(_want("rownorm_quant: x", x, dev, real, (t, d)), _dt(x), _ld(x),
-                               _want("rownorm_quant: w", w, dev, f32, (d,)),
-                               _opt("rownorm_quant: b", b, dev, f32, (d,)),
-                               _opt("rownorm_quant: mod_scale", mod_scale, dev, f32, (d,)), kind, eps, pre,
-                               _want("rownorm_quant: q", q, dev, i8, (t, d)), _ld(q),
-                               _want("rownorm_quant: scale", scale, dev, f32, (t,)), t, d,
-                               _stream(stream)))
+    _ok((_m or _marshalling()).rownorm_quant(x, w, b, kind, eps, q, scale, pre, mod_scale, stream))
 
 
 def i8_workspace(m: int, k: int, n: int) -> int:
@@ -416,34 +369,13 @@ def i8_linear(xq, x_scale, items: Sequence[dict], workspace, stream=None):
     weights; items as q8_linear (y [m, n] with leading dimension ldy).
     workspace: a uint8 device tensor of i8_workspace(m, k, sum of n) bytes, or
     None when that is 0."""
-    dev, f32, real, i8, _ = _types()
-    m, k = xq.shape
-    arr = b""                       # the te_q8_item array, packed
-    for it in items:
-        y, w, r = it["y"], it["w"], it.get("residual")
-        if r is None:
-            rp, ldr = 0, 0
-        else:
-            rp, ldr = _want("i8_linear: residual", r, dev, f32, (m, r.shape[1])), it["ldr"]
-        arr += bytes(w) + _ITEM_TAIL.pack(_want("i8_linear: y", y, dev, real, (m, w.n)), it["ldy"], _dt(y),
-                                          it.get("epilogue", TE_EPI_NONE), rp, ldr)
-    ws, nb = _scratch("i8_linear", workspace, dev)
-    _ok(lib().te_i8_linear(_want("i8_linear: xq", xq, dev, i8, (m, k)), _ld(xq),
-                           _want("i8_linear: x_scale", x_scale, dev, f32, (m,)), m, k, arr, len(items),
-                           ws, nb, _stream(stream)))
+    _ok((_m or _marshalling()).i8_linear(xq, x_scale, items, workspace, stream))
 
 
 def i8_gated_linear(xq, x_scale, wg: te_q8w, wu: te_q8w, act, out, workspace, stream=None):
     """out (bf16) = act(x Wg^T) * (x Wu^T) from int8 tokens, rounded once;
     workspace of i8_workspace(m, k, 2 f) bytes."""
-    dev, f32, _, i8, _ = _types()
-    m, k = xq.shape
-    ws, nb = _scratch("i8_gated_linear", workspace, dev)
-    _ok(lib().te_i8_gated_linear(_want("i8_gated_linear: xq", xq, dev, i8, (m, k)), _ld(xq),
-                                 _want("i8_gated_linear: x_scale", x_scale, dev, f32, (m,)), m, k,
-                                 ctypes.byref(wg), ctypes.byref(wu), act,
-                                 _want("i8_gated_linear: out", out, dev, (_T[0].bfloat16,), (m, wg.n)),
-                                 _ld(out), ws, nb, _stream(stream)))
+    _ok((_m or _marshalling()).i8_gated_linear(xq, x_scale, wg, wu, act, out, workspace, stream))
 
 
 # ---------------------------------------- rotary positions with several axes
@@ -469,16 +401,8 @@ def qk_rope_axes(src, ld_src, dst, ld_dst, q_off, k_off, nq, nkv, hd, qn, kn, ep
                  plan: te_rope_axes, pos, q_mul, rows, stream=None):
     """q/k norm + rotation of the q and k heads of src into the same columns of
     dst (dst may be src); pos int32 [rows, axes] on the device."""
-    dev, f32, real, _, i32 = _types()
-    if src.dtype != dst.dtype:
-        raise TypeError(f"qk_rope_axes: src is {src.dtype}, dst {dst.dtype}")
-    _ok(lib().te_qk_rope_axes(_want("qk_rope_axes: src", src, dev, real, (rows, src.shape[-1])), ld_src,
-                              _want("qk_rope_axes: dst", dst, dev, real, (rows, dst.shape[-1])), ld_dst,
-                              _dt(src), q_off, k_off, nq, nkv, hd,
-                              _opt("qk_rope_axes: qn", qn, dev, f32, (hd,)),
-                              _opt("qk_rope_axes: kn", kn, dev, f32, (hd,)), eps, ctypes.byref(plan),
-                              _want("qk_rope_axes: pos", pos, dev, i32, (rows, plan.axes)), _ld(pos),
-                              q_mul, rows, _stream(stream)))
+    _ok((_m or _marshalling()).qk_rope_axes(src, ld_src, dst, ld_dst, q_off, k_off, nq, nkv, hd, qn, kn, eps,
+                                        plan, pos, q_mul, rows, stream))
 
 
 def block_workspace(desc: te_block_desc, t: int) -> int:

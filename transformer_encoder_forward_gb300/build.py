@@ -1,8 +1,11 @@
-"""Builds libtefwd.so in the package directory with nvcc for sm_103a.
+"""Builds libtefwd.so in the package directory with nvcc for sm_103a, and the
+binding's marshalling module next to it.
 
 Each CUDA translation unit compiles in parallel to an object under _build/,
 then one nvcc link produces the shared library (CUDA runtime linked
-statically).  Run ``python -m transformer_encoder_forward_gb300.build``.
+statically).  The marshalling module (csrc/marshal.cpp: a CPython extension
+over PyTorch's headers) compiles beside them and links against it.  Run
+``python -m transformer_encoder_forward_gb300.build``.
 """
 from __future__ import annotations
 
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtefwd.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 SOURCES = ["rowops.cu", "q8_linear.cu", "attn.cu", "block.cu", "block_static.cu", "codecs.cu",
            "quant.cu", "i8_linear.cu", "rope_axes.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -30,6 +34,23 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def _marshal_flags():
+    """Compile and link flags of the marshalling module (PyTorch's and Python's)."""
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    comp = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+            "-isystem", os.path.join(root, "include"),
+            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"]]
+    libs = os.path.join(root, "lib")
+    link = ["-L", PKG, "-ltefwd", "-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    return comp, link
 
 
 def _stale(out: str, deps) -> bool:
@@ -52,21 +73,30 @@ def build(verbose: bool = False, force: bool = False, extra=()) -> str:
         objs.append(o)
         if force or _stale(o, [s, *headers]):
             jobs.append([cc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o])
+    cuda_jobs = len(jobs)
+    comp, link = _marshal_flags()
+    cxx = os.environ.get("CXX") or "g++"
+    m_src, m_obj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.o")
+    if force or _stale(m_obj, [m_src, os.path.join(INCLUDE, "tefwd.h")]):
+        jobs.append([cxx, *comp, "-c", m_src, "-o", m_obj])
 
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, flush=True)
 
     with cf.ThreadPoolExecutor(max_workers=len(jobs) or 1) as ex:
         list(ex.map(run, jobs))
-    if force or jobs or _stale(LIB, objs):
-        run([cc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs])
+    if force or cuda_jobs or _stale(LIB, objs):
+        run([cc, *ARCH, "-shared", "-Xlinker", "-soname=libtefwd.so", "-o", LIB + ".tmp", *objs])
         os.replace(LIB + ".tmp", LIB)
+    if force or _stale(MARSHAL, [m_obj]):
+        run([cxx, "-shared", "-o", MARSHAL + ".tmp", m_obj, *link])
+        os.replace(MARSHAL + ".tmp", MARSHAL)
     return LIB
 
 
