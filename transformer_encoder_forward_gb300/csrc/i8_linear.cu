@@ -420,16 +420,18 @@ __global__ void __launch_bounds__(Mid<N>::THREADS) i8_mid_kernel(const __grid_co
         int d = h * (N / 2) / TC, tl = h * (N / 2) - d * TC;    // owner and place of the next token
         const uint32_t mine = sb + (uint32_t)(((int)rank * TC * 128 + 32 * q + lane) * 4);
         uint32_t to = mapa_shared(mine, d < S ? d : 0);
+        constexpr int LD = N >= 64 ? 4 : N / 16;    // TMEM loads in flight, 8 columns each
 #pragma unroll
-        for (int c8 = 0; c8 < N / 16; ++c8) {
-            const int c = h * (N / 2) + 8 * c8;
-            if (c >= tn) break;                 // warp-uniform
-            uint32_t v[8];
-            tmem_ld8(tbase + ((uint32_t)(32 * q) << 16) + c, v);
+        for (int c8 = 0; c8 < N / 16; c8 += LD) {
+            const int c0 = h * (N / 2) + 8 * c8;
+            if (c0 >= tn) break;                // warp-uniform
+            uint32_t v[LD][8];
+#pragma unroll
+            for (int i = 0; i < LD; ++i) tmem_ld8(tbase + ((uint32_t)(32 * q) << 16) + c0 + 8 * i, v[i]);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (c + j < tn) st_cluster_f32(to + 512 * tl, __uint_as_float(v[j]));
+            for (int j = 0; j < 8 * LD; ++j) {
+                if (c0 + j < tn) st_cluster_f32(to + 512 * tl, __uint_as_float(v[j / 8][j % 8]));
                 if (++tl == TC) {
                     tl = 0;
                     to = mapa_shared(mine, ++d < S ? d : 0);
@@ -493,32 +495,83 @@ __global__ void __launch_bounds__(Mid<N>::THREADS) i8_mid_kernel(const __grid_co
     }
 }
 
-// The split of k: the least of whole waves of CTAs times a CTA's stages, with
-// four stages' time for a CTA's start and end.  Returns the time in stages.
-double mid_split(int tiles, int nkb, int slots, int &split) {
-    double best = 1e30;
+// A choice of token tile and split of k, and its time by the model below.
+struct MidPlan {
+    int n, split;
+    double us;
+};
+
+// Device time of the mid kernel, fitted to single calls on cold weights: a
+// wave of CTAs costs `start` us and `stage` us a stage of 128 k.  Splitting k
+// shortens the stages of a CTA while the clusters still fit the device at once;
+// clusters of `split` CTAs sit inside a GPC, so fewer CTAs are resident at
+// larger splits (residents: asked of the runtime).
+template <int N>
+void mid_consider(MidPlan &best, int ftiles, int m, int nkb, const int *residents) {
+    constexpr double start = N <= 16 ? 4.2 : (N <= 32 ? 4.6 : (N <= 64 ? 5.5 : 6.5));
+    constexpr double stage = N <= 16 ? 0.5 : (N <= 32 ? 0.55 : (N <= 64 ? 0.65 : 0.8));
+    const long long tiles = (long long)ftiles * ((m + N - 1) / N);
     for (int s = 1; s <= 8 && s <= nkb; s *= 2) {
-        const int waves = (int)(((long long)tiles * s + slots - 1) / slots), stages = (nkb + s - 1) / s;
-        if ((double)waves * (stages + 4) < best - 1e-9) {
-            best = (double)waves * (stages + 4);
-            split = s;
-        }
+        const int r = residents[s] > 0 ? residents[s] : 1;
+        const double us = (double)((tiles + r - 1) / r) * (start + stage * ((nkb + s - 1) / s));
+        if (us < best.us) best = {N, s, us};
     }
-    return best - 4;
 }
 
+// Resident clusters of 1, 2, 4 and 8 CTAs of the kernel on the current device,
+// asked for once (and its shared memory size set).
 template <int N, bool GATED>
-te_status mid_launch(const I8Params &q, cudaStream_t s) {
-    constexpr int F = GATED ? 64 : 128, smem = Mid<N>::BYTES + 1024;
-    static bool ready[64] = {};
+te_status mid_residents(const int *&out) {
+    static int table[64][9] = {};
+    constexpr int smem = Mid<N>::BYTES + 1024;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cuda_fail(e, "i8_linear: device");
-    if (!ready[dev]) {
+    int *t = table[dev];
+    if (!t[1]) {
         e = cudaFuncSetAttribute(i8_mid_kernel<N, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return cuda_fail(e, "i8_linear: set shared memory size");
-        ready[dev] = true;
+        for (int s = 8; s >= 1; s /= 2) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(8 * SMS, 1, 1);
+            cfg.blockDim = dim3(Mid<N>::THREADS, 1, 1);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = s;
+            attr.val.clusterDim.y = 1;
+            attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, i8_mid_kernel<N, GATED>, &cfg);
+            if (e != cudaSuccess || n < 1) return cuda_fail(e, "i8_linear: cluster occupancy");
+            t[s] = n;
+        }
     }
+    out = t;
+    return TE_OK;
+}
+
+template <bool GATED>
+te_status mid_plan(MidPlan &best, int ftiles, int m, int k) {
+    const int nkb = (k + 127) / 128;
+    const int *r16, *r32, *r64, *r128;
+    te_status st;
+    if ((st = mid_residents<16, GATED>(r16)) != TE_OK || (st = mid_residents<32, GATED>(r32)) != TE_OK ||
+        (st = mid_residents<64, GATED>(r64)) != TE_OK || (st = mid_residents<128, GATED>(r128)) != TE_OK)
+        return st;
+    best = {0, 1, 1e30};
+    mid_consider<16>(best, ftiles, m, nkb, r16);
+    mid_consider<32>(best, ftiles, m, nkb, r32);
+    mid_consider<64>(best, ftiles, m, nkb, r64);
+    mid_consider<128>(best, ftiles, m, nkb, r128);
+    return TE_OK;
+}
+
+template <int N, bool GATED>
+te_status mid_launch(const I8Params &q, int S, cudaStream_t s) {
+    constexpr int F = GATED ? 64 : 128, smem = Mid<N>::BYTES + 1024;
     MidParams p;
     memset(&p, 0, sizeof(p));
     te_status st = make_map_2d(&p.tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x, (uint64_t)q.k, (uint64_t)q.m, (uint64_t)q.ldx,
@@ -541,8 +594,6 @@ te_status mid_launch(const I8Params &q, cudaStream_t s) {
     p.z = q.z;
     if ((st = gemm_error_word(&p.err)) != TE_OK) return st;
     const int ttiles = (q.m + N - 1) / N;
-    int S = 1;
-    mid_split(tiles * ttiles, (q.k + 127) / 128, SMS * Mid<N>::CTAS, S);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles * S, ttiles, 1);
     cfg.blockDim = dim3(Mid<N>::THREADS, 1, 1);
@@ -555,14 +606,14 @@ te_status mid_launch(const I8Params &q, cudaStream_t s) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, i8_mid_kernel<N, GATED>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, i8_mid_kernel<N, GATED>, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
 }
 template <bool GATED>
-te_status mid(const I8Params &p, cudaStream_t s) {
-    if (p.m <= 16) return mid_launch<16, GATED>(p, s);
-    if (p.m <= 32) return mid_launch<32, GATED>(p, s);
-    return p.m <= 64 ? mid_launch<64, GATED>(p, s) : mid_launch<128, GATED>(p, s);
+te_status mid(const I8Params &p, const MidPlan &plan, cudaStream_t s) {
+    if (plan.n == 16) return mid_launch<16, GATED>(p, plan.split, s);
+    if (plan.n == 32) return mid_launch<32, GATED>(p, plan.split, s);
+    return plan.n == 64 ? mid_launch<64, GATED>(p, plan.split, s) : mid_launch<128, GATED>(p, plan.split, s);
 }
 
 // x int8 [m, k] (rows ldx apart) widened to f16 [m, k], exactly: 16 values a
@@ -610,29 +661,29 @@ constexpr int MAX_K = 65536;
 //   m = 384 k 3840 n 11520            54.5   32.7
 // Small: to 8 tokens; to 16 (32) tokens while the weights are under 16 M (4 M)
 // values, beyond which its warps' widening of the tokens costs more than the
-// TMEM pipeline's start.  Between mid and large, by their stage counts: mid
-// 5.5 us and 0.62 us a stage (0.8 at 128 tokens a tile), large 7 us (the
-// widening pass and a second launch) and 0.39 us a stage of each wave of
-// 256 x 128 units; both fit what was measured to about 15 %.
+// TMEM pipeline's start.  Between mid and large, by their modelled times: mid
+// as above; large 7 us (the widening pass and a second launch) and 0.39 us a
+// stage of each wave of 256 x 128 units (both fit the measured to about 15 %).
 enum Path { SMALL, MID, LARGE };
-Path path_of(int m, int k, const int *n, int z, bool gated) {
+template <bool GATED>
+te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
     long long total = 0;
     int tiles = 0;                              // 128 weight rows (gated: 64 gate and 64 up)
-    for (int i = 0; i < z; ++i) {
-        total += n[i];
-        tiles += gated ? (n[i] + 63) / 64 : (n[i] + 127) / 128;
+    for (int i = 0; i < p.z; ++i) {
+        total += GATED ? 2 * p.it[i].n : p.it[i].n;
+        tiles += GATED ? (p.it[i].n + 63) / 64 : (p.it[i].n + 127) / 128;
     }
-    if (gated) total *= 2;
-    if (m <= 8 || (m <= 16 && total * k <= (16 << 20)) || (m <= 32 && total * k <= (4 << 20))) return SMALL;
-    if (m <= 32) return MID;
-    if (m > 1024) return LARGE;
-    const int nkb = (k + 127) / 128, N = m <= 64 ? 64 : 128;
-    int split = 1;
-    const double mid_us = 5.5 + (N == 64 ? 0.62 : 0.8) * mid_split(tiles * ((m + N - 1) / N), nkb, SMS, split);
-    const int units = (tiles + 1) / 2 * ((m + 127) / 128), waves = (units + SMS / 2 - 1) / (SMS / 2);
-    return mid_us < 7.0 + 0.39 * nkb * waves ? MID : LARGE;
+    path = SMALL;
+    if (p.m <= 8 || (p.m <= 16 && total * p.k <= (16 << 20)) || (p.m <= 32 && total * p.k <= (4 << 20))) return TE_OK;
+    path = LARGE;
+    if (p.m > 1024) return TE_OK;
+    const te_status st = mid_plan<GATED>(plan, tiles, p.m, p.k);
+    if (st != TE_OK) return st;
+    const long long units = (long long)((tiles + 1) / 2) * ((p.m + 127) / 128);
+    const long long waves = (units + SMS / 2 - 1) / (SMS / 2);
+    if (p.m <= 32 || plan.us < 7.0 + 0.39 * ((p.k + 127) / 128) * waves) path = MID;
+    return TE_OK;
 }
-
 te_status check_x(const char *what, const void *x, int64_t ldx, const float *xs, int32_t m, int32_t k) {
     if (!x || !xs) return fail(TE_EINVAL, "%s: NULL x or x_scale", what);
     if (m < 0 || k < 64 || k > MAX_K || k % 64)
@@ -724,10 +775,10 @@ extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_s
     if ((st = check_ws("i8_linear", workspace, ws_bytes, te_i8_workspace(m, k, (int32_t)n))) != TE_OK) return st;
     if (m == 0) return TE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int ns[MAXZ];
-    for (int i = 0; i < z; ++i) ns[i] = p.it[i].n;
-    const Path path = path_of(m, k, ns, z, false);
-    if (path == MID) return mid<false>(p, s);
+    Path path;
+    MidPlan plan;
+    if ((st = path_of<false>(p, path, plan)) != TE_OK) return st;
+    if (path == MID) return mid<false>(p, plan, s);
     if (path == LARGE) {
         if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
         return i8_gemm_linear(workspace, x_scale, m, k, items, z, s);
@@ -754,11 +805,6 @@ extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const floa
     if ((st = check_ws("i8_gated_linear", workspace, ws_bytes, te_i8_workspace(m, k, 2 * f))) != TE_OK) return st;
     if (m == 0) return TE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const Path path = path_of(m, k, &f, 1, true);
-    if (path == LARGE) {
-        if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
-        return i8_gemm_gated(workspace, x_scale, m, k, wg, wu, act, out, ldm, s);
-    }
     I8Params p;
     memset(&p, 0, sizeof(p));
     p.x = x;
@@ -779,7 +825,14 @@ extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const floa
     d.n = f;
     d.ydt = TE_BF16;
     d.act = act;
-    if (path == MID) return mid<true>(p, s);
+    Path path;
+    MidPlan plan;
+    if ((st = path_of<true>(p, path, plan)) != TE_OK) return st;
+    if (path == MID) return mid<true>(p, plan, s);
+    if (path == LARGE) {
+        if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
+        return i8_gemm_gated(workspace, x_scale, m, k, wg, wu, act, out, ldm, s);
+    }
     if (m <= 8) return small_launch<1, 2, true>(p, s);
     return m <= 16 ? small_launch<2, 2, true>(p, s) : small_launch<4, 2, true>(p, s);
 }
