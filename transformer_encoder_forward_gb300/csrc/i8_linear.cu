@@ -616,6 +616,405 @@ te_status mid(const I8Params &p, const MidPlan &plan, cudaStream_t s) {
     return plan.n == 64 ? mid_launch<64, GATED>(p, plan.split, s) : mid_launch<128, GATED>(p, plan.split, s);
 }
 
+// ------------------------------------------------ many tokens, short k (k <= 512)
+//
+// The widened weights of 128 features fit TMEM beside two accumulators, so a
+// CTA keeps them there and lets its run of token tiles pass: per tile it loads
+// the int8 tokens only, widens them into shared memory and drains 128 x 128
+// outputs.  Against the large pipeline with its separate widening pass that
+// saves the pass and its f16 copy of the tokens, which at short k cost as much
+// as the product.
+//   * persistent CTAs, one an SM; units are (128 features, 128 tokens), features
+//     outermost; a CTA takes a contiguous run and reloads its weights where the
+//     run crosses into the next features;
+//   * warp 0: TMA, one ring of 128 x 128-byte chunks for weights and tokens;
+//   * warps 2-9 widen every chunk together, in order: weights into TMEM (two
+//     warps a lane quadrant), tokens into a ring of f16 chunks in the MMA's
+//     128-byte-swizzled layout;
+//   * warp 1: MMAs, kind::f16, M = 128, N = 128, into alternating accumulators;
+//   * warps 10-17 drain the other accumulator: lane = feature, half of the
+//     tokens a warp, scaled in registers, written to a staging block in y's
+//     layout and sent by TMA stores (a reduce-add where y is its own residual),
+//     two blocks in turn.  (Straight from registers a row cost an address and a
+//     predicate as well: 16.6 k warp instructions a tile, twice its MMA time.)
+// Gated: a quadrant holds 16 gate rows and the same features' up rows
+// (gate_block).  Waits are bounded as everywhere.
+struct ResParams {
+    CUtensorMap tx;
+    CUtensorMap tw[MAXZ];
+    CUtensorMap ty[MAXZ];     // y_i: boxes of 32 (gated: 16) features x 32 tokens
+    I8Item it[MAXZ];
+    const float *xs;
+    int *err;
+    int m, k, z, ttiles, units;
+};
+struct Res {
+    static constexpr int NS = 3, NB = 3;
+    static constexpr int CHUNK = 128 * 128;     // int8 chunk
+    static constexpr int BBOX = 128 * 128;      // 64 k of 128 widened tokens
+    static constexpr int B_OFF = NS * CHUNK;
+    static constexpr int TS_OFF = B_OFF + NB * 2 * BBOX;        // 64 token scales a draining warp
+    static constexpr int STG = 8192;            // output blocks of a draining warp: two halves
+    static constexpr int STG_OFF = TS_OFF + 8 * 64 * 4;
+    static constexpr int BAR_OFF = STG_OFF + 8 * STG;
+    static constexpr int NBAR = 2 * NS + 2 * NB + 2 + 4 + 1;
+    static constexpr int BYTES = BAR_OFF + 8 * NBAR + 16;
+    static constexpr int THREADS = 18 * 32;
+    static constexpr int A_COL = 256;           // TMEM: two accumulators of 128 columns, then A
+    static_assert(BYTES + 1024 <= 227 * 1024, "shared memory");
+};
+
+template <bool GATED>
+__global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_constant__ ResParams p) {
+    using L = Res;
+    constexpr int NS = L::NS, NB = L::NB, F = GATED ? 64 : 128;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem);
+    const uint32_t bar_full = sb + L::BAR_OFF, bar_empty = bar_full + 8 * NS, bar_bfull = bar_empty + 8 * NS,
+                   bar_bempty = bar_bfull + 8 * NB, bar_afull = bar_bempty + 8 * NB, bar_aempty = bar_afull + 8,
+                   bar_accfull = bar_aempty + 8, bar_accempty = bar_accfull + 16, bar_done = bar_accempty + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFF + 8 * L::NBAR);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nkb = (p.k + 127) / 128;
+    const int u0 = (int)((long long)p.units * blockIdx.x / gridDim.x);
+    const int u1 = (int)((long long)p.units * (blockIdx.x + 1) / gridDim.x);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 8);
+        }
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(bar_bfull + 8 * i, 8);
+            mbar_init(bar_bempty + 8 * i, 1);
+        }
+        mbar_init(bar_afull, 8);
+        mbar_init(bar_aempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_accfull + 8 * i, 1);
+            mbar_init(bar_accempty + 8 * i, 8);
+        }
+        mbar_init(bar_done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+    bool ok = true;
+    // unit u is (feature tile ft, token tile tt); it brings new weights where a
+    // run or a feature tile begins
+    const int ft0 = u0 / p.ttiles, tt0 = u0 - ft0 * p.ttiles;
+    auto next = [&](int &ft, int &tt) {
+        if (++tt == p.ttiles) {
+            tt = 0;
+            ++ft;
+        }
+    };
+    auto item_of = [&](int ft) {
+        int zi = 0;
+        while (zi + 1 < p.z && ft >= p.it[zi + 1].tile0) ++zi;
+        return zi;
+    };
+
+    if (warp == 0) {
+        const uint32_t e = elect_one();
+        if (e) tma_prefetch_desc(&p.tx);
+        int ci = 0;
+        auto slot = [&]() {                     // the next free chunk of the ring
+            const int s = ci % NS;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_empty + 8 * s, ((ci / NS) & 1) ^ 1));
+            if (ok) mbar_arrive_expect_tx_e(bar_full + 8 * s, L::CHUNK, e);
+            return s;
+        };
+        for (int u = u0, ft = ft0, tt = tt0; u < u1 && ok; ++u, next(ft, tt)) {
+            if (u == u0 || tt == 0) {
+                const int zi = item_of(ft), o0 = (ft - p.it[zi].tile0) * F;
+                for (int kb = 0; kb < nkb; ++kb, ++ci) {
+                    const int s = slot();
+                    if (!ok) break;
+                    if (GATED) {
+                        tma_load_2d_e(sb + s * L::CHUNK, &p.tw[0], bar_full + 8 * s, kb * 128, o0, e);
+                        tma_load_2d_e(sb + s * L::CHUNK + L::CHUNK / 2, &p.tw[1], bar_full + 8 * s, kb * 128, o0, e);
+                    } else {
+                        tma_load_2d_e(sb + s * L::CHUNK, &p.tw[zi], bar_full + 8 * s, kb * 128, o0, e);
+                    }
+                }
+            }
+            for (int kb = 0; kb < nkb && ok; ++kb, ++ci) {
+                const int s = slot();
+                if (ok) tma_load_2d_e(sb + s * L::CHUNK, &p.tx, bar_full + 8 * s, kb * 128, tt * 128, e);
+            }
+        }
+        for (int j = ci - NS < 0 ? 0 : ci - NS; j < ci; ++j)    // no copy of ours lands after the CTA's end
+            mbar_wait(bar_full + 8 * (j % NS), (j / NS) & 1, 20000000ull);
+    } else if (warp == 1) {
+        const uint32_t e = elect_one();
+        constexpr uint32_t idesc = idesc_f16_f32(128, 128);
+        int xi = 0, nfill = 0;
+        for (int u = u0, ft = ft0, tt = tt0; u < u1 && ok; ++u, next(ft, tt)) {
+            const int i = u - u0, b = i & 1;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_accempty + 8 * b, ((i >> 1) & 1) ^ 1));
+            if (ok && (u == u0 || tt == 0)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_afull, nfill++ & 1));
+            for (int kb = 0; kb < nkb && ok; ++kb, ++xi) {
+                const int s = xi % NB;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_bfull + 8 * s, (xi / NB) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t d0 = smem_desc_sw128(sb + L::B_OFF + s * 2 * L::BBOX);
+                const uint32_t a0 = tbase + L::A_COL + 64 * kb;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    mma_ts_bf16_e(tbase + 128 * b, a0 + 8 * j, d0 + (uint64_t)(((j >> 2) * L::BBOX + (j & 3) * 32) >> 4),
+                                  idesc, (uint32_t)(kb != 0 || j != 0), e);
+                mma_commit_e(bar_bempty + 8 * s, e);
+            }
+            if (!ok) break;
+            mma_commit_e(bar_accfull + 8 * b, e);
+            // the last unit on these weights: they may be replaced
+            if (u + 1 < u1 && tt + 1 == p.ttiles) mma_commit_e(bar_aempty, e);
+        }
+        mma_commit_e(bar_done, e);              // every MMA issued above
+        if (!mbar_wait(bar_done, 0, 20000000ull)) ok = false;
+    } else if (warp < 10) {
+        const int q = warp & 3, h = (warp - 2) >> 2;
+        // gated: lanes 0-15 gate rows, 16-31 the same features' up rows
+        const int row = GATED ? (lane & 16 ? 64 : 0) + 16 * q + (lane & 15) : 32 * q + lane;
+        // Tokens: the warp widens 16 of a chunk's, lane l the 16-byte piece c = l % 8
+        // of tokens l / 8 + 4 j.  Piece c becomes pieces 2c, 2c + 1 of 128-byte
+        // rows in the box of its half of k, all swizzled by the row (row + 4 flips
+        // bit 6 of the offset); the halves' lanes store in opposite order, so
+        // that no two hit one bank.
+        const int xr = 16 * (warp - 2) + (lane >> 3), xc = lane & 7, xhi = xc >> 2;
+        const int xrow = xr * 128, xs0 = (xc ^ (xr & 7)) << 4, xbox = xhi * L::BBOX + xr * 128;
+        const int xd0 = ((2 * (xc & 3) + xhi) ^ (xr & 7)) << 4, xd1 = ((2 * (xc & 3) + 1 - xhi) ^ (xr & 7)) << 4;
+        int ci = 0, xi = 0, nfill = 0;
+        for (int u = u0, ft = ft0, tt = tt0; u < u1 && ok; ++u, next(ft, tt)) {
+            if (u == u0 || tt == 0) {
+                // the MMAs on the weights before are complete
+                if (nfill) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_aempty, (nfill - 1) & 1));
+                ++nfill;
+                tc_fence_after();
+                for (int kb = 0; kb < nkb && ok; ++kb, ++ci) {
+                    const int s = ci % NS;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * s, (ci / NS) & 1));
+                    if (!ok) break;
+                    uint32_t r[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(smem + s * L::CHUNK + row * 128 +
+                                                                         (((4 * h + c) ^ (row & 7)) << 4));
+                        widen4(v.x, r[8 * c + 0], r[8 * c + 1]);
+                        widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+                        widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+                        widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    }
+                    tmem_st32(tbase + ((uint32_t)(32 * q) << 16) + L::A_COL + 64 * kb + 32 * h, r);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(bar_afull);
+            }
+            for (int kb = 0; kb < nkb && ok; ++kb, ++ci, ++xi) {
+                const int s = ci % NS, bs = xi % NB;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * s, (ci / NS) & 1) &&
+                                                 mbar_wait(bar_bempty + 8 * bs, ((xi / NB) & 1) ^ 1));
+                if (!ok) break;
+                const uint8_t *src = smem + s * L::CHUNK + xrow;
+                uint8_t *dst = smem + L::B_OFF + bs * 2 * L::BBOX + xbox;
+                uint4 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = *reinterpret_cast<const uint4 *>(src + 512 * j + (xs0 ^ (64 * (j & 1))));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint4 lo, hi;
+                    widen4(v[j].x, lo.x, lo.y);
+                    widen4(v[j].y, lo.z, lo.w);
+                    widen4(v[j].z, hi.x, hi.y);
+                    widen4(v[j].w, hi.z, hi.w);
+                    *reinterpret_cast<uint4 *>(dst + 512 * j + (xd0 ^ (64 * (j & 1)))) = xhi ? hi : lo;
+                    *reinterpret_cast<uint4 *>(dst + 512 * j + (xd1 ^ (64 * (j & 1)))) = xhi ? lo : hi;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar_bfull + 8 * bs);
+                    mbar_arrive(bar_empty + 8 * s);
+                }
+            }
+        }
+    } else {
+        const int q = warp & 3, h = (warp - 10) >> 2;
+        const bool upper = GATED && (lane & 16);
+        float *tsw = reinterpret_cast<float *>(smem + L::TS_OFF) + (warp - 10) * 64;
+        uint8_t *stg = smem + L::STG_OFF + (warp - 10) * L::STG;
+        int turn = 0;                           // blocks so far: two halves in turn
+        // the half's last stores (a group two back) have read it
+        auto block = [&]() {
+            if (lane == 0) bulk_wait_read_n<1>();
+            __syncwarp();
+            return stg + (turn++ & 1) * (L::STG / 2);
+        };
+        // a unit's per-feature and per-token factors, loaded a unit ahead
+        struct Factors {
+            float sc, bi, ts0, ts1;
+        };
+        auto factors = [&](int ft, int tt) {
+            const I8Item &it = p.it[item_of(ft)];
+            const int fo = (ft - it.tile0) * F + (GATED ? 16 : 32) * q, o = fo + (GATED ? lane & 15 : lane);
+            const float *scale = upper ? it.scale2 : it.scale, *bias = upper ? it.bias2 : it.bias;
+            const int t = tt * 128 + 64 * h + lane;
+            Factors f;
+            f.sc = fo < it.n ? scale[o] : 0.f;
+            f.bi = fo < it.n && bias ? bias[o] : 0.f;
+            f.ts0 = t < p.m ? p.xs[t] : 0.f;
+            f.ts1 = t + 32 < p.m ? p.xs[t + 32] : 0.f;
+            return f;
+        };
+        Factors nf = factors(ft0, tt0);
+        for (int u = u0, ft = ft0, tt = tt0; u < u1 && ok; ++u, next(ft, tt)) {
+            const int i = u - u0, b = i & 1;
+            const int zi = item_of(ft);
+            const I8Item &it = p.it[zi];
+            const int fo = (ft - it.tile0) * F + (GATED ? 16 : 32) * q;     // the warp's features: all below n or none
+            const int t0 = tt * 128 + 64 * h;   // this warp's tokens
+            const bool f32 = it.ydt == TE_F32, inplace = it.resid != nullptr && it.resid == it.y;
+            const float sc = nf.sc, bi = nf.bi;
+            __syncwarp();                       // the last tile's scales have been read
+            tsw[lane] = nf.ts0;
+            tsw[32 + lane] = nf.ts1;
+            __syncwarp();
+            if (u + 1 < u1) {
+                int fn = ft, tn = tt;
+                next(fn, tn);
+                nf = factors(fn, tn);
+            }
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_accfull + 8 * b, (i >> 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const int blocks = fo >= it.n || t0 >= p.m ? 0 : (t0 + 32 >= p.m ? 1 : 2);
+            for (int c = 0; c < 2; ++c) {
+                const int tb = t0 + 32 * c;
+                uint32_t v[32];
+                if (c < blocks) {
+                    tmem_ld32(tbase + ((uint32_t)(32 * q) << 16) + 128 * b + 64 * h + 32 * c, v);
+                    tmem_wait_ld();
+                }
+                if (c == 1) {                   // read: the accumulator may take the next tile but one
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_accempty + 8 * b);
+                }
+                if (c >= blocks) continue;
+                uint8_t *st = nullptr;
+                if constexpr (GATED) {
+                    float y[16];
+                    if (it.act == TE_ACT_GELU_TANH)
+                        gate_block<true, TE_ACT_GELU_TANH>(v, sc, bi, tsw + 32 * c, upper, y);
+                    else
+                        gate_block<true, TE_ACT_SILU>(v, sc, bi, tsw + 32 * c, upper, y);
+                    st = block();
+                    uint16_t *sh = reinterpret_cast<uint16_t *>(st) + (upper ? 256 : 0) + (lane & 15);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sh[j * 16] = __bfloat16_as_ushort(__float2bfloat16_rn(y[j]));
+                } else {
+                    scale_block<true>(v, sc, bi, tsw + 32 * c);
+                    if (it.act) act_block<true>(v, it.act - 1);
+                    if (it.resid && !inplace) {
+                        const float *rp = it.resid + (long long)tb * it.ldr + fo + lane;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (tb + j < p.m) v[j] = __float_as_uint(__uint_as_float(v[j]) + rp[(long long)j * it.ldr]);
+                    }
+                    st = block();
+                    if (f32) {
+                        float *sf = reinterpret_cast<float *>(st) + lane;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sf[j * 32] = __uint_as_float(v[j]);
+                    } else {
+                        uint16_t *sh = reinterpret_cast<uint16_t *>(st) + lane;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const uint32_t w = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                            sh[j * 32] = (uint16_t)w;
+                            sh[(j + 1) * 32] = (uint16_t)(w >> 16);
+                        }
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (inplace) tma_reduce_add_2d(&p.ty[zi], smem_u32(st), fo, tb);
+                    else tma_store_2d(&p.ty[zi], smem_u32(st), fo, tb);
+                    bulk_commit();
+                }
+            }
+        }
+        bulk_wait_all();                        // before the CTA's shared memory goes away
+        __syncwarp();
+    }
+    if (!ok && lane == 0) atomicExch(p.err, 1);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+template <bool GATED>
+te_status res_launch(const I8Params &q, cudaStream_t s) {
+    constexpr int F = GATED ? 64 : 128, smem = Res::BYTES + 1024;
+    static bool ready[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return cuda_fail(e, "i8_linear: device");
+    if (!ready[dev]) {
+        e = cudaFuncSetAttribute(i8_res_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return cuda_fail(e, "i8_linear: set shared memory size");
+        ready[dev] = true;
+    }
+    ResParams p;
+    memset(&p, 0, sizeof(p));
+    te_status st = make_map_2d(&p.tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x, (uint64_t)q.k, (uint64_t)q.m, (uint64_t)q.ldx,
+                               128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    int tiles = 0;
+    for (int i = 0; i < q.z && st == TE_OK; ++i) {
+        p.it[i] = q.it[i];
+        p.it[i].tile0 = tiles;
+        tiles += (q.it[i].n + F - 1) / F;
+        st = make_map_2d(&p.tw[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, q.it[i].w, (uint64_t)q.k, (uint64_t)q.it[i].n,
+                         (uint64_t)q.k, 128, F, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    if (GATED && st == TE_OK)
+        st = make_map_2d(&p.tw[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, q.it[0].w2, (uint64_t)q.k, (uint64_t)q.it[0].n,
+                         (uint64_t)q.k, 128, F, CU_TENSOR_MAP_SWIZZLE_128B);
+    for (int i = 0; i < q.z && st == TE_OK; ++i) {
+        const bool f32 = q.it[i].ydt == TE_F32;
+        st = make_map_2d(&p.ty[i], f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q.it[i].y,
+                         (uint64_t)q.it[i].n, (uint64_t)q.m, (uint64_t)q.it[i].ldy * (f32 ? 4 : 2), GATED ? 16 : 32,
+                         32, CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
+    if (st != TE_OK) return st;
+    if ((st = gemm_error_word(&p.err)) != TE_OK) return st;
+    p.xs = q.xs;
+    p.m = q.m;
+    p.k = q.k;
+    p.z = q.z;
+    p.ttiles = (q.m + 127) / 128;
+    const long long units = (long long)p.ttiles * tiles;
+    if (units > 0x7FFFFFFFll) return fail(TE_ESHAPE, "i8_linear: too many tiles");
+    p.units = (int)units;
+    i8_res_kernel<GATED><<<p.units < SMS ? p.units : SMS, Res::THREADS, smem, s>>>(p);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
+}
+
 // x int8 [m, k] (rows ldx apart) widened to f16 [m, k], exactly: 16 values a
 // thread, 16 bytes in and 32 out.
 __global__ void __launch_bounds__(256) widen_kernel(const int8_t *__restrict__ x, long long ldx,
@@ -664,7 +1063,7 @@ constexpr int MAX_K = 65536;
 // TMEM pipeline's start.  Between mid and large, by their modelled times: mid
 // as above; large 7 us (the widening pass and a second launch) and 0.39 us a
 // stage of each wave of 256 x 128 units (both fit the measured to about 15 %).
-enum Path { SMALL, MID, LARGE };
+enum Path { SMALL, MID, RES, LARGE };
 template <bool GATED>
 te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
     long long total = 0;
@@ -675,7 +1074,7 @@ te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
     }
     path = SMALL;
     if (p.m <= 8 || (p.m <= 16 && total * p.k <= (16 << 20)) || (p.m <= 32 && total * p.k <= (4 << 20))) return TE_OK;
-    path = LARGE;
+    path = p.k <= 512 ? RES : LARGE;
     if (p.m > 1024) return TE_OK;
     const te_status st = mid_plan<GATED>(plan, tiles, p.m, p.k);
     if (st != TE_OK) return st;
@@ -779,6 +1178,7 @@ extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_s
     MidPlan plan;
     if ((st = path_of<false>(p, path, plan)) != TE_OK) return st;
     if (path == MID) return mid<false>(p, plan, s);
+    if (path == RES) return res_launch<false>(p, s);
     if (path == LARGE) {
         if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
         return i8_gemm_linear(workspace, x_scale, m, k, items, z, s);
@@ -829,6 +1229,7 @@ extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const floa
     MidPlan plan;
     if ((st = path_of<true>(p, path, plan)) != TE_OK) return st;
     if (path == MID) return mid<true>(p, plan, s);
+    if (path == RES) return res_launch<true>(p, s);
     if (path == LARGE) {
         if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
         return i8_gemm_gated(workspace, x_scale, m, k, wg, wu, act, out, ldm, s);

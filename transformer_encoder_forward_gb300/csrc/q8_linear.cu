@@ -303,106 +303,6 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
                  : "memory");
 }
 
-// One 32-token block of the gated form, in a draining warp whose lanes 0-15
-// hold the gate rows and 16-31 the up rows of its 16 features: v becomes the
-// outputs yv, lane l's for tokens 0-15 of feature l and lane l + 16's for
-// tokens 16-31.  Scale and bias, then gate lane l and up lane l + 16 swap half
-// their tokens, then m = act(g) * u, in f32 pairs.  bf16 activations: both
-// halves are rounded to bf16 before the gate, as a stored g|u panel would be,
-// and the activation takes the hardware tanh (error below that rounding).
-// 8-bit activations (ts: the block's 32 token scales in shared memory): g and
-// u stay f32 and the activation is exact to f32 rounding, so that the output
-// is rounded once.
-template <bool I8, int ACT>
-__device__ __forceinline__ void gate_block(const uint32_t (&v)[32], float sc, float bi, const float *ts, bool upper,
-                                           float (&yv)[16]) {
-    const uint64_t sc2 = f2_pack(sc, sc), bi2 = f2_pack(bi, bi), half2 = f2_pack(0.5f, 0.5f);
-    float gv[16], uv[16];
-    float4 ta, tb;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        uint64_t v2 = f2_pack(__uint_as_float(v[j]), __uint_as_float(v[16 + j]));
-        if constexpr (I8) {
-            if ((j & 3) == 0) {
-                ta = *reinterpret_cast<const float4 *>(ts + j);
-                tb = *reinterpret_cast<const float4 *>(ts + 16 + j);
-            }
-            const float t0 = (j & 3) == 0 ? ta.x : ((j & 3) == 1 ? ta.y : ((j & 3) == 2 ? ta.z : ta.w));
-            const float t1 = (j & 3) == 0 ? tb.x : ((j & 3) == 1 ? tb.y : ((j & 3) == 2 ? tb.z : tb.w));
-            v2 = f2_mul(v2, f2_pack(t0, t1));
-        }
-        float lo, hi;
-        f2_unpack(f2_fma(v2, sc2, bi2), lo, hi);
-        if constexpr (!I8) {
-            const uint32_t b2 = pack_bf16x2(lo, hi);
-            lo = bf16_lo(b2);
-            hi = bf16_hi(b2);
-        }
-        // the gate lane sends its token 16 + j, the up lane its token j
-        const float got = __shfl_xor_sync(0xFFFFFFFFu, upper ? lo : hi, 16);
-        // operands selected first: one activation per lane, no branch
-        gv[j] = upper ? got : lo;
-        uv[j] = upper ? hi : got;
-    }
-#pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-        if constexpr (I8) {
-            yv[j] = apply_act(gv[j], ACT) * uv[j];
-            yv[j + 1] = apply_act(gv[j + 1], ACT) * uv[j + 1];
-        } else {
-            const uint64_t g2 = f2_pack(gv[j], gv[j + 1]);
-            // GELU-tanh: z = g (0.79788456 + 0.035677408 g^2); SiLU: z = g / 2
-            uint64_t z2;
-            if constexpr (ACT == TE_ACT_GELU_TANH)
-                z2 = f2_mul(g2, f2_fma(f2_pack(0.035677408f, 0.035677408f), f2_mul(g2, g2),
-                                       f2_pack(0.79788456f, 0.79788456f)));
-            else
-                z2 = f2_mul(half2, g2);
-            float z0, z1;
-            f2_unpack(z2, z0, z1);
-            const uint64_t h2 = f2_mul(half2, g2);
-            const uint64_t a2 = f2_fma(h2, f2_pack(hw_tanh(z0), hw_tanh(z1)), h2);
-            f2_unpack(f2_mul(a2, f2_pack(uv[j], uv[j + 1])), yv[j], yv[j + 1]);
-        }
-    }
-}
-
-// s*acc + b of one 32-token block in place (f32 bits), two tokens an
-// instruction; 8-bit activations: (acc * ts) * s + b with the block's 32 token
-// scales ts in shared memory.
-template <bool I8>
-__device__ __forceinline__ void scale_block(uint32_t (&v)[32], float sc, float bi, const float *ts) {
-    const uint64_t sc2 = f2_pack(sc, sc), bi2 = f2_pack(bi, bi);
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        uint64_t a2 = f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-        uint64_t b2 = f2_pack(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
-        if constexpr (I8) {
-            const float4 t = *reinterpret_cast<const float4 *>(ts + j);
-            a2 = f2_mul(a2, f2_pack(t.x, t.y));
-            b2 = f2_mul(b2, f2_pack(t.z, t.w));
-        }
-        float y0, y1, y2, y3;
-        f2_unpack(f2_fma(a2, sc2, bi2), y0, y1);
-        f2_unpack(f2_fma(b2, sc2, bi2), y2, y3);
-        v[j] = __float_as_uint(y0);
-        v[j + 1] = __float_as_uint(y1);
-        v[j + 2] = __float_as_uint(y2);
-        v[j + 3] = __float_as_uint(y3);
-    }
-}
-
-// The ungated MLP's activation of one block, act(bf16(y)); 8-bit activations:
-// act(y) of the f32 value.
-template <bool I8>
-__device__ __forceinline__ void act_block(uint32_t (&v)[32], int act) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const float y = __uint_as_float(v[j]);
-        v[j] = __float_as_uint(I8 ? apply_act(y, act) : apply_act_tanh(round_bf16(y), act));
-    }
-}
-
 template <int BN, bool GATED, int TPA, bool I8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     q8_gemm_kernel(const __grid_constant__ Params p) {
