@@ -618,62 +618,67 @@ te_status mid(const I8Params &p, const MidPlan &plan, cudaStream_t s) {
 
 // ------------------------------------------------ many tokens, short k (k <= 512)
 //
-// The widened weights of 128 features fit TMEM beside two accumulators, so a
-// CTA keeps them there and lets its run of token tiles pass: per tile it loads
-// the int8 tokens only, widens them into shared memory and drains 128 x 128
-// outputs.  Against the large pipeline with its separate widening pass that
-// saves the pass and its f16 copy of the tokens, which at short k cost as much
-// as the product.
+// The widened weights of 128 features stay in shared memory (k x 256 bytes)
+// while a CTA's run of token tiles passes: per tile it loads the int8 tokens
+// only, widens them into TMEM and drains 128 x 128 outputs.  Against the large
+// pipeline with its separate widening pass that saves the pass and its f16 copy
+// of the tokens, which at short k cost as much as the product.  Tokens are the
+// MMA's A operand (TMEM) and weights its B (shared memory): shared-memory
+// bandwidth bounds the tile, and what is widened for every tile then costs a
+// load and no store there.  (The other way round, weights in TMEM, a tile at
+// k = 512 moved 512 KB through shared memory and took 5500 cycles.)
 //   * persistent CTAs, one an SM; units are (128 features, 128 tokens), features
 //     outermost; a CTA takes a contiguous run and reloads its weights where the
 //     run crosses into the next features;
 //   * warp 0: TMA, one ring of 128 x 128-byte chunks for weights and tokens;
-//   * warps 2-9 widen every chunk together, in order: weights into TMEM (two
-//     warps a lane quadrant), tokens into a ring of f16 chunks in the MMA's
-//     128-byte-swizzled layout;
+//   * warps 2-9 widen every chunk together, in order: weights into shared memory
+//     in the MMA's 128-byte-swizzled layout, tokens into a ring of TMEM stages
+//     (two warps a lane quadrant);
 //   * warp 1: MMAs, kind::f16, M = 128, N = 128, into alternating accumulators;
-//   * warps 10-17 drain the other accumulator: lane = feature, half of the
-//     tokens a warp, scaled in registers, written to a staging block in y's
-//     layout and sent by TMA stores (a reduce-add where y is its own residual),
-//     two blocks in turn.  (Straight from registers a row cost an address and a
-//     predicate as well: 16.6 k warp instructions a tile, twice its MMA time.)
-// Gated: a quadrant holds 16 gate rows and the same features' up rows
-// (gate_block).  Waits are bounded as everywhere.
+//   * warps 10-17 drain the other accumulator: lane = token, half of the features
+//     a warp, scaled in f32 pairs, written to a staging block in the swizzled
+//     layout of the TMA store that sends it (a reduce-add where y is its own
+//     residual), two blocks in turn.
+// Gated: columns 0-63 are gate features, 64-127 the same features' up rows, so
+// a lane holds both of a pair.  Waits are bounded as everywhere.
 struct ResParams {
     CUtensorMap tx;
     CUtensorMap tw[MAXZ];
-    CUtensorMap ty[MAXZ];     // y_i: boxes of 32 (gated: 16) features x 32 tokens
+    CUtensorMap ty[MAXZ];     // y_i: boxes of 32 features x 32 tokens
     I8Item it[MAXZ];
     const float *xs;
     int *err;
     int m, k, z, ttiles, units;
 };
 struct Res {
-    static constexpr int NS = 3, NB = 3;
+    static constexpr int NS = 3;                // int8 chunks
+    static constexpr int NA = 4;                // TMEM stages of widened tokens
     static constexpr int CHUNK = 128 * 128;     // int8 chunk
-    static constexpr int BBOX = 128 * 128;      // 64 k of 128 widened tokens
+    static constexpr int BBOX = 128 * 128;      // 64 k of 128 widened weight rows
     static constexpr int B_OFF = NS * CHUNK;
-    static constexpr int TS_OFF = B_OFF + NB * 2 * BBOX;        // 64 token scales a draining warp
-    static constexpr int STG = 8192;            // output blocks of a draining warp: two halves
-    static constexpr int STG_OFF = TS_OFF + 8 * 64 * 4;
+    static constexpr int FAC_OFF = B_OFF + 8 * BBOX;            // scale and bias of the tile's 128 columns
+    static constexpr int STG_OFF = FAC_OFF + 2 * 128 * 4;
+    static constexpr int STG = 4096;            // an output block of a draining warp (f32 32 x 32)
     static constexpr int BAR_OFF = STG_OFF + 8 * STG;
-    static constexpr int NBAR = 2 * NS + 2 * NB + 2 + 4 + 1;
+    static constexpr int NBAR = 2 * NS + 2 * NA + 2 + 4 + 2 + 1;
     static constexpr int BYTES = BAR_OFF + 8 * NBAR + 16;
     static constexpr int THREADS = 18 * 32;
-    static constexpr int A_COL = 256;           // TMEM: two accumulators of 128 columns, then A
+    static constexpr int A_COL = 256;           // TMEM: two accumulators of 128 columns, then the stages
+    static_assert(STG_OFF % 1024 == 0 && B_OFF % 1024 == 0, "swizzled tiles");
     static_assert(BYTES + 1024 <= 227 * 1024, "shared memory");
 };
 
 template <bool GATED>
 __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_constant__ ResParams p) {
     using L = Res;
-    constexpr int NS = L::NS, NB = L::NB, F = GATED ? 64 : 128;
+    constexpr int NS = L::NS, NA = L::NA, F = GATED ? 64 : 128;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(smem);
-    const uint32_t bar_full = sb + L::BAR_OFF, bar_empty = bar_full + 8 * NS, bar_bfull = bar_empty + 8 * NS,
-                   bar_bempty = bar_bfull + 8 * NB, bar_afull = bar_bempty + 8 * NB, bar_aempty = bar_afull + 8,
-                   bar_accfull = bar_aempty + 8, bar_accempty = bar_accfull + 16, bar_done = bar_accempty + 16;
+    const uint32_t bar_full = sb + L::BAR_OFF, bar_empty = bar_full + 8 * NS, bar_afull = bar_empty + 8 * NS,
+                   bar_aempty = bar_afull + 8 * NA, bar_wfull = bar_aempty + 8 * NA, bar_wempty = bar_wfull + 8,
+                   bar_accfull = bar_wempty + 8, bar_accempty = bar_accfull + 16, bar_ffull = bar_accempty + 16,
+                   bar_fempty = bar_ffull + 8, bar_done = bar_fempty + 8;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFF + 8 * L::NBAR);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nkb = (p.k + 127) / 128;
@@ -684,16 +689,18 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
             mbar_init(bar_full + 8 * i, 1);
             mbar_init(bar_empty + 8 * i, 8);
         }
-        for (int i = 0; i < NB; ++i) {
-            mbar_init(bar_bfull + 8 * i, 8);
-            mbar_init(bar_bempty + 8 * i, 1);
+        for (int i = 0; i < NA; ++i) {
+            mbar_init(bar_afull + 8 * i, 8);
+            mbar_init(bar_aempty + 8 * i, 1);
         }
-        mbar_init(bar_afull, 8);
-        mbar_init(bar_aempty, 1);
+        mbar_init(bar_wfull, 8);
+        mbar_init(bar_wempty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_accfull + 8 * i, 1);
             mbar_init(bar_accempty + 8 * i, 8);
         }
+        mbar_init(bar_ffull, 8);
+        mbar_init(bar_fempty, 8);
         mbar_init(bar_done, 1);
         fence_mbar_init();
     }
@@ -734,7 +741,7 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
                 for (int kb = 0; kb < nkb; ++kb, ++ci) {
                     const int s = slot();
                     if (!ok) break;
-                    if (GATED) {
+                    if (GATED) {                // rows 0-63 gate, 64-127 up
                         tma_load_2d_e(sb + s * L::CHUNK, &p.tw[0], bar_full + 8 * s, kb * 128, o0, e);
                         tma_load_2d_e(sb + s * L::CHUNK + L::CHUNK / 2, &p.tw[1], bar_full + 8 * s, kb * 128, o0, e);
                     } else {
@@ -756,203 +763,256 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
         for (int u = u0, ft = ft0, tt = tt0; u < u1 && ok; ++u, next(ft, tt)) {
             const int i = u - u0, b = i & 1;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_accempty + 8 * b, ((i >> 1) & 1) ^ 1));
-            if (ok && (u == u0 || tt == 0)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_afull, nfill++ & 1));
+            if (ok && (u == u0 || tt == 0)) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_wfull, nfill++ & 1));
             for (int kb = 0; kb < nkb && ok; ++kb, ++xi) {
-                const int s = xi % NB;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_bfull + 8 * s, (xi / NB) & 1));
+                const int s = xi % NA;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_afull + 8 * s, (xi / NA) & 1));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t d0 = smem_desc_sw128(sb + L::B_OFF + s * 2 * L::BBOX);
-                const uint32_t a0 = tbase + L::A_COL + 64 * kb;
+                const uint64_t d0 = smem_desc_sw128(sb + L::B_OFF + kb * 2 * L::BBOX);
+                const uint32_t a0 = tbase + L::A_COL + 64 * s;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     mma_ts_bf16_e(tbase + 128 * b, a0 + 8 * j, d0 + (uint64_t)(((j >> 2) * L::BBOX + (j & 3) * 32) >> 4),
                                   idesc, (uint32_t)(kb != 0 || j != 0), e);
-                mma_commit_e(bar_bempty + 8 * s, e);
+                mma_commit_e(bar_aempty + 8 * s, e);
             }
             if (!ok) break;
             mma_commit_e(bar_accfull + 8 * b, e);
             // the last unit on these weights: they may be replaced
-            if (u + 1 < u1 && tt + 1 == p.ttiles) mma_commit_e(bar_aempty, e);
+            if (u + 1 < u1 && tt + 1 == p.ttiles) mma_commit_e(bar_wempty, e);
         }
         mma_commit_e(bar_done, e);              // every MMA issued above
         if (!mbar_wait(bar_done, 0, 20000000ull)) ok = false;
     } else if (warp < 10) {
-        const int q = warp & 3, h = (warp - 2) >> 2;
-        // gated: lanes 0-15 gate rows, 16-31 the same features' up rows
-        const int row = GATED ? (lane & 16 ? 64 : 0) + 16 * q + (lane & 15) : 32 * q + lane;
-        // Tokens: the warp widens 16 of a chunk's, lane l the 16-byte piece c = l % 8
-        // of tokens l / 8 + 4 j.  Piece c becomes pieces 2c, 2c + 1 of 128-byte
-        // rows in the box of its half of k, all swizzled by the row (row + 4 flips
-        // bit 6 of the offset); the halves' lanes store in opposite order, so
-        // that no two hit one bank.
-        const int xr = 16 * (warp - 2) + (lane >> 3), xc = lane & 7, xhi = xc >> 2;
-        const int xrow = xr * 128, xs0 = (xc ^ (xr & 7)) << 4, xbox = xhi * L::BBOX + xr * 128;
-        const int xd0 = ((2 * (xc & 3) + xhi) ^ (xr & 7)) << 4, xd1 = ((2 * (xc & 3) + 1 - xhi) ^ (xr & 7)) << 4;
+        const int q = warp & 3, h = (warp - 2) >> 2, row = 32 * q + lane;
+        // Weights: the warp widens 16 rows of a chunk, lane l the 16-byte piece
+        // c = l % 8 of rows l / 8 + 4 j.  Piece c becomes pieces 2c, 2c + 1 of
+        // 128-byte rows in the box of its half of k, all swizzled by the row (row
+        // + 4 flips bit 6 of the offset); the halves' lanes store in opposite
+        // order, so that no two hit one bank.
+        const int wr = 16 * (warp - 2) + (lane >> 3), wc = lane & 7, whi = wc >> 2;
+        const int wrow = wr * 128, ws0 = (wc ^ (wr & 7)) << 4, wbox = whi * L::BBOX + wr * 128;
+        const int wd0 = ((2 * (wc & 3) + whi) ^ (wr & 7)) << 4, wd1 = ((2 * (wc & 3) + 1 - whi) ^ (wr & 7)) << 4;
         int ci = 0, xi = 0, nfill = 0;
         for (int u = u0, ft = ft0, tt = tt0; u < u1 && ok; ++u, next(ft, tt)) {
             if (u == u0 || tt == 0) {
+                // the factors of the tile's columns: this warp's 16, once the drain
+                // of the features before is over
+                if (nfill) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_fempty, (nfill - 1) & 1));
+                if (!ok) break;
+                {
+                    const I8Item &it = p.it[item_of(ft)];
+                    const int c = 16 * (warp - 2) + (lane & 15), o = (ft - it.tile0) * F + (GATED ? c & 63 : c);
+                    const bool up = GATED && c >= 64;
+                    const float *src = lane < 16 ? (up ? it.scale2 : it.scale) : (up ? it.bias2 : it.bias);
+                    reinterpret_cast<float *>(smem + L::FAC_OFF)[(lane < 16 ? 0 : 128) + c] =
+                        o < it.n && src ? src[o] : 0.f;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_ffull);
+                }
                 // the MMAs on the weights before are complete
-                if (nfill) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_aempty, (nfill - 1) & 1));
+                if (nfill) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_wempty, (nfill - 1) & 1));
                 ++nfill;
-                tc_fence_after();
                 for (int kb = 0; kb < nkb && ok; ++kb, ++ci) {
                     const int s = ci % NS;
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * s, (ci / NS) & 1));
                     if (!ok) break;
-                    uint32_t r[32];
+                    const uint8_t *src = smem + s * L::CHUNK + wrow;
+                    uint8_t *dst = smem + L::B_OFF + kb * 2 * L::BBOX + wbox;
+                    uint4 v[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(smem + s * L::CHUNK + row * 128 +
-                                                                         (((4 * h + c) ^ (row & 7)) << 4));
-                        widen4(v.x, r[8 * c + 0], r[8 * c + 1]);
-                        widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
-                        widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
-                        widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = *reinterpret_cast<const uint4 *>(src + 512 * j + (ws0 ^ (64 * (j & 1))));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint4 lo, hi;
+                        widen4(v[j].x, lo.x, lo.y);
+                        widen4(v[j].y, lo.z, lo.w);
+                        widen4(v[j].z, hi.x, hi.y);
+                        widen4(v[j].w, hi.z, hi.w);
+                        *reinterpret_cast<uint4 *>(dst + 512 * j + (wd0 ^ (64 * (j & 1)))) = whi ? hi : lo;
+                        *reinterpret_cast<uint4 *>(dst + 512 * j + (wd1 ^ (64 * (j & 1)))) = whi ? lo : hi;
                     }
-                    tmem_st32(tbase + ((uint32_t)(32 * q) << 16) + L::A_COL + 64 * kb + 32 * h, r);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar_empty + 8 * s);
                 }
+                fence_async_smem();             // the weights, visible to the MMAs
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(bar_wfull);
+            }
+            for (int kb = 0; kb < nkb && ok; ++kb, ++ci, ++xi) {
+                const int s = ci % NS, a = xi % NA;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * s, (ci / NS) & 1));
+                if (!ok) break;
+                uint32_t r[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(smem + s * L::CHUNK + row * 128 +
+                                                                     (((4 * h + c) ^ (row & 7)) << 4));
+                    widen4(v.x, r[8 * c + 0], r[8 * c + 1]);
+                    widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+                    widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+                    widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_aempty + 8 * a, ((xi / NA) & 1) ^ 1));
+                if (!ok) break;
+                tc_fence_after();
+                tmem_st32(tbase + ((uint32_t)(32 * q) << 16) + L::A_COL + 64 * a + 32 * h, r);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(bar_afull);
-            }
-            for (int kb = 0; kb < nkb && ok; ++kb, ++ci, ++xi) {
-                const int s = ci % NS, bs = xi % NB;
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_full + 8 * s, (ci / NS) & 1) &&
-                                                 mbar_wait(bar_bempty + 8 * bs, ((xi / NB) & 1) ^ 1));
-                if (!ok) break;
-                const uint8_t *src = smem + s * L::CHUNK + xrow;
-                uint8_t *dst = smem + L::B_OFF + bs * 2 * L::BBOX + xbox;
-                uint4 v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[j] = *reinterpret_cast<const uint4 *>(src + 512 * j + (xs0 ^ (64 * (j & 1))));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint4 lo, hi;
-                    widen4(v[j].x, lo.x, lo.y);
-                    widen4(v[j].y, lo.z, lo.w);
-                    widen4(v[j].z, hi.x, hi.y);
-                    widen4(v[j].w, hi.z, hi.w);
-                    *reinterpret_cast<uint4 *>(dst + 512 * j + (xd0 ^ (64 * (j & 1)))) = xhi ? hi : lo;
-                    *reinterpret_cast<uint4 *>(dst + 512 * j + (xd1 ^ (64 * (j & 1)))) = xhi ? lo : hi;
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar_bfull + 8 * bs);
-                    mbar_arrive(bar_empty + 8 * s);
-                }
+                if (lane == 0) mbar_arrive(bar_afull + 8 * a);
             }
         }
     } else {
         const int q = warp & 3, h = (warp - 10) >> 2;
-        const bool upper = GATED && (lane & 16);
-        float *tsw = reinterpret_cast<float *>(smem + L::TS_OFF) + (warp - 10) * 64;
+        const float *fac = reinterpret_cast<const float *>(smem + L::FAC_OFF);
         uint8_t *stg = smem + L::STG_OFF + (warp - 10) * L::STG;
-        int turn = 0;                           // blocks so far: two halves in turn
-        // the half's last stores (a group two back) have read it
-        auto block = [&]() {
-            if (lane == 0) bulk_wait_read_n<1>();
+        int nfill = 0, last_bytes = 0, turn = 0;
+        // The next staging block of `bytes` (2 KB blocks in two halves; a 4 KB
+        // block, or a change of size, waits for all stores before).
+        auto block = [&](int bytes) {
+            if (lane == 0) {
+                if (bytes == L::STG || bytes != last_bytes) bulk_wait_read_n<0>();
+                else bulk_wait_read_n<1>();
+            }
             __syncwarp();
-            return stg + (turn++ & 1) * (L::STG / 2);
+            last_bytes = bytes;
+            return stg + (bytes == L::STG ? 0 : (turn++ & 1) * (L::STG / 2));
         };
-        // a unit's per-feature and per-token factors, loaded a unit ahead
-        struct Factors {
-            float sc, bi, ts0, ts1;
-        };
-        auto factors = [&](int ft, int tt) {
-            const I8Item &it = p.it[item_of(ft)];
-            const int fo = (ft - it.tile0) * F + (GATED ? 16 : 32) * q, o = fo + (GATED ? lane & 15 : lane);
-            const float *scale = upper ? it.scale2 : it.scale, *bias = upper ? it.bias2 : it.bias;
-            const int t = tt * 128 + 64 * h + lane;
-            Factors f;
-            f.sc = fo < it.n ? scale[o] : 0.f;
-            f.bi = fo < it.n && bias ? bias[o] : 0.f;
-            f.ts0 = t < p.m ? p.xs[t] : 0.f;
-            f.ts1 = t + 32 < p.m ? p.xs[t + 32] : 0.f;
-            return f;
-        };
-        Factors nf = factors(ft0, tt0);
+        const uint32_t trow = (uint32_t)(32 * q) << 16;
+        float nts = tt0 * 128 + 32 * q + lane < p.m ? p.xs[tt0 * 128 + 32 * q + lane] : 0.f;
         for (int u = u0, ft = ft0, tt = tt0; u < u1 && ok; ++u, next(ft, tt)) {
             const int i = u - u0, b = i & 1;
             const int zi = item_of(ft);
             const I8Item &it = p.it[zi];
-            const int fo = (ft - it.tile0) * F + (GATED ? 16 : 32) * q;     // the warp's features: all below n or none
-            const int t0 = tt * 128 + 64 * h;   // this warp's tokens
+            const int tb = tt * 128 + 32 * q;   // this warp's tokens
+            const int t = tb + lane;
             const bool f32 = it.ydt == TE_F32, inplace = it.resid != nullptr && it.resid == it.y;
-            const float sc = nf.sc, bi = nf.bi;
-            __syncwarp();                       // the last tile's scales have been read
-            tsw[lane] = nf.ts0;
-            tsw[32 + lane] = nf.ts1;
-            __syncwarp();
-            if (u + 1 < u1) {
+            const float ts = nts;
+            if (u + 1 < u1) {                   // the next tile's token scale
                 int fn = ft, tn = tt;
                 next(fn, tn);
-                nf = factors(fn, tn);
+                nts = tn * 128 + 32 * q + lane < p.m ? p.xs[tn * 128 + 32 * q + lane] : 0.f;
             }
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_accfull + 8 * b, (i >> 1) & 1));
+            if (u == u0 || tt == 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_ffull, nfill++ & 1));
+            if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_accfull + 8 * b, (i >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
-            const int blocks = fo >= it.n || t0 >= p.m ? 0 : (t0 + 32 >= p.m ? 1 : 2);
-            for (int c = 0; c < 2; ++c) {
-                const int tb = t0 + 32 * c;
-                uint32_t v[32];
-                if (c < blocks) {
-                    tmem_ld32(tbase + ((uint32_t)(32 * q) << 16) + 128 * b + 64 * h + 32 * c, v);
-                    tmem_wait_ld();
+            const uint64_t ts2 = f2_pack(ts, ts);
+            // (acc * ts) * scale + bias of 32 columns from column c, in place
+            auto scaled = [&](uint32_t (&v)[32], int c) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 s4 = *reinterpret_cast<const float4 *>(fac + c + j);
+                    const float4 b4 = *reinterpret_cast<const float4 *>(fac + 128 + c + j);
+                    const uint64_t y0 = f2_fma(f2_mul(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), ts2),
+                                               f2_pack(s4.x, s4.y), f2_pack(b4.x, b4.y));
+                    const uint64_t y1 = f2_fma(f2_mul(f2_pack(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), ts2),
+                                               f2_pack(s4.z, s4.w), f2_pack(b4.z, b4.w));
+                    float a0, a1, a2, a3;
+                    f2_unpack(y0, a0, a1);
+                    f2_unpack(y1, a2, a3);
+                    v[j] = __float_as_uint(a0);
+                    v[j + 1] = __float_as_uint(a1);
+                    v[j + 2] = __float_as_uint(a2);
+                    v[j + 3] = __float_as_uint(a3);
                 }
-                if (c == 1) {                   // read: the accumulator may take the next tile but one
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_accempty + 8 * b);
-                }
-                if (c >= blocks) continue;
-                uint8_t *st = nullptr;
-                if constexpr (GATED) {
-                    float y[16];
-                    if (it.act == TE_ACT_GELU_TANH)
-                        gate_block<true, TE_ACT_GELU_TANH>(v, sc, bi, tsw + 32 * c, upper, y);
-                    else
-                        gate_block<true, TE_ACT_SILU>(v, sc, bi, tsw + 32 * c, upper, y);
-                    st = block();
-                    uint16_t *sh = reinterpret_cast<uint16_t *>(st) + (upper ? 256 : 0) + (lane & 15);
+            };
+            // 32 tokens x 32 features as bf16: 64-byte rows, 64-byte swizzle
+            auto store_bf16 = [&](const uint32_t (&v)[32], int fo) {
+                uint8_t *st = block(2048);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) sh[j * 16] = __bfloat16_as_ushort(__float2bfloat16_rn(y[j]));
-                } else {
-                    scale_block<true>(v, sc, bi, tsw + 32 * c);
-                    if (it.act) act_block<true>(v, it.act - 1);
-                    if (it.resid && !inplace) {
-                        const float *rp = it.resid + (long long)tb * it.ldr + fo + lane;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (tb + j < p.m) v[j] = __float_as_uint(__uint_as_float(v[j]) + rp[(long long)j * it.ldr]);
-                    }
-                    st = block();
-                    if (f32) {
-                        float *sf = reinterpret_cast<float *>(st) + lane;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) sf[j * 32] = __uint_as_float(v[j]);
-                    } else {
-                        uint16_t *sh = reinterpret_cast<uint16_t *>(st) + lane;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const uint32_t w = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                            sh[j * 32] = (uint16_t)w;
-                            sh[(j + 1) * 32] = (uint16_t)(w >> 16);
-                        }
-                    }
+                for (int c = 0; c < 4; ++c) {
+                    uint4 w;
+                    w.x = pack_bf16x2(__uint_as_float(v[8 * c]), __uint_as_float(v[8 * c + 1]));
+                    w.y = pack_bf16x2(__uint_as_float(v[8 * c + 2]), __uint_as_float(v[8 * c + 3]));
+                    w.z = pack_bf16x2(__uint_as_float(v[8 * c + 4]), __uint_as_float(v[8 * c + 5]));
+                    w.w = pack_bf16x2(__uint_as_float(v[8 * c + 6]), __uint_as_float(v[8 * c + 7]));
+                    *reinterpret_cast<uint4 *>(st + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = w;
                 }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (inplace) tma_reduce_add_2d(&p.ty[zi], smem_u32(st), fo, tb);
-                    else tma_store_2d(&p.ty[zi], smem_u32(st), fo, tb);
+                    tma_store_2d(&p.ty[zi], smem_u32(st), fo, tb);
                     bulk_commit();
                 }
+            };
+            const bool any = tb < p.m;          // warp-uniform
+            if constexpr (GATED) {
+                const int fo = (ft - it.tile0) * F + 32 * h;
+                uint32_t g[32], up[32];
+                if (any) {
+                    tmem_ld32(tbase + trow + 128 * b + 32 * h, g);
+                    tmem_ld32(tbase + trow + 128 * b + 64 + 32 * h, up);
+                    tmem_wait_ld();
+                    scaled(g, 32 * h);
+                    scaled(up, 64 + 32 * h);
+                }
+                // read, and the factors too
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_accempty + 8 * b);
+                if (any && fo < it.n) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        g[j] = __float_as_uint(apply_act(__uint_as_float(g[j]), it.act) * __uint_as_float(up[j]));
+                    store_bf16(g, fo);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    const int col = 64 * h + 32 * c, fo = (ft - it.tile0) * F + col;
+                    uint32_t v[32];
+                    if (any) {
+                        tmem_ld32(tbase + trow + 128 * b + col, v);
+                        tmem_wait_ld();
+                        scaled(v, col);
+                    }
+                    if (c == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_accempty + 8 * b);
+                    }
+                    if (!any || fo >= it.n) continue;       // n is a multiple of 32
+                    if (it.act) act_block<true>(v, it.act - 1);
+                    if (it.resid && !inplace && t < p.m) {
+                        const float4 *rp = reinterpret_cast<const float4 *>(it.resid + (long long)t * it.ldr + fo);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 r4 = rp[j];
+                            v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + r4.x);
+                            v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + r4.y);
+                            v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + r4.z);
+                            v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + r4.w);
+                        }
+                    }
+                    if (!f32) {
+                        store_bf16(v, fo);
+                        continue;
+                    }
+                    // f32: 128-byte rows, 128-byte swizzle
+                    uint8_t *st = block(4096);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4 *>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (inplace) tma_reduce_add_2d(&p.ty[zi], smem_u32(st), fo, tb);
+                        else tma_store_2d(&p.ty[zi], smem_u32(st), fo, tb);
+                        bulk_commit();
+                    }
+                }
+            }
+            // the last unit on these features: their factors may be replaced
+            if (u + 1 < u1 && tt + 1 == p.ttiles) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_fempty);
             }
         }
         bulk_wait_all();                        // before the CTA's shared memory goes away
@@ -997,8 +1057,8 @@ te_status res_launch(const I8Params &q, cudaStream_t s) {
     for (int i = 0; i < q.z && st == TE_OK; ++i) {
         const bool f32 = q.it[i].ydt == TE_F32;
         st = make_map_2d(&p.ty[i], f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q.it[i].y,
-                         (uint64_t)q.it[i].n, (uint64_t)q.m, (uint64_t)q.it[i].ldy * (f32 ? 4 : 2), GATED ? 16 : 32,
-                         32, CU_TENSOR_MAP_SWIZZLE_NONE);
+                         (uint64_t)q.it[i].n, (uint64_t)q.m, (uint64_t)q.it[i].ldy * (f32 ? 4 : 2), 32, 32,
+                         f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
     }
     if (st != TE_OK) return st;
     if ((st = gemm_error_word(&p.err)) != TE_OK) return st;
