@@ -651,7 +651,7 @@ struct ResParams {
     int m, k, z, ttiles, units;
 };
 struct Res {
-    static constexpr int NS = 3;                // int8 chunks
+    static constexpr int NS = 4;                // int8 chunks
     static constexpr int NA = 4;                // TMEM stages of widened tokens
     static constexpr int CHUNK = 128 * 128;     // int8 chunk
     static constexpr int BBOX = 128 * 128;      // 64 k of 128 widened weight rows
@@ -1120,9 +1120,14 @@ constexpr int MAX_K = 65536;
 //   m = 384 k 3840 n 11520            54.5   32.7
 // Small: to 8 tokens; to 16 (32) tokens while the weights are under 16 M (4 M)
 // values, beyond which its warps' widening of the tokens costs more than the
-// TMEM pipeline's start.  Between mid and large, by their modelled times: mid
-// as above; large 7 us (the widening pass and a second launch) and 0.39 us a
-// stage of each wave of 256 x 128 units (both fit the measured to about 15 %).
+// TMEM pipeline's start.  Else to 1024 tokens mid where its modelled time (see
+// mid_consider) is below that of what takes the larger counts: at k <= 512 the
+// kernel with resident weights, 5.5 us and 1 + 0.45 us a stage for each round
+// of its CTAs; beyond, large, 7 us (the widening pass and a second launch) and
+// 0.39 us a stage of each wave of 256 x 128 units (fits of what was measured,
+// to about 15 %).  Resident against large at 16238 tokens (us): k 512, n 1536
+// bf16 28.8 and 35.7; n 512 f32 15.0 and 22.3; gated 2 x 2048 64.5 and 71.6;
+// k 64, n 512 f32 11.6 and 19.7.
 enum Path { SMALL, MID, RES, LARGE };
 template <bool GATED>
 te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
@@ -1138,9 +1143,17 @@ te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
     if (p.m > 1024) return TE_OK;
     const te_status st = mid_plan<GATED>(plan, tiles, p.m, p.k);
     if (st != TE_OK) return st;
-    const long long units = (long long)((tiles + 1) / 2) * ((p.m + 127) / 128);
-    const long long waves = (units + SMS / 2 - 1) / (SMS / 2);
-    if (p.m <= 32 || plan.us < 7.0 + 0.39 * ((p.k + 127) / 128) * waves) path = MID;
+    const int nkb = (p.k + 127) / 128;
+    const long long ttiles = (p.m + 127) / 128;
+    double other;
+    if (path == RES) {
+        const long long rounds = (tiles * ttiles + SMS - 1) / SMS;
+        other = 5.5 + rounds * (1.0 + 0.45 * nkb);
+    } else {
+        const long long waves = ((tiles + 1) / 2 * ttiles + SMS / 2 - 1) / (SMS / 2);
+        other = 7.0 + 0.39 * nkb * waves;
+    }
+    if (p.m <= 32 || plan.us < other) path = MID;
     return TE_OK;
 }
 te_status check_x(const char *what, const void *x, int64_t ldx, const float *xs, int32_t m, int32_t k) {
