@@ -157,3 +157,22 @@ def test_qk_rope_axes_rejects_bad_arguments(L):
     bad.axis[5] = 3
     assert call(pl=bad)[0] == te.TE_EINVAL
     assert call(rows=0)[0] == call(nq=0, nkv=0)[0] == te.TE_OK
+
+
+def test_the_binding_refuses_what_is_not_a_tensor_on_the_device(L):
+    # the marshalling module's own checks, before any CUDA call
+    import torch
+    x, s, q = torch.zeros(2, 64), torch.zeros(2), torch.zeros(2, 64, dtype=torch.int8)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        te.quant_rows(x, q, s)
+    with pytest.raises(TypeError, match="dtype"):
+        te.quant_rows(x.double(), q, s)
+    with pytest.raises(TypeError, match="not a tensor"):
+        te.quant_rows(3, q, s)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        te.i8_linear(q, s, [], None)
+    plan = te.rope_axes_plan(64, (16, 24, 24))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        te.qk_rope_axes(x, 64, x, 64, 0, 0, 1, 0, 64, None, None, 1e-6, plan, q, 1.0, 2)
+    with pytest.raises(OverflowError):
+        te.qk_rope_axes(x, 64, x, 64, 0, 0, 1, 0, 64, None, None, 1e-6, plan, q, 1.0, 1 << 40)

@@ -241,6 +241,13 @@ LINEAR = [
     (5000, 512, [512, 512, 512], False, None, "f32"),
     (6001, 448, [1536], False, None, "bf16"),
     (8448, 3840, [3840], False, "in", "f32"),
+    # short k, many tokens: weights that stay, runs that cross into the next features
+    (3000, 448, [96, 160, 512], True, "in", "f32"),
+    (2000, 64, [32], False, "sep", "bf16"),
+    (2500, 128, [640], True, None, "bf16"),
+    (1100, 320, [96, 32], True, "sep", "f32"),
+    (20000, 512, [224], True, None, "f32"),
+    (12345, 192, [96, 416], False, None, "bf16"),
 ]
 
 
@@ -294,7 +301,8 @@ def test_i8_linear_matches_64_bits(m, k, ns, bias, resid, ydt):
 
 @pytest.mark.parametrize("act", [te.TE_EPI_GELU_TANH, te.TE_EPI_SILU])
 @pytest.mark.parametrize("m,k,n,ydt", [(1, 512, 2048, "bf16"), (6, 768, 320, "f32"), (45, 768, 256, "bf16"),
-                                       (300, 512, 1024, "f32"), (2500, 768, 768, "bf16"), (2500, 2304, 3840, "f32")])
+                                       (300, 512, 1024, "f32"), (2500, 768, 768, "bf16"), (2500, 2304, 3840, "f32"),
+                                       (2500, 512, 224, "f32"), (1500, 128, 96, "bf16")])
 def test_i8_linear_epilogue_activation(m, k, n, ydt, act):
     torch = _torch()
     rng = np.random.default_rng([m, k, n, act])
@@ -315,7 +323,7 @@ def test_i8_linear_epilogue_activation(m, k, n, ydt, act):
 
 GATED = [(1, 64, 32), (1, 3840, 160), (4, 512, 2048), (8, 1024, 96), (13, 768, 480), (37, 512, 2048), (64, 256, 64),
          (70, 3840, 1024), (101, 768, 3840), (257, 192, 96), (600, 512, 2048), (1100, 512, 2048), (2112, 1024, 1440),
-         (2112, 3840, 2560), (5000, 512, 320)]
+         (2112, 3840, 2560), (5000, 512, 320), (1500, 64, 32), (3333, 320, 992), (20000, 192, 96)]
 
 
 @pytest.mark.parametrize("act", [te.TE_ACT_GELU_TANH, te.TE_ACT_SILU])
@@ -346,6 +354,84 @@ def test_i8_gated_linear_matches_64_bits(m, k, f, act):
     worst = record_margin("i8_gated", f"m={m} k={k} f={f}", _ratio(got, ref, lim), 1.0)
     assert worst <= 1.0
     assert bool(torch.isnan(full[:m, f:]).all()) and bool(torch.isnan(full[m:]).all())
+
+
+@pytest.mark.parametrize("m", [1, 8, 9, 16, 17, 32, 33, 64, 65, 100, 128, 129, 200, 333, 512, 1000, 1024, 1025, 1999])
+@pytest.mark.parametrize("k", [64, 192, 512, 576, 4096])
+def test_every_kernel_choice_is_exact_on_integers(m, k):
+    # unit scales and an f32 output: the sums themselves, for item widths that
+    # end inside a tile, one item and several, plain and gated
+    torch = _torch()
+    gen = torch.Generator("cuda").manual_seed(m * 7 + k)
+    x = torch.randint(-60, 61, (m, k), generator=gen, device="cuda", dtype=torch.int8)
+    ones = torch.ones(max(m, 4096), device="cuda")
+    for ns in ([32], [96, 160, 32], [1600]):
+        w = [torch.randint(-127, 128, (n, k), generator=gen, device="cuda", dtype=torch.int8) for n in ns]
+        full = [torch.full((m + 1, n), float("nan"), device="cuda") for n in ns]
+        te.i8_linear(x, ones[:m], [dict(w=te.q8w(a, ones[:a.shape[0]]), y=y[:m], ldy=y.shape[1])
+                                   for a, y in zip(w, full)], _ws(m, k, sum(ns)))
+        for a, y in zip(w, full):
+            ref = x.double() @ a.double().T
+            assert float(ref.abs().max()) < 2 ** 24
+            assert torch.equal(y[:m].double(), ref), (m, k, ns)
+            assert bool(torch.isnan(y[m]).all())
+    te.check()
+
+
+@pytest.mark.parametrize("m,k,ns,gated", [(7, 3840, [384, 96], False), (25, 1024, [512], False), (40, 512, [640], True),
+                                          (101, 768, [768, 768], False), (200, 2048, [1024], True),
+                                          (700, 4096, [256], False), (3000, 512, [512, 96], False),
+                                          (2500, 448, [320], True), (2112, 1152, [1024], True)])
+def test_repeated_calls_give_the_same_bits(m, k, ns, gated):
+    # back to back on one workspace and one set of outputs, other work between
+    torch = _torch()
+    rng = np.random.default_rng([m, k])
+    x, xs = _tokens(rng, m, k, full=True)
+    xd, sd, ws = _dev(x), _dev(xs), _ws(m, k, 2 * sum(ns))
+    ws_tensors = [_dev_w(_weight(rng, n, k, True)) for n in ns + ns]
+    qw = [t[0] for t in ws_tensors]
+    dt = torch.bfloat16 if gated else torch.float32
+    outs = [torch.empty(m, n, device="cuda", dtype=dt) for n in ns]
+
+    def call():
+        if gated:
+            te.i8_gated_linear(xd, sd, qw[0], qw[1], te.TE_ACT_GELU_TANH, outs[0], ws)
+        else:
+            te.i8_linear(xd, sd, [dict(w=w, y=y, ldy=y.shape[1]) for w, y in zip(qw, outs)], ws)
+
+    call()
+    first = [y.clone() for y in outs]
+    differ = torch.zeros((), device="cuda", dtype=torch.int64)
+    for _ in range(60):
+        for y in outs:
+            y.zero_()
+        call()
+        for y, f in zip(outs, first):
+            differ += (y != f).sum()
+    te.check()
+    assert int(differ) == 0
+
+
+def test_calls_on_two_streams_with_workspaces_of_their_own():
+    torch = _torch()
+    rng = np.random.default_rng(77)
+    jobs = []
+    for m, k, n in ((3000, 1024, 768), (90, 768, 768), (2500, 512, 512), (5, 2048, 1024)):
+        x, xs = _tokens(rng, m, k)
+        w = _weight(rng, n, k, True)
+        qw, keep = _dev_w(w)
+        xd, sd = _dev(x), _dev(xs)
+        ref, y = torch.empty(m, n, device="cuda"), torch.empty(m, n, device="cuda")
+        te.i8_linear(xd, sd, [dict(w=qw, y=ref, ldy=n)], _ws(m, k, n))
+        jobs.append((xd, sd, qw, keep, ref, y, _ws(m, k, n), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for xd, sd, qw, _, ref, y, ws, s in jobs:
+            te.i8_linear(xd, sd, [dict(w=qw, y=y, ldy=y.shape[1])], ws, stream=s)
+    torch.cuda.synchronize()
+    te.check()
+    for *_, ref, y, ws, s in jobs:
+        assert torch.equal(y, ref)
 
 
 @pytest.mark.parametrize("m", [1, 6, 40, 300, 2200])
