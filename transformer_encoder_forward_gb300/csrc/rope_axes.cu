@@ -27,10 +27,11 @@ struct RopeParams {
     const float *qn, *kn;
     const int32_t *pos;
     long long lds, ldd, ldp;
-    int items;                // rows * (cq + ck)
+    int items;                // rows * cuts
     int q_off, k_off, nq, nkv, hd;
-    int cq, ck;               // chunks a row's q heads and k heads are cut into
-    int hq, hk;               // heads a chunk
+    int hpi;                  // heads a slot
+    int sq, slots;            // slots of the q heads, and with the k heads'
+    int cuts, per;            // items a row's slots are cut into, slots an item
     float eps, q_mul, inv_hd;
     int pairs;
     // rope_vec_kernel: unit u of a head is 4 channels from c1[u] and 4 from
@@ -112,228 +113,281 @@ __device__ __forceinline__ void put_unit(T *p1, T *p2, const uint64_t (&y1)[2], 
     store4(p2, b);
 }
 
-// One item: a run of the q or the k heads of one row.
+// One item: a run of one row's slots; q heads first, then k heads, each part
+// in slots of hpi heads.
 struct Chunk {
     long long row;
-    int h0, h1, off;          // heads [h0, h1) of the part whose columns start at off
-    bool isq;
+    int s0, s1;
 };
 __device__ __forceinline__ Chunk chunk_of(const RopeParams &p, unsigned item) {
-    const unsigned per = p.cq + p.ck, row = item / per;
+    const unsigned row = item / (unsigned)p.cuts;
     Chunk c;
     c.row = row;
-    const int i = (int)(item - row * per);
-    c.isq = i < p.cq;
-    const int n = c.isq ? p.nq : p.nkv, h = c.isq ? p.hq : p.hk, j = c.isq ? i : i - p.cq;
-    c.h0 = j * h;
-    c.h1 = c.h0 + h < n ? c.h0 + h : n;
-    c.off = c.isq ? p.q_off : p.k_off;
+    c.s0 = (int)(item - row * p.cuts) * p.per;
+    c.s1 = c.s0 + p.per < p.slots ? c.s0 + p.per : p.slots;
     return c;
 }
+// The heads [h0, h1) of part `k` (0: q, 1: k) in the chunk; empty where h0 >= h1.
+__device__ __forceinline__ void part_heads(const RopeParams &p, const Chunk &c, int k, int &h0, int &h1) {
+    const int lo = k ? (c.s0 > p.sq ? c.s0 - p.sq : 0) : c.s0, hi = k ? c.s1 - p.sq : (c.s1 < p.sq ? c.s1 : p.sq);
+    const int n = k ? p.nkv : p.nq;
+    h0 = lo * p.hpi;
+    h1 = hi * p.hpi < n ? hi * p.hpi : n;
+}
 
-// A warp an item (persistent over items).  A head spans LPH lanes, each with
+// A warp an item (persistent over items).  A head spans hd / 8 lanes, each with
 // the two 4-channel pieces of one unit: both members of its four pairs
 // (adjacent pairing: 8 neighbouring channels), so the rotation exchanges
-// nothing between lanes and the norm is a reduction over the lane group.  A
-// lane's unit never changes, so its pairs' matrices serve all heads of the
-// item.  All loads of a slot group go out before any arithmetic, which runs in
-// f32 pairs.  Bound by HBM: registers are held to 64 (f32 80) for four (three)
-// CTAs an SM, with the frequency words in shared memory; at 79 and two CTAs
-// the 32760-row clip (1.0 GB) took 174 us instead of 158 (6.4 TB/s, 0.94 of
-// the measured copy rate).  8448 rows (259 MB) take 47 us, where a plain copy
-// of as many bytes takes 41: a launch's start and end cost both.
+// nothing between lanes and the norm is a reduction over the lane group (LPH
+// lanes, or hd / 8 where that is no power of two: LPH == 0).  A lane's unit
+// never changes, so its pairs' matrices serve all heads of a part.  The row's
+// sines and cosines are worked out once by the whole warp.  All loads of a slot group go out before
+// any arithmetic, which runs in f32 pairs.  Bound by HBM: registers are held to
+// 64 (f32 80) for four (three) CTAs an SM, with the frequency words in shared
+// memory; at 79 and two CTAs the 32760-row clip (1.0 GB) took 174 us instead of
+// 159 (6.3 TB/s, 0.93 of the measured copy rate).  8448 rows (259 MB) take 49
+// us, where a plain copy of as many bytes takes 41: a launch's start and end
+// cost both.  Loads a step ahead in registers (fewer warps) took 55 us.  With few
+// heads a row instructions bound it: 8448 rows of 12 + 4 heads of 96 take 20 us.
 template <typename T, bool ADJ, bool PART, int LPH>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_vec_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int HPI = 32 / LPH;               // heads a load slot
     constexpr int QU = 4;                       // load slots in flight
-    __shared__ __align__(16) unsigned long long turns[TE_ROPE_MAX_PAIRS + 4];
-    __shared__ __align__(4) uint8_t axes[TE_ROPE_MAX_PAIRS + 4];
-    for (int i = threadIdx.x; i < TE_ROPE_MAX_PAIRS + 4; i += 256) {
+    // the row's cosines and sines, a warp's own; pairs past the last do not turn
+    __shared__ __align__(16) float2 rows_cs[8][TE_ROPE_MAX_PAIRS + 4];
+    __shared__ unsigned long long turns[TE_ROPE_MAX_PAIRS];
+    __shared__ uint8_t axes[TE_ROPE_MAX_PAIRS];
+    for (int i = threadIdx.x; i < TE_ROPE_MAX_PAIRS; i += 256) {
         turns[i] = i < p.pairs ? p.turn[i] : 0ull;
         axes[i] = i < p.pairs ? p.axis[i] : 0;
     }
+    if (PART) {
+        for (int i = threadIdx.x; i < 8 * (TE_ROPE_MAX_PAIRS + 4); i += 256) (&rows_cs[0][0])[i] = make_float2(1.f, 0.f);
+    }
     __syncthreads();
     const int lane = threadIdx.x & 31;
-    const int hl = lane / LPH, u = lane % LPH;
-    const bool on = u < p.hd / 8;               // lanes past the head's units idle
+    float2 *cs = rows_cs[threadIdx.x >> 5];
+    const int lph = LPH ? LPH : p.hd / 8, hpi = LPH ? 32 / LPH : p.hpi;
+    const int hl = lane / lph, u = lane - hl * lph;
+    const bool on = LPH ? u < p.hd / 8 : hl < hpi;      // the other lanes idle
     const int uu = on ? u : 0;
     const int c1 = p.c1[uu], c2 = p.c2[uu], p0 = p.p0[uu];
     for (unsigned item = blockIdx.x * 8 + (threadIdx.x >> 5); item < (unsigned)p.items; item += gridDim.x * 8) {
         const Chunk ch = chunk_of(p, item);
-        const T *src = static_cast<const T *>(p.src) + ch.row * p.lds + ch.off;
-        T *dst = static_cast<T *>(p.dst) + ch.row * p.ldd + ch.off;
-        const float *nw = ch.isq ? p.qn : p.kn;
-        // y1 = (x1 m11 - x2 m12) inv, y2 = (x2 m22 + x1 m21) inv: the rotation
-        // with the norm's weights and q_mul multiplied into its matrix, once an item
-        uint64_t m11[2], m12[2], m21[2], m22[2];
-        bool first = true;
-        for (int h0 = ch.h0; h0 < ch.h1; h0 += HPI * QU) {
-            Unit<T> raw[QU];
+        bool turned = false;                    // the row's cosines and sines are there
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            int hbeg, hend;
+            part_heads(p, ch, part, hbeg, hend);
+            const int off = part ? p.k_off : p.q_off;
+            const T *src = static_cast<const T *>(p.src) + ch.row * p.lds + off;
+            T *dst = static_cast<T *>(p.dst) + ch.row * p.ldd + off;
+            const float *nw = part ? p.kn : p.qn;
+            // y1 = (x1 m11 - x2 m12) inv, y2 = (x2 m22 + x1 m21) inv: the rotation
+            // with the norm's weights and q_mul multiplied into its matrix
+            uint64_t m11[2], m12[2], m21[2], m22[2];
+            for (int h0 = hbeg; h0 < hend; h0 += hpi * QU) {
+                Unit<T> raw[QU];
 #pragma unroll
-            for (int i = 0; i < QU; ++i) {
-                const int hh = h0 + i * HPI + hl;
-                if (on && hh < ch.h1) raw[i].load(src + (hh * p.hd + c1), src + (hh * p.hd + c2));
-                else raw[i].zero();
-            }
-            if (first) {                        // behind the first loads
-                first = false;
-                const float mul = ch.isq ? p.q_mul : 1.f;
-                const int32_t *pos = p.pos + ch.row * p.ldp;
-                const uint32_t ax = *reinterpret_cast<const uint32_t *>(axes + p0);
-                float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
-                if (nw && on) {
-                    load4(nw + c1, wa);
-                    load4(nw + c2, wb);
+                for (int i = 0; i < QU; ++i) {
+                    const int hh = h0 + i * hpi + hl;
+                    if (on && hh < hend) raw[i].load(src + (hh * p.hd + c1), src + (hh * p.hd + c2));
+                    else raw[i].zero();
                 }
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float r11[2], r12[2], r21[2], r22[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int pr = 2 * g + e;
-                        const float2 t = turn_cs(pos[(ax >> (8 * pr)) & 3], turns[p0 + pr]);
-                        const float w1 = (ADJ ? (pr < 2 ? wa[2 * pr] : wb[2 * pr - 4]) : wa[pr]) * mul;
-                        const float w2 = (ADJ ? (pr < 2 ? wa[2 * pr + 1] : wb[2 * pr - 3]) : wb[pr]) * mul;
-                        r11[e] = w1 * t.x;
-                        r12[e] = -w2 * t.y;
-                        r21[e] = w1 * t.y;
-                        r22[e] = w2 * t.x;
+                if (h0 == hbeg) {               // behind the first loads
+                    if (!turned) {
+                        turned = true;
+                        const int32_t *pos = p.pos + ch.row * p.ldp;
+                        __syncwarp();           // the last row's have been read
+                        for (int i = lane; i < p.pairs; i += 32) cs[i] = turn_cs(pos[axes[i]], turns[i]);
+                        __syncwarp();
                     }
-                    m11[g] = f2_pack(r11[0], r11[1]);
-                    m12[g] = f2_pack(r12[0], r12[1]);
-                    m21[g] = f2_pack(r21[0], r21[1]);
-                    m22[g] = f2_pack(r22[0], r22[1]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < QU; ++i) {
-                const int hh = h0 + i * HPI + hl;
-                uint64_t x1[2], x2[2], y1[2], y2[2];
-                raw[i].template get<ADJ>(x1, x2);
-                float inv = 1.f;
-                if (nw) {
-                    const uint64_t q2 = f2_fma(x1[0], x1[0], f2_fma(x2[0], x2[0], f2_fma(x1[1], x1[1], f2_mul(x2[1], x2[1]))));
-                    float q, qb;
-                    f2_unpack(q2, q, qb);
-                    q += qb;
-#pragma unroll
-                    for (int o = 1; o < LPH; o <<= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
-                    inv = rsqrtf(fmaf(q, p.inv_hd, p.eps));
-                }
-                const uint64_t inv2 = f2_pack(inv, inv);
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const uint64_t s1 = f2_mul(x1[g], m11[g]), s2 = f2_mul(x2[g], m22[g]);
-                    y1[g] = f2_fma(x2[g], m12[g], s1);
-                    y2[g] = f2_fma(x1[g], m21[g], s2);
-                    if (PART) {                 // pairs that do not turn never see their neighbour
-                        float a0, a1, b0, b1, u0, u1, v0, v1;
-                        f2_unpack(y1[g], a0, a1);
-                        f2_unpack(y2[g], b0, b1);
-                        f2_unpack(s1, u0, u1);
-                        f2_unpack(s2, v0, v1);
-                        const bool t0 = p0 + 2 * g < p.pairs, t1 = p0 + 2 * g + 1 < p.pairs;
-                        y1[g] = f2_pack(t0 ? a0 : u0, t1 ? a1 : u1);
-                        y2[g] = f2_pack(t0 ? b0 : v0, t1 ? b1 : v1);
+                    float4 t4[2];
+                    t4[0] = *reinterpret_cast<const float4 *>(cs + p0);
+                    t4[1] = *reinterpret_cast<const float4 *>(cs + p0 + 2);
+                    const float mul = part ? 1.f : p.q_mul;
+                    float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
+                    if (nw && on) {
+                        load4(nw + c1, wa);
+                        load4(nw + c2, wb);
                     }
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        float r11[2], r12[2], r21[2], r22[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int pr = 2 * g + e;
+                            const float w1 = (ADJ ? (pr < 2 ? wa[2 * pr] : wb[2 * pr - 4]) : wa[pr]) * mul;
+                            const float w2 = (ADJ ? (pr < 2 ? wa[2 * pr + 1] : wb[2 * pr - 3]) : wb[pr]) * mul;
+                            const float c = e ? t4[g].z : t4[g].x, sn = e ? t4[g].w : t4[g].y;
+                            r11[e] = w1 * c;
+                            r12[e] = -w2 * sn;
+                            r21[e] = w1 * sn;
+                            r22[e] = w2 * c;
+                        }
+                        m11[g] = f2_pack(r11[0], r11[1]);
+                        m12[g] = f2_pack(r12[0], r12[1]);
+                        m21[g] = f2_pack(r21[0], r21[1]);
+                        m22[g] = f2_pack(r22[0], r22[1]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < QU; ++i) {
+                    if (h0 + i * hpi >= hend) break;    // warp-uniform: no head left
+                    const int hh = h0 + i * hpi + hl;
+                    uint64_t x1[2], x2[2], y1[2], y2[2];
+                    raw[i].template get<ADJ>(x1, x2);
+                    float inv = 1.f;
                     if (nw) {
-                        y1[g] = f2_mul(y1[g], inv2);
-                        y2[g] = f2_mul(y2[g], inv2);
+                        const uint64_t q2 = f2_fma(x1[0], x1[0], f2_fma(x2[0], x2[0], f2_fma(x1[1], x1[1], f2_mul(x2[1], x2[1]))));
+                        float q, qb;
+                        f2_unpack(q2, q, qb);
+                        q += qb;
+                        if (LPH) {
+#pragma unroll
+                            for (int o = 1; o < LPH; o <<= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
+                        } else {                // up to 32 lanes of any count: to the group's first, and back
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1) {
+                                const float r = __shfl_down_sync(0xFFFFFFFFu, q, o);
+                                if (u + o < lph) q += r;
+                            }
+                            q = __shfl_sync(0xFFFFFFFFu, q, lane - u);
+                        }
+                        inv = rsqrtf(fmaf(q, p.inv_hd, p.eps));
                     }
+                    const uint64_t inv2 = f2_pack(inv, inv);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const uint64_t s1 = f2_mul(x1[g], m11[g]), s2 = f2_mul(x2[g], m22[g]);
+                        y1[g] = f2_fma(x2[g], m12[g], s1);
+                        y2[g] = f2_fma(x1[g], m21[g], s2);
+                        if (PART) {             // pairs that do not turn never see their neighbour
+                            float a0, a1, b0, b1, u0, u1, v0, v1;
+                            f2_unpack(y1[g], a0, a1);
+                            f2_unpack(y2[g], b0, b1);
+                            f2_unpack(s1, u0, u1);
+                            f2_unpack(s2, v0, v1);
+                            const bool t0 = p0 + 2 * g < p.pairs, t1 = p0 + 2 * g + 1 < p.pairs;
+                            y1[g] = f2_pack(t0 ? a0 : u0, t1 ? a1 : u1);
+                            y2[g] = f2_pack(t0 ? b0 : v0, t1 ? b1 : v1);
+                        }
+                        if (nw) {
+                            y1[g] = f2_mul(y1[g], inv2);
+                            y2[g] = f2_mul(y2[g], inv2);
+                        }
+                    }
+                    if (on && hh < hend) put_unit<ADJ>(dst + (hh * p.hd + c1), dst + (hh * p.hd + c2), y1, y2);
                 }
-                if (on && hh < ch.h1) put_unit<ADJ>(dst + (hh * p.hd + c1), dst + (hh * p.hd + c2), y1, y2);
             }
         }
     }
 }
 
-// Any even sections: the heads of an item pass through shared memory, STG
-// bytes at a time (16-byte loads and stores, single channels in between); lane
-// l turns pairs l, l + 32, ... of each head.
+// Any even sections: the heads of an item pass through shared memory, up to
+// ANY_STG bytes at a time (16-byte loads and stores, single channels in
+// between); lane l turns pairs l, l + 32, ... (NP of them) of each head, four
+// heads at once so that their chains of load, norm and rotation overlap.
 constexpr int ANY_STG = 4096;
 
-template <typename T>
-__global__ void __launch_bounds__(256) rope_any_kernel(const __grid_constant__ RopeParams p) {
+template <typename T, int NP>
+__global__ void __launch_bounds__(256, 4) rope_any_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int HU = NP == 4 ? 2 : 4;         // heads at once
     __shared__ __align__(16) uint8_t stage[8][ANY_STG];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     T *buf = reinterpret_cast<T *>(stage[warp]);
     constexpr int V = 16 / (int)sizeof(T);      // channels a 16-byte piece
     const int hb = ANY_STG / ((int)sizeof(T) * p.hd);   // heads a pass
-    int c1[4], c2[4], axis[4];
-    unsigned long long turn[4];
-    bool rot[4];
+    int c1[NP], c2[NP];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NP; ++i) {
         const int pr = lane + 32 * i;
-        rot[i] = pr < p.pairs;
         c1[i] = pr < p.hd / 2 ? p.c1[pr] : -1;
         c2[i] = pr < p.hd / 2 ? p.c2[pr] : -1;
-        turn[i] = rot[i] ? p.turn[pr] : 0ull;
-        axis[i] = rot[i] ? p.axis[pr] : 0;
     }
     for (unsigned item = blockIdx.x * 8 + warp; item < (unsigned)p.items; item += gridDim.x * 8) {
         const Chunk ch = chunk_of(p, item);
-        const T *src = static_cast<const T *>(p.src) + ch.row * p.lds + ch.off;
-        T *dst = static_cast<T *>(p.dst) + ch.row * p.ldd + ch.off;
+        float2 cs[NP];
         const int32_t *pos = p.pos + ch.row * p.ldp;
-        const float *nw = ch.isq ? p.qn : p.kn;
-        const float mul = ch.isq ? p.q_mul : 1.f;
-        float2 cs[4];
-        float w1[4], w2[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            cs[i] = turn_cs(pos[axis[i]], turn[i]);
-            w1[i] = w2[i] = 1.f;
-            if (nw && c1[i] >= 0) {
-                w1[i] = nw[c1[i]];
-                w2[i] = nw[c2[i]];
-            }
+        for (int i = 0; i < NP; ++i) {
+            const int pr = lane + 32 * i;
+            cs[i] = pr < p.pairs ? turn_cs(pos[p.axis[pr]], p.turn[pr]) : make_float2(1.f, 0.f);
         }
-        for (int h0 = ch.h0; h0 < ch.h1; h0 += hb) {
-            const int hn = ch.h1 - h0 < hb ? ch.h1 - h0 : hb;
-            const int n16 = hn * p.hd / V;
-            const uint4 *s16 = reinterpret_cast<const uint4 *>(src + (long long)h0 * p.hd);
-            uint4 *d16 = reinterpret_cast<uint4 *>(dst + (long long)h0 * p.hd);
-            uint4 *b16 = reinterpret_cast<uint4 *>(buf);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            int hbeg, hend;
+            part_heads(p, ch, part, hbeg, hend);
+            const int off = part ? p.k_off : p.q_off;
+            const T *src = static_cast<const T *>(p.src) + ch.row * p.lds + off;
+            T *dst = static_cast<T *>(p.dst) + ch.row * p.ldd + off;
+            const float *nw = part ? p.kn : p.qn;
+            const float mul = part ? 1.f : p.q_mul;
+            float w1[NP], w2[NP];
 #pragma unroll
-            for (int j = 0; j < ANY_STG / 512; ++j)
-                if (lane + 32 * j < n16) b16[lane + 32 * j] = s16[lane + 32 * j];
-            __syncwarp();
-            for (int h = 0; h < hn; ++h) {
-                T *x = buf + h * p.hd;
-                float x1[4], x2[4], q = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x1[i] = x2[i] = 0.f;
-                    if (c1[i] >= 0) {
-                        x1[i] = (float)x[c1[i]];
-                        x2[i] = (float)x[c2[i]];
-                    }
-                    q = fmaf(x1[i], x1[i], fmaf(x2[i], x2[i], q));
-                }
-                const float inv = nw ? rsqrtf(fmaf(warp_sum(q), p.inv_hd, p.eps)) : 1.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (c1[i] < 0) continue;
-                    float a = x1[i], b = x2[i];
-                    if (nw) {
-                        a *= inv * w1[i];
-                        b *= inv * w2[i];
-                    }
-                    if (rot[i]) {
-                        const float y1 = fmaf(a, cs[i].x, -b * cs[i].y);
-                        b = fmaf(b, cs[i].x, a * cs[i].y);
-                        a = y1;
-                    }
-                    x[c1[i]] = (T)(a * mul);
-                    x[c2[i]] = (T)(b * mul);
-                }
+            for (int i = 0; i < NP; ++i) {
+                w1[i] = c1[i] >= 0 && nw ? nw[c1[i]] * mul : mul;
+                w2[i] = c1[i] >= 0 && nw ? nw[c2[i]] * mul : mul;
             }
-            __syncwarp();
+            for (int h0 = hbeg; h0 < hend; h0 += hb) {
+                const int hn = hend - h0 < hb ? hend - h0 : hb;
+                const int n16 = hn * p.hd / V;
+                const uint4 *s16 = reinterpret_cast<const uint4 *>(src + (long long)h0 * p.hd);
+                uint4 *d16 = reinterpret_cast<uint4 *>(dst + (long long)h0 * p.hd);
+                uint4 *b16 = reinterpret_cast<uint4 *>(buf);
 #pragma unroll
-            for (int j = 0; j < ANY_STG / 512; ++j)
-                if (lane + 32 * j < n16) d16[lane + 32 * j] = b16[lane + 32 * j];
-            __syncwarp();                       // before the next pass overwrites the stage
+                for (int j = 0; j < ANY_STG / 512; ++j)
+                    if (lane + 32 * j < n16) b16[lane + 32 * j] = s16[lane + 32 * j];
+                __syncwarp();
+                for (int h = 0; h < hn; h += HU) {
+                    T *x = buf + h * p.hd;
+                    float x1[HU][NP], x2[HU][NP], inv[HU];
+#pragma unroll
+                    for (int k = 0; k < HU; ++k) {
+                        const bool have = h + k < hn;   // warp-uniform
+                        float q = 0.f;
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) {
+                            x1[k][i] = have && c1[i] >= 0 ? (float)x[k * p.hd + c1[i]] : 0.f;
+                            x2[k][i] = have && c1[i] >= 0 ? (float)x[k * p.hd + c2[i]] : 0.f;
+                            q = fmaf(x1[k][i], x1[k][i], fmaf(x2[k][i], x2[k][i], q));
+                        }
+                        inv[k] = q;
+                    }
+                    if (nw) {
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                            for (int k = 0; k < HU; ++k) inv[k] += __shfl_xor_sync(0xFFFFFFFFu, inv[k], o);
+#pragma unroll
+                        for (int k = 0; k < HU; ++k) inv[k] = rsqrtf(fmaf(inv[k], p.inv_hd, p.eps));
+                    }
+#pragma unroll
+                    for (int k = 0; k < HU; ++k) {
+                        if (h + k >= hn) break;
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) {
+                            if (c1[i] < 0) continue;
+                            float a = x1[k][i] * w1[i], b = x2[k][i] * w2[i];
+                            if (nw) {
+                                a *= inv[k];
+                                b *= inv[k];
+                            }
+                            if (lane + 32 * i < p.pairs) {
+                                const float y1 = fmaf(a, cs[i].x, -b * cs[i].y);
+                                b = fmaf(b, cs[i].x, a * cs[i].y);
+                                a = y1;
+                            }
+                            x[k * p.hd + c1[i]] = (T)a;
+                            x[k * p.hd + c2[i]] = (T)b;
+                        }
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < ANY_STG / 512; ++j)
+                    if (lane + 32 * j < n16) d16[lane + 32 * j] = b16[lane + 32 * j];
+                __syncwarp();                   // before the next pass overwrites the stage
+            }
         }
     }
 }
@@ -354,21 +408,21 @@ te_status launch(RopeParams &p, int rows, int hpi, cudaStream_t s) {
         resident[dev] = sms * per;
     }
     const long long most = resident[dev], warps = 8 * most;
-    // A row's q heads and k heads are an item each, or, with few rows, cut into
-    // runs of whole load slots until every resident warp has an item.  (With
-    // many rows, cuts that even out the last round of the warps cost more in
-    // repeated sines and cosines than they gain: 47.7 -> 49.2 us at 8448 rows.)
-    long long cuts = warps / (2ll * rows);
+    // A row's slots (q heads, then k heads, hpi a slot) are cut into items of
+    // about 16 slots, whose sines and cosines are then worth their while; with
+    // few rows further, until every resident warp has an item.  (Cuts that even
+    // out the last round of the warps cost more in repeated sines and cosines
+    // than they gain: 47.7 -> 49.2 us at 8448 rows of 60 heads.)
+    p.hpi = hpi;
+    p.sq = (p.nq + hpi - 1) / hpi;
+    p.slots = p.sq + (p.nkv + hpi - 1) / hpi;
+    long long cuts = (p.slots + 8) / 16;
+    if (cuts * rows < warps) cuts = warps / rows;
     if (cuts < 1) cuts = 1;
-    auto cut = [&](int n, int &chunks, int &heads) {
-        const int slots = (n + hpi - 1) / hpi;
-        const int c = cuts < slots ? (int)cuts : slots;
-        heads = c ? (slots + c - 1) / c * hpi : hpi;
-        chunks = (n + heads - 1) / heads;
-    };
-    cut(p.nq, p.cq, p.hq);
-    cut(p.nkv, p.ck, p.hk);
-    const long long items = (long long)rows * (p.cq + p.ck);
+    if (cuts > p.slots) cuts = p.slots;
+    p.per = (int)((p.slots + cuts - 1) / cuts);
+    p.cuts = (p.slots + p.per - 1) / p.per;
+    const long long items = (long long)rows * p.cuts;
     if (items > 0x7FFFFFFFll) return fail(TE_ESHAPE, "qk_rope_axes: rows=%d too many", rows);
     p.items = (int)items;
     const long long need = (items + 7) / 8;
@@ -379,9 +433,14 @@ te_status launch(RopeParams &p, int rows, int hpi, cudaStream_t s) {
 
 template <typename T, bool ADJ, bool PART>
 te_status launch_vec(RopeParams &p, int rows, cudaStream_t s) {
-    if (p.hd <= 64) return launch<rope_vec_kernel<T, ADJ, PART, 8>>(p, rows, 4, s);
-    if (p.hd <= 128) return launch<rope_vec_kernel<T, ADJ, PART, 16>>(p, rows, 2, s);
-    return launch<rope_vec_kernel<T, ADJ, PART, 32>>(p, rows, 1, s);
+    // lanes a head: a power of two where as many heads fit the warp as without
+    // the rounding (its norm takes half the instructions), else hd / 8
+    const int nu = p.hd / 8;
+    if (nu == 4) return launch<rope_vec_kernel<T, ADJ, PART, 4>>(p, rows, 8, s);
+    if (nu == 7 || nu == 8) return launch<rope_vec_kernel<T, ADJ, PART, 8>>(p, rows, 4, s);
+    if (nu >= 11 && nu <= 16) return launch<rope_vec_kernel<T, ADJ, PART, 16>>(p, rows, 2, s);
+    if (nu >= 17) return launch<rope_vec_kernel<T, ADJ, PART, 32>>(p, rows, 1, s);
+    return launch<rope_vec_kernel<T, ADJ, PART, 0>>(p, rows, 32 / nu, s);
 }
 
 template <typename T>
@@ -427,7 +486,8 @@ te_status run(RopeParams &p, const te_rope_axes &pl, int rows, cudaStream_t s) {
         p.c1[pr] = (uint8_t)(2 * pr);
         p.c2[pr] = (uint8_t)(2 * pr + 1);
     }
-    return launch<rope_any_kernel<T>>(p, rows, 1, s);
+    if (hd <= 64) return launch<rope_any_kernel<T, 1>>(p, rows, 1, s);
+    return hd <= 128 ? launch<rope_any_kernel<T, 2>>(p, rows, 1, s) : launch<rope_any_kernel<T, 4>>(p, rows, 1, s);
 }
 
 // A plan whose fields the kernels may index by.
