@@ -539,10 +539,11 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
 // and the activation takes the hardware tanh (error below that rounding).
 // 8-bit activations (ts: the block's 32 token scales in shared memory): g and
 // u stay f32 and the activation is exact to f32 rounding, so that the output
-// is rounded once.
-template <bool I8, int ACT>
+// is rounded once.  act: a constant where the caller keeps a copy of the code
+// an activation, a variable where one copy that selects is enough.
+template <bool I8>
 __device__ __forceinline__ void gate_block(const uint32_t (&v)[32], float sc, float bi, const float *ts, bool upper,
-                                           float (&yv)[16]) {
+                                           int act, float (&yv)[16]) {
     const uint64_t sc2 = f2_pack(sc, sc), bi2 = f2_pack(bi, bi), half2 = f2_pack(0.5f, 0.5f);
     float gv[16], uv[16];
     float4 ta, tb;
@@ -574,17 +575,15 @@ __device__ __forceinline__ void gate_block(const uint32_t (&v)[32], float sc, fl
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
         if constexpr (I8) {
-            yv[j] = apply_act(gv[j], ACT) * uv[j];
-            yv[j + 1] = apply_act(gv[j + 1], ACT) * uv[j + 1];
+            yv[j] = apply_act(gv[j], act) * uv[j];
+            yv[j + 1] = apply_act(gv[j + 1], act) * uv[j + 1];
         } else {
             const uint64_t g2 = f2_pack(gv[j], gv[j + 1]);
             // GELU-tanh: z = g (0.79788456 + 0.035677408 g^2); SiLU: z = g / 2
-            uint64_t z2;
-            if constexpr (ACT == TE_ACT_GELU_TANH)
-                z2 = f2_mul(g2, f2_fma(f2_pack(0.035677408f, 0.035677408f), f2_mul(g2, g2),
-                                       f2_pack(0.79788456f, 0.79788456f)));
-            else
-                z2 = f2_mul(half2, g2);
+            const uint64_t z2 = act == TE_ACT_GELU_TANH
+                                    ? f2_mul(g2, f2_fma(f2_pack(0.035677408f, 0.035677408f), f2_mul(g2, g2),
+                                                        f2_pack(0.79788456f, 0.79788456f)))
+                                    : f2_mul(half2, g2);
             float z0, z1;
             f2_unpack(z2, z0, z1);
             const uint64_t h2 = f2_mul(half2, g2);

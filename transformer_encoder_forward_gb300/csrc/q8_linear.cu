@@ -439,10 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 tmem_ld32(tbase + tl + acol + 32 * c, v);
                 tmem_wait_ld();
                 float yv[16];
-                if (act == TE_ACT_GELU_TANH)
-                    gate_block<I8, TE_ACT_GELU_TANH>(v, sc, bi, tsw + 32 * c, upper, yv);
-                else
-                    gate_block<I8, TE_ACT_SILU>(v, sc, bi, tsw + 32 * c, upper, yv);
+                gate_block<I8>(v, sc, bi, tsw + 32 * c, upper, act, yv);
                 const uint32_t so = hstg + (uint32_t)(((gslot + c - c0) & 3) * 1024);
                 uint16_t *ostg_h = reinterpret_cast<uint16_t *>(smem + (so - sb));
 #pragma unroll
@@ -510,10 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const int tb = t0 + 32 * c;
             if constexpr (GATED) {
                 float yv[16];
-                if (it.act == TE_ACT_GELU_TANH)
-                    gate_block<I8, TE_ACT_GELU_TANH>(v, sc, bi, tsw + 32 * c, upper, yv);
-                else
-                    gate_block<I8, TE_ACT_SILU>(v, sc, bi, tsw + 32 * c, upper, yv);
+                gate_block<I8>(v, sc, bi, tsw + 32 * c, upper, it.act, yv);
                 // the store two blocks back, which used this slot, has read it
                 if (lane == 0) bulk_wait_read_n<1>();
                 __syncwarp();
@@ -1098,9 +1092,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                             tmem_wait_ld();
                             float yv[16];
                             if (act == TE_ACT_GELU_TANH)
-                                gate_block<I8, TE_ACT_GELU_TANH>(v, sc, bi, tsw + 32 * c, upper, yv);
+                                gate_block<I8>(v, sc, bi, tsw + 32 * c, upper, TE_ACT_GELU_TANH, yv);
                             else
-                                gate_block<I8, TE_ACT_SILU>(v, sc, bi, tsw + 32 * c, upper, yv);
+                                gate_block<I8>(v, sc, bi, tsw + 32 * c, upper, TE_ACT_SILU, yv);
                             const uint32_t so = stg + (uint32_t)(((gslot + c) & (2 * GBSZ - 1)) * 1024);
                             uint16_t *ostg_h = reinterpret_cast<uint16_t *>(smem + (so - sb));
 #pragma unroll
