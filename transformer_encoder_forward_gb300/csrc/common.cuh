@@ -528,6 +528,60 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
            | ((uint32_t)(M >> 4) << 24);          // M / 16
 }
 
+// ------------------------------------------- launches that follow closely
+//
+// A kernel launched by launch_close may start once the CTAs of the stream's
+// previous kernel have all ended or called next_go: its start (placement,
+// barriers, TMEM) then overlaps the end of the other.  It has to call
+// prior_wait, in every thread, before it touches global memory: that returns
+// when the previous kernel has ended and all of its writes are to be seen, and
+// since that one waited too, everything before it has ended as well.  So:
+//   * next_go comes after the kernel's own prior_wait and after its TMEM
+//     allocation (a later kernel's allocation must not be waited for);
+//   * a kernel whose CTAs work through many units calls it at its last one (at
+//     its start, in the kernel with resident weights, 16238 tokens gated 2 x 2048
+//     took 70 us instead of 63), and the large pipeline not at all (a widening
+//     pass waiting beside its last units: 12297 x 8768 gated 2 x 128 98 -> 108 us);
+//   * nothing is read through the read-only path (__ldg, const __restrict__),
+//     whose loads the compiler may move above the wait.
+// The calls of a block follow one another at 1 to 3 us less each: 1023 rows of 16
+// heads of 72 rotated 6.2 -> 3.7 us, 101 x 768 x 2304 8.2 -> 5.2, quantisation and
+// product 16238 x 512 x 512 24.7 -> 20.4, norm, widening and product 2112 x 3840 x
+// 11520 135 -> 130.
+__device__ __forceinline__ void prior_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_close(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+// int8 x4 -> two f16x2 words, exactly.  u = q + 128 as the low byte of the f16
+// pattern 0x64xx reads 1024 + q + 128; one paired subtraction of 1152 leaves
+// q, which needs 8 of f16's 11 significant bits.
+__device__ __forceinline__ void widen4_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // --------------------------------------------- draining an accumulator block
 
 // One 32-token block of the gated form, in a draining warp whose lanes 0-15

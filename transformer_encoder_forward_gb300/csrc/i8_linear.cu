@@ -33,18 +33,6 @@ struct I8Params {
     I8Item it[MAXZ];
 };
 
-// int8 x4 -> two f16x2 words, exactly: q + 128 as the low byte of the f16
-// pattern 0x64xx reads 1024 + q + 128; subtracting 1152 leaves q.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-}
-
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -97,7 +85,7 @@ __global__ void __launch_bounds__(256) i8_small_kernel(const __grid_constant__ I
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 xr[n][h] = in && g + 8 * n < p.m
-                               ? __ldg(reinterpret_cast<const uint4 *>(xp + (long long)(8 * n) * p.ldx + k0 + 64 * h))
+                               ? *reinterpret_cast<const uint4 *>(xp + (long long)(8 * n) * p.ldx + k0 + 64 * h)
                                : make_uint4(0u, 0u, 0u, 0u);
         }
     };
@@ -110,6 +98,8 @@ __global__ void __launch_bounds__(256) i8_small_kernel(const __grid_constant__ I
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[s][i][n][e] = 0.f;
+    prior_wait();
+    next_go();
     const int step = 128 * ks;
 #pragma unroll
     for (int d = 0; d < D; ++d) load(w[d], x[d], 128 * warp + d * step);
@@ -123,13 +113,13 @@ __global__ void __launch_bounds__(256) i8_small_kernel(const __grid_constant__ I
                     uint32_t a[MT][4];
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
-                        widen4(word(w[d][i][0][h], j), a[i][0], a[i][2]);
-                        widen4(word(w[d][i][1][h], j), a[i][1], a[i][3]);
+                        widen4_f16(word(w[d][i][0][h], j), a[i][0], a[i][2]);
+                        widen4_f16(word(w[d][i][1][h], j), a[i][1], a[i][3]);
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         uint32_t b0, b1;
-                        widen4(word(x[d][n][h], j), b0, b1);
+                        widen4_f16(word(x[d][n][h], j), b0, b1);
 #pragma unroll
                         for (int i = 0; i < MT; ++i) mma_16x8x16(acc[j % AS][i][n], a[i], b0, b1);
                     }
@@ -197,8 +187,8 @@ te_status small_launch(I8Params &p, cudaStream_t s) {
     }
     int ks = 1;
     while (ks < 8 && (long long)groups * ks < SMS * 16 && 128 * ks < p.k) ks *= 2;
-    i8_small_kernel<NT, MT, GATED, D><<<groups, 32 * ks, ks * MT * 16 * NT * 8 * 4, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_close(i8_small_kernel<NT, MT, GATED, D>, dim3(groups), 32 * ks,
+                                       ks * MT * 16 * NT * 8 * 4, s, 1, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
 }
 // --------------------------------------------------- a middling token count
@@ -313,6 +303,8 @@ __global__ void __launch_bounds__(Mid<N>::THREADS) i8_mid_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
+    prior_wait();
+    next_go();
     bool ok = true;
 
     if (warp == 0) {
@@ -368,10 +360,10 @@ __global__ void __launch_bounds__(Mid<N>::THREADS) i8_mid_kernel(const __grid_co
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(st + row * 128 + (((4 * h + c) ^ (row & 7)) << 4));
-                    widen4(v.x, r[8 * c + 0], r[8 * c + 1]);
-                    widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
-                    widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
-                    widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    widen4_f16(v.x, r[8 * c + 0], r[8 * c + 1]);
+                    widen4_f16(v.y, r[8 * c + 2], r[8 * c + 3]);
+                    widen4_f16(v.z, r[8 * c + 4], r[8 * c + 5]);
+                    widen4_f16(v.w, r[8 * c + 6], r[8 * c + 7]);
                 }
                 tmem_st32(tbase + ((uint32_t)(32 * q) << 16) + N + 64 * a + 32 * h, r);
             }
@@ -384,10 +376,10 @@ __global__ void __launch_bounds__(Mid<N>::THREADS) i8_mid_kernel(const __grid_co
                 const int xr = id >> 3, c = id & 7;
                 const uint4 v = *reinterpret_cast<const uint4 *>(st + L::WBYTES + xr * 128 + ((c ^ (xr & 7)) << 4));
                 uint4 lo, hi;
-                widen4(v.x, lo.x, lo.y);
-                widen4(v.y, lo.z, lo.w);
-                widen4(v.z, hi.x, hi.y);
-                widen4(v.w, hi.z, hi.w);
+                widen4_f16(v.x, lo.x, lo.y);
+                widen4_f16(v.y, lo.z, lo.w);
+                widen4_f16(v.z, hi.x, hi.y);
+                widen4_f16(v.w, hi.z, hi.w);
                 uint8_t *box = smem + L::B_OFF + a * 2 * L::BBOX + (c >> 2) * L::BBOX + xr * 128;
                 const int p0 = 2 * (c & 3), first = c >> 2;
                 *reinterpret_cast<uint4 *>(box + (((p0 + first) ^ (xr & 7)) << 4)) = first ? hi : lo;
@@ -594,19 +586,7 @@ te_status mid_launch(const I8Params &q, int S, cudaStream_t s) {
     p.z = q.z;
     if ((st = gemm_error_word(&p.err)) != TE_OK) return st;
     const int ttiles = (q.m + N - 1) / N;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(tiles * S, ttiles, 1);
-    cfg.blockDim = dim3(Mid<N>::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = S;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, i8_mid_kernel<N, GATED>, p);
+    const cudaError_t e = launch_close(i8_mid_kernel<N, GATED>, dim3(tiles * S, ttiles), Mid<N>::THREADS, smem, s, S, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
 }
 template <bool GATED>
@@ -709,6 +689,7 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
+    prior_wait();
     bool ok = true;
     // unit u is (feature tile ft, token tile tt); it brings new weights where a
     // run or a feature tile begins
@@ -749,6 +730,7 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
                     }
                 }
             }
+            if (u + 1 == u1) next_go();
             for (int kb = 0; kb < nkb && ok; ++kb, ++ci) {
                 const int s = slot();
                 if (ok) tma_load_2d_e(sb + s * L::CHUNK, &p.tx, bar_full + 8 * s, kb * 128, tt * 128, e);
@@ -827,10 +809,10 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint4 lo, hi;
-                        widen4(v[j].x, lo.x, lo.y);
-                        widen4(v[j].y, lo.z, lo.w);
-                        widen4(v[j].z, hi.x, hi.y);
-                        widen4(v[j].w, hi.z, hi.w);
+                        widen4_f16(v[j].x, lo.x, lo.y);
+                        widen4_f16(v[j].y, lo.z, lo.w);
+                        widen4_f16(v[j].z, hi.x, hi.y);
+                        widen4_f16(v[j].w, hi.z, hi.w);
                         *reinterpret_cast<uint4 *>(dst + 512 * j + (wd0 ^ (64 * (j & 1)))) = whi ? hi : lo;
                         *reinterpret_cast<uint4 *>(dst + 512 * j + (wd1 ^ (64 * (j & 1)))) = whi ? lo : hi;
                     }
@@ -850,10 +832,10 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
                 for (int c = 0; c < 4; ++c) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(smem + s * L::CHUNK + row * 128 +
                                                                      (((4 * h + c) ^ (row & 7)) << 4));
-                    widen4(v.x, r[8 * c + 0], r[8 * c + 1]);
-                    widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
-                    widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
-                    widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    widen4_f16(v.x, r[8 * c + 0], r[8 * c + 1]);
+                    widen4_f16(v.y, r[8 * c + 2], r[8 * c + 3]);
+                    widen4_f16(v.z, r[8 * c + 4], r[8 * c + 5]);
+                    widen4_f16(v.w, r[8 * c + 6], r[8 * c + 7]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_empty + 8 * s);
@@ -1070,25 +1052,26 @@ te_status res_launch(const I8Params &q, cudaStream_t s) {
     const long long units = (long long)p.ttiles * tiles;
     if (units > 0x7FFFFFFFll) return fail(TE_ESHAPE, "i8_linear: too many tiles");
     p.units = (int)units;
-    i8_res_kernel<GATED><<<p.units < SMS ? p.units : SMS, Res::THREADS, smem, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_close(i8_res_kernel<GATED>, dim3(p.units < SMS ? p.units : SMS), Res::THREADS, smem, s, 1, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
 }
 
 // x int8 [m, k] (rows ldx apart) widened to f16 [m, k], exactly: 16 values a
 // thread, 16 bytes in and 32 out.
-__global__ void __launch_bounds__(256) widen_kernel(const int8_t *__restrict__ x, long long ldx,
-                                                    __half *__restrict__ y, long long total, int chunks) {
+__global__ void __launch_bounds__(256) widen_kernel(const int8_t *x, long long ldx, __half *y,
+                                                    long long total, int chunks) {
+    prior_wait();
+    next_go();
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= total) return;
     const long long r = i / chunks;
     const int c = (int)(i - r * chunks);
     const uint4 v = *reinterpret_cast<const uint4 *>(x + r * ldx + 16 * c);
     uint32_t out[8];
-    widen4(v.x, out[0], out[1]);
-    widen4(v.y, out[2], out[3]);
-    widen4(v.z, out[4], out[5]);
-    widen4(v.w, out[6], out[7]);
+    widen4_f16(v.x, out[0], out[1]);
+    widen4_f16(v.y, out[2], out[3]);
+    widen4_f16(v.z, out[4], out[5]);
+    widen4_f16(v.w, out[6], out[7]);
     uint4 *dst = reinterpret_cast<uint4 *>(y + 16 * i);
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
     dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
@@ -1098,8 +1081,8 @@ te_status widen(const int8_t *x, int64_t ldx, void *y, int m, int k, cudaStream_
     const int chunks = k / 16;
     const long long total = (long long)m * chunks, blocks = (total + 255) / 256;
     if (blocks > 0x7FFFFFFFll) return fail(TE_ESHAPE, "i8_linear: m * k too large");
-    widen_kernel<<<(unsigned)blocks, 256, 0, s>>>(x, ldx, static_cast<__half *>(y), total, chunks);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_close(widen_kernel, dim3((unsigned)blocks), 256, 0, s, 1, x, ldx,
+                                       static_cast<__half *>(y), total, chunks);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear: widen launch");
 }
 
@@ -1107,17 +1090,22 @@ constexpr int MAX_K = 65536;
 
 // Which kernel takes a call.  The measured device times (us, back to back in a
 // graph, weights not in L2; n the output features in all):
-//                      small    mid   large (with its widening pass)
-//   m = 8   k 3840 n 11520     10.5   14.5
-//   m = 16  k 512  n 1536       2.9    4.6    7.9
-//   m = 16  k 3840 n 3840       7.7    9.2   18.2
-//   m = 16  k 10240 n 3840     15.6   12.7   35.9
-//   m = 32  k 768  n 2304       4.6    5.6    8.8
-//   m = 32  k 3840 n 3840      11.3   10.2   18.4
-//   m = 64  k 3840 n 11520            23.9   19.6
-//   m = 128 k 3840 n 3840             14.7   19.7
-//   m = 128 k 10240 n 3840            22.2   38.5
-//   m = 384 k 3840 n 11520            54.5   32.7
+//                      small    mid   resident   large (with its widening pass)
+//   m = 8   k 3840 n 11520     10.9   14.9
+//   m = 16  k 512  n 1536       2.4    3.6    6.3    6.7
+//   m = 16  k 3840 n 3840       7.4    7.9          16.2
+//   m = 16  k 10240 n 3840     15.3   12.7          33.9
+//   m = 32  k 768  n 2304       3.9    4.1           7.2
+//   m = 32  k 3840 n 3840      10.6    8.5          16.3
+//   m = 64  k 3840 n 11520            22.3          17.8
+//   m = 128 k 512  n 1536              4.6    6.7    8.0
+//   m = 128 k 3840 n 3840             13.5          17.5
+//   m = 128 k 10240 n 3840            21.1          35.7
+//   m = 384 k 3840 n 11520            53.0          32.1
+//   m = 600 k 512  n 1536              6.5    6.8    8.2
+//   m = 1000 k 512 n 1536              9.7    7.0    8.7
+//   m = 1000 k 768 n 2304             12.0          11.3
+//   m = 300 k 512  gated 2 x 2048      8.9    7.2    8.0
 // Small: to 8 tokens; to 16 (32) tokens while the weights are under 16 M (4 M)
 // values, beyond which its warps' widening of the tokens costs more than the
 // TMEM pipeline's start.  Else to 1024 tokens mid where its modelled time (see
@@ -1125,16 +1113,17 @@ constexpr int MAX_K = 65536;
 // kernel with resident weights, 5.5 us and 1 + 0.45 us a stage for each round
 // of its CTAs; beyond, large, 7 us (the widening pass and a second launch) and
 // 0.39 us a stage of each wave of 256 x 128 units (fits of what was measured,
-// to about 15 %).  Resident against large at 16238 tokens (us): k 512, n 1536
-// bf16 28.8 and 35.7; n 512 f32 15.0 and 22.3; gated 2 x 2048 64.5 and 71.6;
-// k 64, n 512 f32 11.6 and 19.7.
+// to about 20 %; of the rows above and ten others, none is given to a slower
+// kernel).  Resident against large at 16238 tokens (us): k 512, n 1536 bf16 27.7
+// and 34.2; n 512 f32 13.8 and 21.3; gated 2 x 2048 63.3 and 68.7; k 64, n 512
+// f32 10.2 and 19.0.
 enum Path { SMALL, MID, RES, LARGE };
 template <bool GATED>
 te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
     long long total = 0;
     int tiles = 0;                              // 128 weight rows (gated: 64 gate and 64 up)
     for (int i = 0; i < p.z; ++i) {
-        total += GATED ? 2 * p.it[i].n : p.it[i].n;
+        total += GATED ? 2ll * p.it[i].n : p.it[i].n;
         tiles += GATED ? (p.it[i].n + 63) / 64 : (p.it[i].n + 127) / 128;
     }
     path = SMALL;
@@ -1190,9 +1179,11 @@ te_status check_ws(const char *what, const void *ws, size_t have, size_t need) {
 
 using namespace tefwd;
 
+// the f16 activation of a call that widens it beforehand, whatever n
+static size_t workspace_of(int32_t m, int32_t k) { return m <= 8 ? 0 : ((size_t)m * k * 2 + 255) & ~(size_t)255; }
+
 extern "C" size_t te_i8_workspace(int32_t m, int32_t k, int32_t n) {
-    if (m <= 8 || k < 64 || k > MAX_K || k % 64 || n < 32) return 0;
-    return ((size_t)m * k * 2 + 255) & ~(size_t)255;
+    return k < 64 || k > MAX_K || k % 64 || n < 32 ? 0 : workspace_of(m, k);
 }
 
 extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_scale, int32_t m,
@@ -1244,7 +1235,7 @@ extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_s
         n += src.w.n;
     }
     if (n > 0x7FFFFFFFll) return fail(TE_ESHAPE, "i8_linear: too many output features");
-    if ((st = check_ws("i8_linear", workspace, ws_bytes, te_i8_workspace(m, k, (int32_t)n))) != TE_OK) return st;
+    if ((st = check_ws("i8_linear", workspace, ws_bytes, workspace_of(m, k))) != TE_OK) return st;
     if (m == 0) return TE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     Path path;
@@ -1275,7 +1266,7 @@ extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const floa
     if (f > 0x3FFFFFFF) return fail(TE_ESHAPE, "i8_gated_linear: too many output features");
     if (ldm < f || ldm % 8) return fail(TE_ESHAPE, "i8_gated_linear: ldm=%lld (>= f, multiple of 8)", (long long)ldm);
     if (!aligned16(out)) return fail(TE_EALIGN, "i8_gated_linear: out not 16-byte aligned");
-    if ((st = check_ws("i8_gated_linear", workspace, ws_bytes, te_i8_workspace(m, k, 2 * f))) != TE_OK) return st;
+    if ((st = check_ws("i8_gated_linear", workspace, ws_bytes, workspace_of(m, k))) != TE_OK) return st;
     if (m == 0) return TE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     I8Params p;

@@ -181,19 +181,6 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
     hi = __byte_perm(__float_as_uint(f2), __float_as_uint(f3), 0x7632);
 }
 
-// int8 x4 -> two f16x2 words, exactly.  u = q + 128 as the low byte of the f16
-// pattern 0x64xx reads 1024 + q + 128; one paired subtraction of 1152 leaves
-// q, which needs 8 of f16's 11 significant bits.
-__device__ __forceinline__ void widen4_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // As widen4, value e multiplied by its own factor c[e] (the q8_2f column
 // field) and rounded once to bf16.
 __device__ __forceinline__ void widen4_col(uint32_t w, float4 c, uint32_t &lo, uint32_t &hi) {
@@ -366,6 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     cluster_sync();            // both CTAs' barriers exist before any remote arrival
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
+    if constexpr (I8) prior_wait();
     bool ok = s_skip == 0;
     const int nunits = ok ? p.nunits : 0;
     // the leader's copies of the pair-wide barriers, as cluster addresses
@@ -1391,8 +1379,12 @@ te_status launch(Params &p, int ftiles, cudaStream_t stream) {
     const long long tg = p.res ? p.ttiles : XGROUP_BYTES / xtile;
     p.tgroup = tg < 1 ? 1 : (tg > p.ttiles ? p.ttiles : (int)tg);
     const int clusters = p.nunits < max_clusters[dev] ? p.nunits : max_clusters[dev];
-    q8_gemm_kernel<BN, GATED, TPA, I8><<<2 * clusters, NTHREADS, smem, stream>>>(p);
-    e = cudaGetLastError();
+    if constexpr (I8) {
+        e = launch_close(q8_gemm_kernel<BN, GATED, TPA, I8>, dim3(2 * clusters), NTHREADS, smem, stream, 1, p);
+    } else {
+        q8_gemm_kernel<BN, GATED, TPA, I8><<<2 * clusters, NTHREADS, smem, stream>>>(p);
+        e = cudaGetLastError();
+    }
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "q8_linear launch");
 }
 

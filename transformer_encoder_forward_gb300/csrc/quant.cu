@@ -45,8 +45,8 @@ template <> struct Raw8<__nv_bfloat16> {
 };
 // the per-feature vectors: shared by all rows, kept in cache
 __device__ __forceinline__ void load8_vec(const float *p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    const float4 b = reinterpret_cast<const float4 *>(p)[1];
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
@@ -122,9 +122,10 @@ __device__ __forceinline__ float2 row_both(float x, uint32_t y, float *red, int 
 // row a CTA without the loop 35 us).
 template <typename Tin, int NV, int WPR, bool NORM>
 __global__ void __launch_bounds__(256, NV == 8 ? 2 : (NV == 4 || (NV == 2 && WPR == 1) ? 3 : 4))
-    quant_kernel(const Tin *__restrict__ x, long long ldx, const float *__restrict__ w,
-                 const float *__restrict__ b, const float *__restrict__ ms, int kind, float eps, float pre,
-                 int8_t *__restrict__ q, long long ldq, float *__restrict__ scale, int t, int d) {
+    quant_kernel(const Tin *x, long long ldx, const float *w,
+                 const float *b, const float *ms, int kind, float eps, float pre,
+                 int8_t *q, long long ldq, float *scale, int t, int d) {
+    prior_wait();
     constexpr int TPR = 32 * WPR, RPC = 8 / WPR;
     __shared__ float red[2][8 / WPR][2 * WPR];
     const int slot = threadIdx.x / TPR, tid = threadIdx.x % TPR;
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(256, NV == 8 ? 2 : (NV == 4 || (NV == 2 && WPR
         for (int i = 0; i < NV; ++i) nx[i].get(v[i]);
         const long long after = row + (long long)gridDim.x * RPC;
         if (after < t) fetch(after);
+        else next_go();
         float top = 0.f, inv = 1.f;
         uint32_t mx;
         if (NORM && pre != 1.f) {
@@ -271,9 +273,8 @@ te_status go(const void *x, int64_t ldx, const float *w, const float *b, const f
         resident[dev] = sms * per;
     }
     const long long need = ((long long)t + RPC - 1) / RPC;
-    KERN<<<(unsigned)(need < resident[dev] ? need : resident[dev]), 256, 0, s>>>(
-        static_cast<const Tin *>(x), ldx, w, b, ms, kind, eps, pre, q, ldq, scale, t, d);
-    e = cudaGetLastError();
+    e = launch_close(KERN, dim3((unsigned)(need < resident[dev] ? need : resident[dev])), 256, 0, s, 1,
+                     static_cast<const Tin *>(x), ldx, w, b, ms, kind, eps, pre, q, ldq, scale, t, d);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "quant launch");
 }
 

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_vec_kernel(c
         for (int i = threadIdx.x; i < 8 * (TE_ROPE_MAX_PAIRS + 4); i += 256) (&rows_cs[0][0])[i] = make_float2(1.f, 0.f);
     }
     __syncthreads();
+    prior_wait();
     const int lane = threadIdx.x & 31;
     float2 *cs = rows_cs[threadIdx.x >> 5];
     const int lph = LPH ? LPH : p.hd / 8, hpi = LPH ? 32 / LPH : p.hpi;
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_vec_kernel(c
     const int uu = on ? u : 0;
     const int c1 = p.c1[uu], c2 = p.c2[uu], p0 = p.p0[uu];
     for (unsigned item = blockIdx.x * 8 + (threadIdx.x >> 5); item < (unsigned)p.items; item += gridDim.x * 8) {
+        if (item + gridDim.x * 8 >= (unsigned)p.items) next_go();
         const Chunk ch = chunk_of(p, item);
         bool turned = false;                    // the row's cosines and sines are there
 #pragma unroll 1
@@ -294,6 +296,7 @@ __global__ void __launch_bounds__(256, 4) rope_any_kernel(const __grid_constant_
     constexpr int HU = NP == 4 ? 2 : 4;         // heads at once
     __shared__ __align__(16) uint8_t stage[8][ANY_STG];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    prior_wait();
     T *buf = reinterpret_cast<T *>(stage[warp]);
     constexpr int V = 16 / (int)sizeof(T);      // channels a 16-byte piece
     const int hb = ANY_STG / ((int)sizeof(T) * p.hd);   // heads a pass
@@ -305,6 +308,7 @@ __global__ void __launch_bounds__(256, 4) rope_any_kernel(const __grid_constant_
         c2[i] = pr < p.hd / 2 ? p.c2[pr] : -1;
     }
     for (unsigned item = blockIdx.x * 8 + warp; item < (unsigned)p.items; item += gridDim.x * 8) {
+        if (item + gridDim.x * 8 >= (unsigned)p.items) next_go();
         const Chunk ch = chunk_of(p, item);
         float2 cs[NP];
         const int32_t *pos = p.pos + ch.row * p.ldp;
@@ -426,8 +430,7 @@ te_status launch(RopeParams &p, int rows, int hpi, cudaStream_t s) {
     if (items > 0x7FFFFFFFll) return fail(TE_ESHAPE, "qk_rope_axes: rows=%d too many", rows);
     p.items = (int)items;
     const long long need = (items + 7) / 8;
-    KERN<<<(unsigned)(need < most ? need : most), 256, 0, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_close(KERN, dim3((unsigned)(need < most ? need : most)), 256, 0, s, 1, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "qk_rope_axes launch");
 }
 
