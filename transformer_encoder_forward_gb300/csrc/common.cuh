@@ -584,6 +584,20 @@ __device__ __forceinline__ void widen4_f16(uint32_t w, uint32_t &lo, uint32_t &h
 
 // --------------------------------------------- draining an accumulator block
 
+// apply_act of two values, the same operations in f32 pairs where there are such.
+template <int ACT>
+__device__ __forceinline__ uint64_t act_pair(uint64_t g2) {
+    const uint64_t one2 = f2_pack(1.f, 1.f);
+    const uint64_t t2 = ACT == TE_ACT_GELU_TANH
+                            ? f2_mul(g2, f2_fma(f2_pack(-0.10294324f, -0.10294324f), f2_mul(g2, g2),
+                                                f2_pack(-2.3022082f, -2.3022082f)))
+                            : f2_mul(g2, f2_pack(-1.4426950408889634f, -1.4426950408889634f));
+    float t0, t1;
+    f2_unpack(t2, t0, t1);
+    f2_unpack(f2_fma(f2_pack(hw_exp2(t0), hw_exp2(t1)), one2, one2), t0, t1);
+    return f2_mul(g2, f2_pack(hw_rcp(t0), hw_rcp(t1)));
+}
+
 // One 32-token block of the gated form, in a draining warp whose lanes 0-15
 // hold the gate rows and 16-31 the up rows of its 16 features: v becomes the
 // outputs yv, lane l's for tokens 0-15 of feature l and lane l + 16's for
@@ -629,8 +643,9 @@ __device__ __forceinline__ void gate_block(const uint32_t (&v)[32], float sc, fl
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
         if constexpr (I8) {
-            yv[j] = apply_act(gv[j], act) * uv[j];
-            yv[j + 1] = apply_act(gv[j + 1], act) * uv[j + 1];
+            const uint64_t g2 = f2_pack(gv[j], gv[j + 1]);
+            const uint64_t a2 = act == TE_ACT_GELU_TANH ? act_pair<TE_ACT_GELU_TANH>(g2) : act_pair<TE_ACT_SILU>(g2);
+            f2_unpack(f2_mul(a2, f2_pack(uv[j], uv[j + 1])), yv[j], yv[j + 1]);
         } else {
             const uint64_t g2 = f2_pack(gv[j], gv[j + 1]);
             // GELU-tanh: z = g (0.79788456 + 0.035677408 g^2); SiLU: z = g / 2

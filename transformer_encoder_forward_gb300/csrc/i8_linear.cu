@@ -939,9 +939,19 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_accempty + 8 * b);
                 if (any && fo < it.n) {
+                    auto gate = [&](auto act_c) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        g[j] = __float_as_uint(apply_act(__uint_as_float(g[j]), it.act) * __uint_as_float(up[j]));
+                        for (int j = 0; j < 32; j += 2) {
+                            const uint64_t a2 = act_pair<decltype(act_c)::value>(
+                                f2_pack(__uint_as_float(g[j]), __uint_as_float(g[j + 1])));
+                            float y0, y1;
+                            f2_unpack(f2_mul(a2, f2_pack(__uint_as_float(up[j]), __uint_as_float(up[j + 1]))), y0, y1);
+                            g[j] = __float_as_uint(y0);
+                            g[j + 1] = __float_as_uint(y1);
+                        }
+                    };
+                    if (it.act == TE_ACT_GELU_TANH) gate(std::integral_constant<int, TE_ACT_GELU_TANH>{});
+                    else gate(std::integral_constant<int, TE_ACT_SILU>{});
                     store_bf16(g, fo);
                 }
             } else {
