@@ -550,6 +550,10 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
 // 11520 135 -> 130.
 __device__ __forceinline__ void prior_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void next_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Asks for memory that the previous kernel may still write: nothing is read.
+__device__ __forceinline__ void l2_prefetch(const void *p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 template <typename... P, typename... A>
 cudaError_t launch_close(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, A... args) {
     cudaLaunchConfig_t cfg = {};

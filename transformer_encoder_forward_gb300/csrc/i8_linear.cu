@@ -30,6 +30,7 @@ struct I8Params {
     const float *xs;
     long long ldx;
     int m, k, z;
+    int ahead;                // small: bytes of each weight row asked for beforehand
     I8Item it[MAXZ];
 };
 
@@ -50,10 +51,11 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int j) { return j == 0 
 // 4 g + t loads 16 consecutive bytes of rows g and g + 8 at k + 16 t, and of
 // tokens g, g + 8, ..., and word j of each is its share of the j-th 16-deep
 // product.  Rows and tokens are widened to f16 in registers (exact), five
-// instructions a word; D slots of 128 bytes are in flight meanwhile, and
-// alternate products add into separate sums (a chain of dependent products
-// would wait for each one's latency).  The warps' sums meet in shared memory,
-// always in the same order.
+// instructions a word; D neighbouring slots of 128 bytes are in flight
+// meanwhile (a step of all warps apart: 7 tokens, k 3840, n 11520 10.05 us, k
+// 10240, n 3840 11.8; neighbours 9.6 and 11.0), and alternate products add into
+// separate sums (a chain of dependent products would wait for each one's
+// latency).  The warps' sums meet in shared memory, always in the same order.
 // Gated: tile 0 is 16 gate rows, tile 1 the same features' up rows.
 template <int NT, int MT, bool GATED, int D>
 __global__ void __launch_bounds__(256) i8_small_kernel(const __grid_constant__ I8Params p) {
@@ -98,12 +100,17 @@ __global__ void __launch_bounds__(256) i8_small_kernel(const __grid_constant__ I
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[s][i][n][e] = 0.f;
+    if (threadIdx.x < 16 * MT && p.ahead) {
+        const int i = threadIdx.x >> 4, r = threadIdx.x & 15;
+        l2_prefetch(GATED && i == 1 ? it.w2 + (long long)(o0 + r) * p.k : it.w + (long long)(o0 + 16 * i + r) * p.k,
+                    p.ahead);
+    }
     prior_wait();
     next_go();
-    const int step = 128 * ks;
+    const int step = 128 * D * ks;
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(w[d], x[d], 128 * warp + d * step);
-    for (int k0 = 128 * warp; k0 < p.k; k0 += D * step) {
+    for (int d = 0; d < D; ++d) load(w[d], x[d], 128 * D * warp + 128 * d);
+    for (int k0 = 128 * D * warp; k0 < p.k; k0 += step) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {           // a slot past k holds zeros
 #pragma unroll
@@ -124,8 +131,8 @@ __global__ void __launch_bounds__(256) i8_small_kernel(const __grid_constant__ I
                         for (int i = 0; i < MT; ++i) mma_16x8x16(acc[j % AS][i][n], a[i], b0, b1);
                     }
                 }
-            if (k0 + (D + d) * step < p.k) load(w[d], x[d], k0 + (D + d) * step);
-            else if (k0 + D * step < p.k) {     // the next pass runs, without this slot
+            if (k0 + step + 128 * d < p.k) load(w[d], x[d], k0 + step + 128 * d);
+            else if (k0 + step < p.k) {     // the next pass runs, without this slot
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -174,8 +181,22 @@ __global__ void __launch_bounds__(256) i8_small_kernel(const __grid_constant__ I
     }
 }
 
+template <int NT, int MT, bool GATED, int D>
+te_status small_go(I8Params &p, int groups, cudaStream_t s) {
+    int ks = 1;
+    while (ks < 8 && (long long)groups * ks < SMS * 16 && 128 * D * ks < p.k) ks *= 2;
+    const cudaError_t e = launch_close(i8_small_kernel<NT, MT, GATED, D>, dim3(groups), 32 * ks,
+                                       ks * MT * 16 * NT * 8 * 4, s, 1, p);
+    return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
+}
+
 // One CTA a group of MT x 16 rows, with as many warps as fill the device (16
-// an SM) while each still has 128 bytes of k.
+// an SM) while each still has a pass of k.  Where eight warps a group do not
+// fill it and have several passes, each keeps twice as much in flight (1 token,
+// k 10240, n 3840: 10.7 -> 9.0 us; with 720 groups 9.4 -> 10.8).  The weights'
+// first 14 MB are asked into L2 before the previous kernel has ended (7 tokens,
+// k 3840: n 11520 10.9 -> 10.0 us, n 3840 6.2 -> 5.8; all 44 MB at once take
+// 12.3).  Sixteen warps a group: 10.7 -> 12.8 at k 10240.
 template <int NT, int MT, bool GATED>
 te_status small_launch(I8Params &p, cudaStream_t s) {
     constexpr int F = GATED ? 16 : MT * 16;
@@ -185,11 +206,12 @@ te_status small_launch(I8Params &p, cudaStream_t s) {
         p.it[i].tile0 = groups;
         groups += p.it[i].n / F;
     }
-    int ks = 1;
-    while (ks < 8 && (long long)groups * ks < SMS * 16 && 128 * ks < p.k) ks *= 2;
-    const cudaError_t e = launch_close(i8_small_kernel<NT, MT, GATED, D>, dim3(groups), 32 * ks,
-                                       ks * MT * 16 * NT * 8 * 4, s, 1, p);
-    return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
+    const int ahead = (int)((14ll << 20) / ((long long)groups * 16 * MT)) & ~15;
+    p.ahead = ahead < p.k ? ahead : p.k;
+    if constexpr (NT * MT <= 2) {
+        if ((long long)groups * 8 < SMS * 16 && p.k > 128 * D * 8) return small_go<NT, MT, GATED, 2 * D>(p, groups, s);
+    }
+    return small_go<NT, MT, GATED, D>(p, groups, s);
 }
 // --------------------------------------------------- a middling token count
 //
