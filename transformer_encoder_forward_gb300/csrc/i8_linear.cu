@@ -1123,12 +1123,14 @@ constexpr int MAX_K = 65536;
 // Which kernel takes a call.  The measured device times (us, back to back in a
 // graph, weights not in L2; n the output features in all):
 //                      small    mid   resident   large (with its widening pass)
-//   m = 8   k 3840 n 11520     10.9   14.9
+//   m = 8   k 3840 n 11520      9.7   14.9
 //   m = 16  k 512  n 1536       2.4    3.6    6.3    6.7
-//   m = 16  k 3840 n 3840       7.4    7.9          16.2
-//   m = 16  k 10240 n 3840     15.3   12.7          33.9
+//   m = 16  k 3840 n 3840       6.0    7.9          16.2
+//   m = 16  k 10240 n 3840     12.1   12.6          33.9
+//   m = 16  k 3840 n 11520     16.7   15.4
 //   m = 32  k 768  n 2304       3.9    4.1           7.2
-//   m = 32  k 3840 n 3840      10.6    8.5          16.3
+//   m = 32  k 2048 n 2048       5.3    4.6
+//   m = 32  k 3840 n 3840       9.9    8.5          16.3
 //   m = 64  k 3840 n 11520            22.3          17.8
 //   m = 128 k 512  n 1536              4.6    6.7    8.0
 //   m = 128 k 3840 n 3840             13.5          17.5
@@ -1138,7 +1140,7 @@ constexpr int MAX_K = 65536;
 //   m = 1000 k 512 n 1536              9.7    7.0    8.7
 //   m = 1000 k 768 n 2304             12.0          11.3
 //   m = 300 k 512  gated 2 x 2048      8.9    7.2    8.0
-// Small: to 8 tokens; to 16 (32) tokens while the weights are under 16 M (4 M)
+// Small: to 8 tokens; to 16 (32) tokens while the weights are under 40 M (2 M)
 // values, beyond which its warps' widening of the tokens costs more than the
 // TMEM pipeline's start.  Else to 1024 tokens mid where its modelled time (see
 // mid_consider) is below that of what takes the larger counts: at k <= 512 the
@@ -1159,7 +1161,7 @@ te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
         tiles += GATED ? (p.it[i].n + 63) / 64 : (p.it[i].n + 127) / 128;
     }
     path = SMALL;
-    if (p.m <= 8 || (p.m <= 16 && total * p.k <= (16 << 20)) || (p.m <= 32 && total * p.k <= (4 << 20))) return TE_OK;
+    if (p.m <= 8 || (p.m <= 16 && total * p.k <= (40 << 20)) || (p.m <= 32 && total * p.k <= (2 << 20))) return TE_OK;
     path = p.k <= 512 ? RES : LARGE;
     if (p.m > 1024) return TE_OK;
     const te_status st = mid_plan<GATED>(plan, tiles, p.m, p.k);
