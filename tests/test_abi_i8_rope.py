@@ -176,3 +176,16 @@ def test_the_binding_refuses_what_is_not_a_tensor_on_the_device(L):
         te.qk_rope_axes(x, 64, x, 64, 0, 0, 1, 0, 64, None, None, 1e-6, plan, q, 1.0, 2)
     with pytest.raises(OverflowError):
         te.qk_rope_axes(x, 64, x, 64, 0, 0, 1, 0, 64, None, None, 1e-6, plan, q, 1.0, 1 << 40)
+
+
+def test_qk_rope_axes_rejects_a_plan_of_heads_out_of_range(L):
+    # fields that hold together, of a head wider than the kernels index
+    plan = te.te_rope_axes()
+    plan.hd, plan.axes, plan.pairs, plan.pairing = 512, 1, 256, te.TE_ROPE_ADJACENT
+    plan.sections[0] = 512
+    args = [FAKE, 512, FAKE * 16, 512, te.TE_F32, 0, 0, 1, 0, 512, None, None, 1e-6, ctypes.byref(plan), FAKE, 1, 1.0, 1,
+            None]
+    assert _call(L, "te_qk_rope_axes", *args)[0] == te.TE_EINVAL
+    plan.hd, plan.pairs, plan.sections[0] = 12, 6, 12         # not a multiple of 8
+    args[1] = args[3] = args[9] = 12
+    assert _call(L, "te_qk_rope_axes", *args)[0] == te.TE_EINVAL

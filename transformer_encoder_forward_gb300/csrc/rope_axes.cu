@@ -496,6 +496,7 @@ te_status run(RopeParams &p, const te_rope_axes &pl, int rows, cudaStream_t s) {
 // A plan whose fields the kernels may index by.
 te_status check_plan(const te_rope_axes *pl, int32_t hd) {
     if (pl->hd != hd) return fail(TE_ESHAPE, "qk_rope_axes: plan for hd=%d, heads of %d", pl->hd, hd);
+    if (hd < 8 || hd > 2 * TE_ROPE_MAX_PAIRS || hd % 8) return fail(TE_EINVAL, "qk_rope_axes: not an initialised plan");
     if (pl->axes < 1 || pl->axes > TE_ROPE_MAX_AXES || pl->pairing < TE_ROPE_SECTION_HALVES ||
         pl->pairing > TE_ROPE_ADJACENT)
         return fail(TE_EINVAL, "qk_rope_axes: not an initialised plan");
