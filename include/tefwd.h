@@ -33,9 +33,9 @@
  *   - Work is enqueued on `stream` (NULL = the legacy default stream); the
  *     calls return before it completes.  te_q8_linear, te_q8_gated_linear,
  *     te_attn_varlen_fwd,
- *     the row ops, te_i8_linear, te_i8_gated_linear, te_qk_rope_axes and
- *     te_encoder_block_fwd are capturable in a CUDA graph
- *     (no host synchronisation, no allocation).
+ *     the row ops, te_quant_rows, te_rownorm_quant, te_i8_linear,
+ *     te_i8_gated_linear, te_qk_rope_axes and te_encoder_block_fwd are
+ *     capturable in a CUDA graph (no host synchronisation, no allocation).
  */
 #ifndef TEFWD_H
 #define TEFWD_H

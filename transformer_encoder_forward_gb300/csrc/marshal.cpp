@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <string>
 #include <vector>
 
@@ -57,11 +58,18 @@ Arg want(const char *what, PyObject *o, int types, int dims, int64_t rows, int64
     a.rows = dims == 2 ? t.size(0) : 1;
     a.cols = t.size(-1);
     a.ld = dims == 2 ? t.stride(0) : a.cols;
-    // a single row's stride says nothing
-    if (a.rows == 1 && a.ld < (a.cols + 15) / 16 * 16) a.ld = (a.cols + 15) / 16 * 16;
+    if (a.rows == 1) a.ld = (a.cols + 15) / 16 * 16;    // a single row's stride says nothing
     if (a.rows > 2147483647 || a.cols > 2147483647) raise(PyExc_ValueError, std::string(what) + ": too large");
     a.dtype = have == F32 ? TE_F32 : have == BF16 ? TE_BF16 : -1;
     return a;
+}
+
+// A leading dimension that the caller gives beside the tensor it belongs to.
+int64_t leading(const char *what, const Arg &t, int64_t ld) {
+    if (t.rows > 1 && ld != t.ld)
+        raise(PyExc_ValueError, std::string(what) + ": leading dimension " + std::to_string(ld) + ", the tensor's is " +
+                                    std::to_string(t.ld));
+    return ld;
 }
 
 void *opt(const char *what, PyObject *o, int types, int64_t cols) {
@@ -195,7 +203,7 @@ PyObject *i8_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 d.w = structure<te_q8w>("i8_linear: w", w);
                 const Arg ya = want("i8_linear: y", y, F32 | BF16, 2, x.rows, d.w.n);
                 d.y = ya.ptr;
-                d.ldy = integer(ldy);
+                d.ldy = leading("i8_linear: y", ya, integer(ldy));
                 d.y_dtype = ya.dtype;
                 d.epilogue = e ? int32_of(e) : TE_EPI_NONE;
                 d.residual = nullptr;
@@ -203,8 +211,10 @@ PyObject *i8_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 if (r && r != Py_None) {
                     PyObject *ldr = key(it, K_LDR);
                     if (!ldr) raise(PyExc_KeyError, "i8_linear: a residual needs ldr");
-                    d.residual = static_cast<const float *>(want("i8_linear: residual", r, F32, 2, x.rows, -1).ptr);
-                    d.ldr = integer(ldr);
+                    const Arg ra = want("i8_linear: residual", r, F32, 2, x.rows, -1);
+                    if (ra.cols < d.w.n) raise(PyExc_ValueError, "i8_linear: residual: fewer columns than features");
+                    d.residual = static_cast<const float *>(ra.ptr);
+                    d.ldr = leading("i8_linear: residual", ra, integer(ldr));
                 }
             }
         } catch (...) {
@@ -245,8 +255,14 @@ PyObject *qk_rope_axes(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Arg dst = want("qk_rope_axes: dst", a[2], src.dtype == TE_F32 ? F32 : BF16, 2, rows, -1);
         const te_rope_axes plan = structure<te_rope_axes>("qk_rope_axes: plan", a[12]);
         const Arg pos = want("qk_rope_axes: pos", a[13], I32, 2, rows, plan.axes);
-        return te_qk_rope_axes(src.ptr, integer(a[1]), dst.ptr, integer(a[3]), src.dtype, int32_of(a[4]), int32_of(a[5]),
-                               int32_of(a[6]), int32_of(a[7]), hd,
+        const int64_t lds = leading("qk_rope_axes: src", src, integer(a[1]));
+        const int64_t ldd = leading("qk_rope_axes: dst", dst, integer(a[3]));
+        const int32_t q_off = int32_of(a[4]), k_off = int32_of(a[5]), nq = int32_of(a[6]), nkv = int32_of(a[7]);
+        const int64_t end = std::max(nq ? q_off + (int64_t)nq * hd : 0, nkv ? k_off + (int64_t)nkv * hd : 0);
+        if (end > src.cols || end > dst.cols)
+            raise(PyExc_ValueError, "qk_rope_axes: the heads end at column " + std::to_string(end) + " of " +
+                                        std::to_string(std::min(src.cols, dst.cols)));
+        return te_qk_rope_axes(src.ptr, lds, dst.ptr, ldd, src.dtype, q_off, k_off, nq, nkv, hd,
                                static_cast<const float *>(opt("qk_rope_axes: qn", a[9], F32, hd)),
                                static_cast<const float *>(opt("qk_rope_axes: kn", a[10], F32, hd)), real(a[11]), &plan,
                                static_cast<const int32_t *>(pos.ptr), pos.ld, real(a[14]), rows, stream_of(a[16]));
