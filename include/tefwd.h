@@ -298,6 +298,7 @@ te_status te_pool_mean(const float *x, int32_t d, const int32_t *cu_host,
                        float *out, te_stream stream);
 
 /* ---- activations in 8 bits -------------------------------------------- */
+/* (Here and in te_qk_rope_axes: with no rows, the rows' pointers may be NULL.) */
 
 /* quant_rows: each row in 8 bits with a scale of its own.
  *   a = max_j |x[r, j]|;  scale[r] = a / 127;  q[r, j] = rint(x[r, j] * (127 / a))
@@ -329,7 +330,7 @@ te_status te_rownorm_quant(const void *x, int32_t xdt, int64_t ldx, const float 
  * The sum runs over exact integer products in 32 bits: exact whenever no
  * partial sum reaches 2^24 in magnitude (any k <= 1040, and in practice sums
  * of both signs at every k), else rounded like an f32 sum.
- * Sizes: m >= 0, 64 <= k <= 65536, k % 64 == 0, 1 <= z <= 4.
+ * Sizes: 0 <= m <= 2^31 - 256, 64 <= k <= 65536, k % 64 == 0, 1 <= z <= 4.
  * workspace: te_i8_workspace(m, k, n) bytes or more with n the sum of the
  * items' n, 256-byte aligned (may be NULL when that is 0).  It holds nothing
  * between calls; calls that may run at the same time need one each.

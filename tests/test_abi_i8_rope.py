@@ -189,3 +189,22 @@ def test_qk_rope_axes_rejects_a_plan_of_heads_out_of_range(L):
     plan.hd, plan.pairs, plan.sections[0] = 12, 6, 12         # not a multiple of 8
     args[1] = args[3] = args[9] = 12
     assert _call(L, "te_qk_rope_axes", *args)[0] == te.TE_EINVAL
+
+
+def test_no_rows_need_no_memory(L):
+    assert _linear(L, x=None, xs=None, m=0, item=_item(y=None))[0] == te.TE_OK
+    assert _linear(L, x=None, m=1)[0] == te.TE_EINVAL
+    w = te.te_q8w(FAKE, FAKE, None, 64, 128, None, None)
+    assert _call(L, "te_i8_gated_linear", None, 128, None, 0, 128, ctypes.byref(w), ctypes.byref(w), te.TE_ACT_SILU, None, 64,
+                 None, 0, None)[0] == te.TE_OK
+    assert _call(L, "te_quant_rows", None, te.TE_F32, 64, None, 64, None, 0, 64, None)[0] == te.TE_OK
+    assert _call(L, "te_rownorm_quant", None, te.TE_F32, 64, FAKE, None, None, te.TE_NORM_RMS, 1e-6, 1.0, None, 64, None, 0,
+                 64, None)[0] == te.TE_OK
+    plan = te.rope_axes_plan(64, (16, 24, 24))
+    assert _call(L, "te_qk_rope_axes", None, 128, None, 128, te.TE_BF16, 0, 64, 1, 1, 64, None, None, 1e-6,
+                 ctypes.byref(plan), None, 3, 1.0, 0, None)[0] == te.TE_OK
+
+
+def test_i8_products_reject_rows_whose_tiles_pass_an_int(L):
+    assert _linear(L, m=0x7FFFFFFF)[0] == te.TE_ESHAPE
+    assert te.i8_workspace(0x7FFFFFFF, 128, 64) == 0

@@ -95,3 +95,18 @@ def test_leading_dimensions_are_those_of_the_tensors():
     with pytest.raises(ValueError):
         rope(y[:, :32], 64)
     te.check()
+
+
+def test_an_empty_batch_is_no_error():
+    import torch
+    z = lambda *s, t=torch.float32: torch.empty(*s, dtype=t, device="cuda")
+    w, sw = torch.zeros(32, 64, dtype=torch.int8, device="cuda"), torch.zeros(32, device="cuda")
+    qw = te.q8w(w, sw)
+    x, xs, y = z(0, 64, t=torch.int8), z(0), z(0, 32)
+    te.quant_rows(z(0, 64), x, xs)
+    te.rownorm_quant(z(0, 64), z(64), None, 0, 1e-6, x, xs)
+    te.i8_linear(x, xs, [dict(w=qw, y=y, ldy=32)], None)
+    te.i8_gated_linear(x, xs, qw, qw, 1, z(0, 32, t=torch.bfloat16), None)
+    plan = te.rope_axes_plan(32, (16, 16))
+    te.qk_rope_axes(z(0, 64), 64, z(0, 64), 64, 0, 32, 1, 1, 32, None, None, 1e-6, plan, z(0, 2, t=torch.int32), 1.0, 0)
+    te.check()

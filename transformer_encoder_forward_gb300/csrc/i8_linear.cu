@@ -1118,7 +1118,7 @@ te_status widen(const int8_t *x, int64_t ldx, void *y, int m, int k, cudaStream_
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear: widen launch");
 }
 
-constexpr int MAX_K = 65536;
+constexpr int MAX_K = 65536, MAX_M = 0x7FFFFF00;   // token tiles end within an int
 
 // Which kernel takes a call.  The measured device times (us, back to back in a
 // graph, weights not in L2; n the output features in all):
@@ -1180,9 +1180,9 @@ te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
     return TE_OK;
 }
 te_status check_x(const char *what, const void *x, int64_t ldx, const float *xs, int32_t m, int32_t k) {
-    if (!x || !xs) return fail(TE_EINVAL, "%s: NULL x or x_scale", what);
-    if (m < 0 || k < 64 || k > MAX_K || k % 64)
-        return fail(TE_ESHAPE, "%s: m=%d k=%d (k %% 64 == 0, 64..%d)", what, m, k, MAX_K);
+    if (m > 0 && (!x || !xs)) return fail(TE_EINVAL, "%s: NULL x or x_scale", what);
+    if (m < 0 || m > MAX_M || k < 64 || k > MAX_K || k % 64)
+        return fail(TE_ESHAPE, "%s: m=%d k=%d (m 0..%d, k %% 64 == 0, 64..%d)", what, m, k, MAX_M, MAX_K);
     if (ldx < k || ldx % 16) return fail(TE_ESHAPE, "%s: ldx=%lld (>= k, multiple of 16)", what, (long long)ldx);
     if (!aligned16(x) || (reinterpret_cast<uintptr_t>(xs) & 3))
         return fail(TE_EALIGN, "%s: x 16-byte, x_scale 4-byte aligned", what);
@@ -1214,7 +1214,7 @@ te_status check_ws(const char *what, const void *ws, size_t have, size_t need) {
 using namespace tefwd;
 
 // the f16 activation of a call that widens it beforehand, whatever n
-static size_t workspace_of(int32_t m, int32_t k) { return m <= 8 ? 0 : ((size_t)m * k * 2 + 255) & ~(size_t)255; }
+static size_t workspace_of(int32_t m, int32_t k) { return m <= 8 || m > MAX_M ? 0 : ((size_t)m * k * 2 + 255) & ~(size_t)255; }
 
 extern "C" size_t te_i8_workspace(int32_t m, int32_t k, int32_t n) {
     return k < 64 || k > MAX_K || k % 64 || n < 32 ? 0 : workspace_of(m, k);
@@ -1239,7 +1239,7 @@ extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_s
     for (int i = 0; i < z; ++i) {
         const te_q8_item &src = items[i];
         if ((st = check_w("i8_linear", i, src.w, k)) != TE_OK) return st;
-        if (!src.y) return fail(TE_EINVAL, "i8_linear: item %d has a NULL y", i);
+        if (m > 0 && !src.y) return fail(TE_EINVAL, "i8_linear: item %d has a NULL y", i);
         if (src.y_dtype != TE_F32 && src.y_dtype != TE_BF16) return fail(TE_EINVAL, "i8_linear: item %d bad y dtype", i);
         if (src.ldy < src.w.n) return fail(TE_ESHAPE, "i8_linear: item %d ldy < n", i);
         if (!aligned16(src.y) || (src.ldy * (src.y_dtype == TE_F32 ? 4 : 2)) % 16)
@@ -1289,7 +1289,7 @@ extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const floa
                                         int32_t k, const te_q8w *wg, const te_q8w *wu, int32_t act,
                                         void *out, int64_t ldm, void *workspace, size_t ws_bytes,
                                         te_stream stream) {
-    if (!wg || !wu || !out) return fail(TE_EINVAL, "i8_gated_linear: NULL wg, wu or out");
+    if (!wg || !wu || (m > 0 && !out)) return fail(TE_EINVAL, "i8_gated_linear: NULL wg, wu or out");
     if (act != TE_ACT_GELU_TANH && act != TE_ACT_SILU) return fail(TE_EINVAL, "i8_gated_linear: bad act");
     te_status st = check_x("i8_gated_linear", x, ldx, x_scale, m, k);
     if (st != TE_OK) return st;

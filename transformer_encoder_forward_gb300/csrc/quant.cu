@@ -293,7 +293,7 @@ te_status launch(const void *x, int64_t ldx, const float *w, const float *b, con
 
 te_status check(const char *what, const void *x, int32_t xdt, int64_t ldx, const int8_t *q, int64_t ldq,
                 const float *scale, int32_t t, int32_t d) {
-    if (!x || !q || !scale) return fail(TE_EINVAL, "%s: NULL x, q or scale", what);
+    if (t > 0 && (!x || !q || !scale)) return fail(TE_EINVAL, "%s: NULL x, q or scale", what);
     if (xdt != TE_F32 && xdt != TE_BF16) return fail(TE_EINVAL, "%s: bad dtype", what);
     if (t < 0 || d < 8 || d > 16384 || d % 8)
         return fail(TE_ESHAPE, "%s: t=%d d=%d (d %% 8 == 0, 8..16384)", what, t, d);

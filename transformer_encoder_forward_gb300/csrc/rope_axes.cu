@@ -564,7 +564,8 @@ extern "C" te_status te_qk_rope_axes(const void *src, int64_t ld_src, void *dst,
                                      int32_t hd, const float *qn, const float *kn, float eps,
                                      const te_rope_axes *plan, const int32_t *pos, int64_t ldp,
                                      float q_mul, int32_t rows, te_stream stream) {
-    if (!src || !dst || !plan || !pos) return fail(TE_EINVAL, "qk_rope_axes: NULL src, dst, plan or pos");
+    if (!plan || (rows > 0 && (!src || !dst || !pos)))
+        return fail(TE_EINVAL, "qk_rope_axes: NULL src, dst, plan or pos");
     if (dt != TE_F32 && dt != TE_BF16) return fail(TE_EINVAL, "qk_rope_axes: bad dtype");
     const te_status ps = check_plan(plan, hd);
     if (ps != TE_OK) return ps;
