@@ -347,3 +347,26 @@ def test_the_block_with_8_bit_activations_on_a_video_grid():
     assert rel(m64, _act(g, te.TE_ACT_SILU) * u) <= UB
     d_in = q64(m8, as_)
     assert rel(to_np(x), x1 + _product(*d_in, ws["d"])[1]) <= 16 * U32
+
+
+@pytest.mark.parametrize("rows,nq,nkv,hd,dt", [(2600, 20, 10, 256, "bf16"), (5000, 16, 14, 128, "bf16"),
+                                               (5003, 13, 13, 104, "bf16"), (3700, 17, 12, 256, "f32"),
+                                               (9001, 16, 15, 128, "bf16")])
+def test_rows_are_turned_alike_however_many_there_are(rows, nq, nkv, hd, dt):
+    # many rows, whose last ones are cut finer, against a few at a time: the same bits
+    torch = _torch()
+    t = torch.float32 if dt == "f32" else torch.bfloat16
+    gen = torch.Generator("cuda").manual_seed(rows)
+    w = (nq + nkv) * hd
+    x = torch.randn(rows, w, device="cuda", generator=gen).to(t)
+    qn, kn = torch.rand(hd, device="cuda", generator=gen), torch.rand(hd, device="cuda", generator=gen)
+    pos = torch.randint(-500, 500, (rows, 2), dtype=torch.int32, device="cuda", generator=gen)
+    plan = te.rope_axes_plan(hd, (hd // 2, hd // 2))
+    a, b = torch.full_like(x, float("nan")), torch.full_like(x, float("nan"))
+    te.qk_rope_axes(x, w, a, w, 0, nq * hd, nq, nkv, hd, qn, kn, 1e-6, plan, pos, 0.5, rows)
+    for r in range(0, rows, 400):
+        n = min(400, rows - r)
+        te.qk_rope_axes(x[r:r + n], w, b[r:r + n], w, 0, nq * hd, nq, nkv, hd, qn, kn, 1e-6, plan, pos[r:r + n], 0.5, n)
+    assert not bool(torch.isnan(a.float()).any())
+    assert torch.equal(a, b)
+    te.check()

@@ -27,7 +27,8 @@ struct RopeParams {
     const float *qn, *kn;
     const int32_t *pos;
     long long lds, ldd, ldp;
-    int items;                // rows * cuts
+    int items;                // rows * cuts, those from `full` on in `fine` pieces of `sub` slots
+    int full, fine, sub;
     int q_off, k_off, nq, nkv, hd;
     int hpi;                  // heads a slot
     int sq, slots;            // slots of the q heads, and with the k heads'
@@ -119,12 +120,24 @@ struct Chunk {
     long long row;
     int s0, s1;
 };
+template <bool FINE>
 __device__ __forceinline__ Chunk chunk_of(const RopeParams &p, unsigned item) {
+    unsigned fine = 0;
+    const bool last = FINE && p.fine > 1 && item >= (unsigned)p.full;
+    if (last) {
+        const unsigned r = item - p.full, b = r / (unsigned)p.fine;
+        fine = r - b * p.fine;
+        item = p.full + b;
+    }
     const unsigned row = item / (unsigned)p.cuts;
     Chunk c;
     c.row = row;
     c.s0 = (int)(item - row * p.cuts) * p.per;
     c.s1 = c.s0 + p.per < p.slots ? c.s0 + p.per : p.slots;
+    if (last) {
+        c.s0 += (int)fine * p.sub;
+        c.s1 = c.s0 + p.sub < c.s1 ? c.s0 + p.sub : c.s1;
+    }
     return c;
 }
 // The heads [h0, h1) of part `k` (0: q, 1: k) in the chunk; empty where h0 >= h1.
@@ -145,10 +158,10 @@ __device__ __forceinline__ void part_heads(const RopeParams &p, const Chunk &c, 
 // any arithmetic, which runs in f32 pairs.  Bound by HBM: registers are held to
 // 64 (f32 80) for four (three) CTAs an SM, with the frequency words in shared
 // memory; at 79 and two CTAs the 32760-row clip (1.0 GB) took 174 us instead of
-// 159 (6.3 TB/s, 0.93 of the measured copy rate).  8448 rows (259 MB) take 49
+// 159 (6.3 TB/s, 0.93 of the measured copy rate).  8448 rows (259 MB) take 46
 // us, where a plain copy of as many bytes takes 41: a launch's start and end
 // cost both.  Loads a step ahead in registers (fewer warps) took 55 us.  With few
-// heads a row instructions bound it: 8448 rows of 12 + 4 heads of 96 take 20 us.
+// heads a row instructions bound it: 8448 rows of 12 + 4 heads of 96 take 18 us.
 template <typename T, bool ADJ, bool PART, int LPH>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_vec_kernel(const __grid_constant__ RopeParams p) {
     constexpr int QU = 4;                       // load slots in flight
@@ -174,7 +187,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_vec_kernel(c
     const int c1 = p.c1[uu], c2 = p.c2[uu], p0 = p.p0[uu];
     for (unsigned item = blockIdx.x * 8 + (threadIdx.x >> 5); item < (unsigned)p.items; item += gridDim.x * 8) {
         if (item + gridDim.x * 8 >= (unsigned)p.items) next_go();
-        const Chunk ch = chunk_of(p, item);
+        const Chunk ch = chunk_of<(LPH >= 16)>(p, item);
         bool turned = false;                    // the row's cosines and sines are there
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(256, 4) rope_any_kernel(const __grid_constant_
     }
     for (unsigned item = blockIdx.x * 8 + warp; item < (unsigned)p.items; item += gridDim.x * 8) {
         if (item + gridDim.x * 8 >= (unsigned)p.items) next_go();
-        const Chunk ch = chunk_of(p, item);
+        const Chunk ch = chunk_of<false>(p, item);
         float2 cs[NP];
         const int32_t *pos = p.pos + ch.row * p.ldp;
 #pragma unroll
@@ -397,7 +410,7 @@ __global__ void __launch_bounds__(256, 4) rope_any_kernel(const __grid_constant_
 }
 
 // Cuts the rows into items and launches one wave of warps over them.
-template <auto KERN>
+template <auto KERN, bool FINE = false>
 te_status launch(RopeParams &p, int rows, int hpi, cudaStream_t s) {
     // resident CTAs of the whole device, asked for once a kernel and device
     static int resident[64] = {};
@@ -428,8 +441,23 @@ te_status launch(RopeParams &p, int rows, int hpi, cudaStream_t s) {
     p.cuts = (p.slots + p.per - 1) / p.per;
     const long long items = (long long)rows * p.cuts;
     if (items > 0x7FFFFFFFll) return fail(TE_ESHAPE, "qk_rope_axes: rows=%d too many", rows);
-    p.items = (int)items;
-    const long long need = (items + 7) / 8;
+    // What the last round of warps holds is cut finer, so that it occupies them
+    // all: a round of whole items for a part of them would take as long (8448 rows
+    // of 60 heads of 128, 3.5 rounds: 49.1 -> 45.9 us).  Pieces below 8 slots cost
+    // more in repeated sines and cosines than they gain, and where a slot holds
+    // three heads or more the index arithmetic alone does (16 heads of 72: 15.7 ->
+    // 16.1 us).  Over many rounds the warps drift apart and even out by themselves
+    // (32760 rows, 13.5 rounds: 159.3 -> 160.2 us with them).
+    p.full = (int)(items / warps * warps);
+    const long long rem = items - p.full;
+    long long fine = FINE && p.full && p.full / warps < 8 && rem ? warps / rem : 1;
+    if (fine > (p.per + 1) / 8) fine = (p.per + 1) / 8;
+    if (fine < 1) fine = 1;
+    p.sub = (int)((p.per + fine - 1) / fine);
+    p.fine = (p.per + p.sub - 1) / p.sub;
+    if (p.full + rem * p.fine > 0x7FFFFFFFll) p.fine = 1, p.sub = p.per;
+    p.items = (int)(p.full + rem * p.fine);
+    const long long need = ((long long)p.items + 7) / 8;
     e = launch_close(KERN, dim3((unsigned)(need < most ? need : most)), 256, 0, s, 1, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "qk_rope_axes launch");
 }
@@ -441,8 +469,8 @@ te_status launch_vec(RopeParams &p, int rows, cudaStream_t s) {
     const int nu = p.hd / 8;
     if (nu == 4) return launch<rope_vec_kernel<T, ADJ, PART, 4>>(p, rows, 8, s);
     if (nu == 7 || nu == 8) return launch<rope_vec_kernel<T, ADJ, PART, 8>>(p, rows, 4, s);
-    if (nu >= 11 && nu <= 16) return launch<rope_vec_kernel<T, ADJ, PART, 16>>(p, rows, 2, s);
-    if (nu >= 17) return launch<rope_vec_kernel<T, ADJ, PART, 32>>(p, rows, 1, s);
+    if (nu >= 11 && nu <= 16) return launch<rope_vec_kernel<T, ADJ, PART, 16>, true>(p, rows, 2, s);
+    if (nu >= 17) return launch<rope_vec_kernel<T, ADJ, PART, 32>, true>(p, rows, 1, s);
     return launch<rope_vec_kernel<T, ADJ, PART, 0>>(p, rows, 32 / nu, s);
 }
 
