@@ -275,6 +275,12 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -907,10 +913,10 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
             if (!ok) break;
             tc_fence_after();
             const uint64_t ts2 = f2_pack(ts, ts);
-            // (acc * ts) * scale + bias of 32 columns from column c, in place
-            auto scaled = [&](uint32_t (&v)[32], int c) {
+            // (acc * ts) * scale + bias of v's columns, from column c on, in place
+            auto scaled = [&](auto &v, int c) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
+                for (int j = 0; j < (int)(sizeof(v) / 4); j += 4) {
                     const float4 s4 = *reinterpret_cast<const float4 *>(fac + c + j);
                     const float4 b4 = *reinterpret_cast<const float4 *>(fac + 128 + c + j);
                     const uint64_t y0 = f2_fma(f2_mul(f2_pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), ts2),
@@ -927,6 +933,14 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
                 }
             };
             // 32 tokens x 32 features as bf16: 64-byte rows, 64-byte swizzle
+            auto send_bf16 = [&](const uint8_t *st, int fo) {
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&p.ty[zi], smem_u32(st), fo, tb);
+                    bulk_commit();
+                }
+            };
             auto store_bf16 = [&](const uint32_t (&v)[32], int fo) {
                 uint8_t *st = block(2048);
 #pragma unroll
@@ -938,44 +952,48 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
                     w.w = pack_bf16x2(__uint_as_float(v[8 * c + 6]), __uint_as_float(v[8 * c + 7]));
                     *reinterpret_cast<uint4 *>(st + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = w;
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_2d(&p.ty[zi], smem_u32(st), fo, tb);
-                    bulk_commit();
-                }
+                send_bf16(st, fo);
             };
             const bool any = tb < p.m;          // warp-uniform
             if constexpr (GATED) {
+                // 16 features at a time: with 32 the registers spill
                 const int fo = (ft - it.tile0) * F + 32 * h;
-                uint32_t g[32], up[32];
-                if (any) {
-                    tmem_ld32(tbase + trow + 128 * b + 32 * h, g);
-                    tmem_ld32(tbase + trow + 128 * b + 64 + 32 * h, up);
-                    tmem_wait_ld();
-                    scaled(g, 32 * h);
-                    scaled(up, 64 + 32 * h);
-                }
-                // read, and the factors too
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_accempty + 8 * b);
-                if (any && fo < it.n) {
+                const bool out = any && fo < it.n;
+                uint8_t *st = out ? block(2048) : stg;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t g[16], up[16];
+                    if (any) {
+                        tmem_ld16(tbase + trow + 128 * b + 32 * h + 16 * c, g);
+                        tmem_ld16(tbase + trow + 128 * b + 64 + 32 * h + 16 * c, up);
+                        tmem_wait_ld();
+                        scaled(g, 32 * h + 16 * c);
+                        scaled(up, 64 + 32 * h + 16 * c);
+                    }
+                    if (c == 1) {               // read, and the factors too
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_accempty + 8 * b);
+                    }
+                    if (!out) continue;
                     auto gate = [&](auto act_c) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
+                        for (int j = 0; j < 16; j += 2) {
                             const uint64_t a2 = act_pair<decltype(act_c)::value>(
                                 f2_pack(__uint_as_float(g[j]), __uint_as_float(g[j + 1])));
                             float y0, y1;
                             f2_unpack(f2_mul(a2, f2_pack(__uint_as_float(up[j]), __uint_as_float(up[j + 1]))), y0, y1);
-                            g[j] = __float_as_uint(y0);
-                            g[j + 1] = __float_as_uint(y1);
+                            g[j / 2] = pack_bf16x2(y0, y1);
                         }
                     };
                     if (it.act == TE_ACT_GELU_TANH) gate(std::integral_constant<int, TE_ACT_GELU_TANH>{});
                     else gate(std::integral_constant<int, TE_ACT_SILU>{});
-                    store_bf16(g, fo);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<uint4 *>(st + lane * 64 + (((2 * c + j) ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(g[4 * j], g[4 * j + 1], g[4 * j + 2], g[4 * j + 3]);
                 }
+                if (out) send_bf16(st, fo);
             } else {
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
