@@ -538,10 +538,11 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
 // since that one waited too, everything before it has ended as well.  So:
 //   * next_go comes after the kernel's own prior_wait and after its TMEM
 //     allocation (a later kernel's allocation must not be waited for);
-//   * a kernel whose CTAs work through many units calls it at its last one (at
-//     its start, in the kernel with resident weights, 16238 tokens gated 2 x 2048
-//     took 70 us instead of 63), and the large pipeline not at all (a widening
-//     pass waiting beside its last units: 12297 x 8768 gated 2 x 128 98 -> 108 us);
+//   * a kernel whose CTAs work through many rows calls it behind its last one
+//     (32760 rotated rows: at the start 161.4 us, as the last row begins 159.3,
+//     behind it 158.1; 8448 x 3840 f32 norm and quantisation: 29.7, 34.5, 29.3),
+//     and the large pipeline not at all (a widening pass waiting beside its last
+//     units: 12297 x 8768 gated 2 x 128 98 -> 108 us);
 //   * nothing is read through the read-only path (__ldg, const __restrict__),
 //     whose loads the compiler may move above the wait.
 // The calls of a block follow one another at 1 to 3 us less each: 1023 rows of 16

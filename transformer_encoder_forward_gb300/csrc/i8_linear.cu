@@ -717,21 +717,28 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
+    const int ft0 = u0 / p.ttiles, tt0 = u0 - ft0 * p.ttiles;
+    auto item_of = [&](int ft) {
+        int zi = 0;
+        while (zi + 1 < p.z && ft >= p.it[zi + 1].tile0) ++zi;
+        return zi;
+    };
+    // The tile's weights, by its first CTA (16238 x 512 x 512 f32: 14.0 -> 13.7 us;
+    // by every CTA 14.1).
+    if (threadIdx.x < 128 && u0 < u1 && tt0 == 0) {
+        const I8Item &it = p.it[item_of(ft0)];
+        const int r = threadIdx.x, o = (ft0 - it.tile0) * F + (GATED ? r & 63 : r);
+        if (o < it.n) l2_prefetch((GATED && r >= 64 ? it.w2 : it.w) + (long long)o * p.k, p.k);
+    }
     prior_wait();
     bool ok = true;
     // unit u is (feature tile ft, token tile tt); it brings new weights where a
     // run or a feature tile begins
-    const int ft0 = u0 / p.ttiles, tt0 = u0 - ft0 * p.ttiles;
     auto next = [&](int &ft, int &tt) {
         if (++tt == p.ttiles) {
             tt = 0;
             ++ft;
         }
-    };
-    auto item_of = [&](int ft) {
-        int zi = 0;
-        while (zi + 1 < p.z && ft >= p.it[zi + 1].tile0) ++zi;
-        return zi;
     };
 
     if (warp == 0) {
@@ -1157,7 +1164,7 @@ constexpr int MAX_K = 65536, MAX_M = 0x7FFFFF00;   // token tiles end within an 
 //   m = 600 k 512  n 1536              6.5    6.8    8.2
 //   m = 1000 k 512 n 1536              9.7    7.0    8.7
 //   m = 1000 k 768 n 2304             12.0          11.3
-//   m = 300 k 512  gated 2 x 2048      8.9    7.2    8.0
+//   m = 300 k 512  gated 2 x 2048      8.9    7.1    8.0
 // Small: to 8 tokens; to 16 (32) tokens while the weights are under 40 M (2 M)
 // values, beyond which its warps' widening of the tokens costs more than the
 // TMEM pipeline's start.  Else to 1024 tokens mid where its modelled time (see
@@ -1166,9 +1173,9 @@ constexpr int MAX_K = 65536, MAX_M = 0x7FFFFF00;   // token tiles end within an 
 // of its CTAs; beyond, large, 7 us (the widening pass and a second launch) and
 // 0.39 us a stage of each wave of 256 x 128 units (fits of what was measured,
 // to about 20 %; of the rows above and ten others, none is given to a slower
-// kernel).  Resident against large at 16238 tokens (us): k 512, n 1536 bf16 27.7
-// and 34.2; n 512 f32 13.8 and 21.3; gated 2 x 2048 63.3 and 68.7; k 64, n 512
-// f32 10.2 and 19.0.
+// kernel).  Resident against large at 16238 tokens (us): k 512, n 1536 bf16 27.9
+// and 34.2; n 512 f32 13.7 and 21.3; gated 2 x 2048 58.1 and 68.7; k 64, n 512
+// f32 10.1 and 19.0.
 enum Path { SMALL, MID, RES, LARGE };
 template <bool GATED>
 te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {

@@ -158,7 +158,7 @@ __device__ __forceinline__ void part_heads(const RopeParams &p, const Chunk &c, 
 // any arithmetic, which runs in f32 pairs.  Bound by HBM: registers are held to
 // 64 (f32 80) for four (three) CTAs an SM, with the frequency words in shared
 // memory; at 79 and two CTAs the 32760-row clip (1.0 GB) took 174 us instead of
-// 159 (6.3 TB/s, 0.93 of the measured copy rate).  8448 rows (259 MB) take 46
+// 158 (6.4 TB/s, 0.94 of the measured copy rate).  8448 rows (259 MB) take 46
 // us, where a plain copy of as many bytes takes 41: a launch's start and end
 // cost both.  Loads a step ahead in registers (fewer warps) took 55 us.  With few
 // heads a row instructions bound it: 8448 rows of 12 + 4 heads of 96 take 18 us.
@@ -186,7 +186,6 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_vec_kernel(c
     const int uu = on ? u : 0;
     const int c1 = p.c1[uu], c2 = p.c2[uu], p0 = p.p0[uu];
     for (unsigned item = blockIdx.x * 8 + (threadIdx.x >> 5); item < (unsigned)p.items; item += gridDim.x * 8) {
-        if (item + gridDim.x * 8 >= (unsigned)p.items) next_go();
         const Chunk ch = chunk_of<(LPH >= 16)>(p, item);
         bool turned = false;                    // the row's cosines and sines are there
 #pragma unroll 1
@@ -295,6 +294,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_vec_kernel(c
                 }
             }
         }
+        if (item + gridDim.x * 8 >= (unsigned)p.items) next_go();
     }
 }
 
@@ -321,7 +321,6 @@ __global__ void __launch_bounds__(256, 4) rope_any_kernel(const __grid_constant_
         c2[i] = pr < p.hd / 2 ? p.c2[pr] : -1;
     }
     for (unsigned item = blockIdx.x * 8 + warp; item < (unsigned)p.items; item += gridDim.x * 8) {
-        if (item + gridDim.x * 8 >= (unsigned)p.items) next_go();
         const Chunk ch = chunk_of<false>(p, item);
         float2 cs[NP];
         const int32_t *pos = p.pos + ch.row * p.ldp;
@@ -406,6 +405,7 @@ __global__ void __launch_bounds__(256, 4) rope_any_kernel(const __grid_constant_
                 __syncwarp();                   // before the next pass overwrites the stage
             }
         }
+        if (item + gridDim.x * 8 >= (unsigned)p.items) next_go();
     }
 }
 
