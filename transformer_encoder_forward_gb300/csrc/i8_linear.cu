@@ -215,7 +215,7 @@ te_status small_launch(I8Params &p, cudaStream_t s) {
 }
 // --------------------------------------------------- a middling token count
 //
-// Up to a few hundred tokens the products are still bound by the weights'
+// Up to a few hundred tokens, or more with few features, the products are still bound by the weights'
 // bytes or by latency: the wide tiles of the large pipeline (q8_linear.cu) leave
 // SMs idle there, and its activation needs a widening pass of its own.  Here a
 // CTA takes 128 weight rows (TMEM lanes) x N tokens x a share of k, in one
@@ -530,7 +530,8 @@ template <int N>
 void mid_consider(MidPlan &best, int ftiles, int m, int nkb, const int *residents) {
     constexpr double start = N <= 16 ? 4.2 : (N <= 32 ? 4.6 : (N <= 64 ? 5.5 : 6.5));
     constexpr double stage = N <= 16 ? 0.5 : (N <= 32 ? 0.55 : (N <= 64 ? 0.65 : 0.8));
-    const long long tiles = (long long)ftiles * ((m + N - 1) / N);
+    const long long ttiles = ((long long)m + N - 1) / N, tiles = ftiles * ttiles;
+    if (ttiles > 65535) return;                 // a grid's second axis
     for (int s = 1; s <= 8 && s <= nkb; s *= 2) {
         const int r = residents[s] > 0 ? residents[s] : 1;
         const double us = (double)((tiles + r - 1) / r) * (start + stage * ((nkb + s - 1) / s));
@@ -1164,16 +1165,19 @@ constexpr int MAX_K = 65536, MAX_M = 0x7FFFFF00;   // token tiles end within an 
 //   m = 600 k 512  n 1536              6.5    6.8    8.2
 //   m = 1000 k 512 n 1536              9.7    7.0    8.7
 //   m = 1000 k 768 n 2304             12.0          11.3
+//   m = 4000 k 1024 n 128              6.5          12.7
+//   m = 4000 k 1024 n 512             14.1          13.2
+//   m = 8448 k 10240 n 256            59.0          85.0
 //   m = 300 k 512  gated 2 x 2048      8.9    7.1    8.0
 // Small: to 8 tokens; to 16 (32) tokens while the weights are under 40 M (2 M)
 // values, beyond which its warps' widening of the tokens costs more than the
-// TMEM pipeline's start.  Else to 1024 tokens mid where its modelled time (see
-// mid_consider) is below that of what takes the larger counts: at k <= 512 the
-// kernel with resident weights, 5.5 us and 1 + 0.45 us a stage for each round
-// of its CTAs; beyond, large, 7 us (the widening pass and a second launch) and
-// 0.39 us a stage of each wave of 256 x 128 units (fits of what was measured,
-// to about 20 %; of the rows above and ten others, none is given to a slower
-// kernel).  Resident against large at 16238 tokens (us): k 512, n 1536 bf16 27.9
+// TMEM pipeline's start.  Else mid where its modelled time (see mid_consider)
+// is below that of what takes the larger counts: at k <= 512 the kernel with
+// resident weights, 5.5 us and 1 + 0.45 us a stage for each round of its CTAs;
+// beyond, large, 7 us (two launches), the widening pass's 3 bytes a value at 6
+// TB/s and 0.39 us a stage of each wave of 256 x 128 units (fits of what was
+// measured, to about 20 %; of the rows above and thirty others, one is given to
+// a kernel slower by more than 2 %, 11.3 against 12.1 us).  Resident against large at 16238 tokens (us): k 512, n 1536 bf16 27.9
 // and 34.2; n 512 f32 13.7 and 21.3; gated 2 x 2048 58.1 and 68.7; k 64, n 512
 // f32 10.1 and 19.0.
 enum Path { SMALL, MID, RES, LARGE };
@@ -1188,7 +1192,6 @@ te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
     path = SMALL;
     if (p.m <= 8 || (p.m <= 16 && total * p.k <= (40 << 20)) || (p.m <= 32 && total * p.k <= (2 << 20))) return TE_OK;
     path = p.k <= 512 ? RES : LARGE;
-    if (p.m > 1024) return TE_OK;
     const te_status st = mid_plan<GATED>(plan, tiles, p.m, p.k);
     if (st != TE_OK) return st;
     const int nkb = (p.k + 127) / 128;
@@ -1199,7 +1202,7 @@ te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
         other = 5.5 + rounds * (1.0 + 0.45 * nkb);
     } else {
         const long long waves = ((tiles + 1) / 2 * ttiles + SMS / 2 - 1) / (SMS / 2);
-        other = 7.0 + 0.39 * nkb * waves;
+        other = 7.0 + 0.39 * nkb * waves + (double)p.m * p.k * 3 / 6e6;
     }
     if (p.m <= 32 || plan.us < other) path = MID;
     return TE_OK;
