@@ -215,11 +215,11 @@ te_status small_launch(I8Params &p, cudaStream_t s) {
 }
 // --------------------------------------------------- a middling token count
 //
-// Up to a few hundred tokens, or more with few features, the products are still bound by the weights'
-// bytes or by latency: the wide tiles of the large pipeline (q8_linear.cu) leave
-// SMs idle there, and its activation needs a widening pass of its own.  Here a
-// CTA takes 128 weight rows (TMEM lanes) x N tokens x a share of k, in one
-// launch and without a workspace:
+// Up to a few hundred tokens, or more with few features, the products are
+// still bound by the weights' bytes or by latency: the wide tiles of the large
+// pipeline (q8_linear.cu) leave SMs idle there, and its activation needs a
+// widening pass of its own.  Here a CTA takes 128 weight rows (TMEM lanes) x N
+// tokens x a share of k, in one launch and without a workspace:
 //   * warp 0 streams stages of 128 k by TMA: the int8 weight rows and tokens
 //     (128-byte swizzle);
 //   * groups of four warps from warp 2 on, a lane quadrant a warp, take the stages in turn and
