@@ -48,3 +48,42 @@ def test_many_tokens_are_exact_on_integers(m, k, ns):
         assert torch.equal(y[:m].double(), ref)
         assert bool(torch.isnan(y[m]).all())
     te.check()
+
+
+@pytest.mark.parametrize("m,k", [(5, 512), (13, 1024), (30, 64), (60, 768), (700, 192), (9000, 512), (20000, 64), (3000, 1024)])
+def test_items_of_one_call_of_every_kind_at_once(m, k):
+    # f32 and bf16 outputs, bias, both residuals and both activations in one call,
+    # against a call for each; sums below 2^24 are exact, so the bits are the same
+    torch = _torch()
+    gen = torch.Generator("cuda").manual_seed(m + k)
+    x = torch.randint(-127, 128, (m, k), generator=gen, device="cuda", dtype=torch.int8)
+    xs = torch.rand(m, generator=gen, device="cuda") * 1e-3
+    ns = [512, 96, 288, 32]
+    keep, qw = [], []
+    for i, n in enumerate(ns):
+        w = torch.randint(-127, 128, (n, k), generator=gen, device="cuda", dtype=torch.int8)
+        s, b = torch.rand(n, generator=gen, device="cuda"), torch.randn(n, generator=gen, device="cuda")
+        keep.append((w, s, b))
+        qw.append(te.q8w(w, s, b if i % 2 else None))
+    start = torch.randn(m, 512, generator=gen, device="cuda")
+    sep = torch.randn(m, 288, generator=gen, device="cuda")
+
+    def outputs():
+        return [start.clone(), torch.zeros(m, 96, device="cuda", dtype=torch.bfloat16), torch.zeros(m, 288, device="cuda"),
+                torch.zeros(m, 32, device="cuda", dtype=torch.bfloat16)]
+
+    def item(i, y):
+        d = dict(w=qw[i], y=y, ldy=ns[i])
+        d.update([dict(residual=y, ldr=512), dict(epilogue=te.TE_EPI_SILU), dict(residual=sep, ldr=288),
+                  dict(epilogue=te.TE_EPI_GELU_TANH)][i])
+        return d
+
+    ws = _ws(m, k, sum(ns))
+    together, apart = outputs(), outputs()
+    te.i8_linear(x, xs, [item(i, y) for i, y in enumerate(together)], ws)
+    for i, y in enumerate(apart):
+        te.i8_linear(x, xs, [item(i, y)], ws)
+    te.check()
+    for a, b in zip(together, apart):
+        assert torch.equal(a, b)
+        assert bool((a != 0).any())

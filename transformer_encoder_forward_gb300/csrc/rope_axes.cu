@@ -300,13 +300,17 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3) rope_vec_kernel(c
 
 // Any even sections: the heads of an item pass through shared memory, up to
 // ANY_STG bytes at a time (16-byte loads and stores, single channels in
-// between); lane l turns pairs l, l + 32, ... (NP of them) of each head, four
-// heads at once so that their chains of load, norm and rotation overlap.
+// between); lane l turns pairs l, l + 32, ... (NP of them) of each head, HU heads
+// at once so that their chains of load, norm and rotation overlap.  (Four pairs
+// a lane and several heads side by side in the warp: 8448 x 60 x 128 83 -> 138 us.)
 constexpr int ANY_STG = 4096;
 
 template <typename T, int NP>
-__global__ void __launch_bounds__(256, 4) rope_any_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int HU = NP == 4 ? 2 : 4;         // heads at once
+__global__ void __launch_bounds__(256, NP == 4 ? 3 : 4) rope_any_kernel(const __grid_constant__ RopeParams p) {
+    // heads at once: as many as the registers of four CTAs an SM hold (three
+    // where a lane has four pairs: 2000 rows of 12 heads of 256 24.1 -> 17.9 us;
+    // below, six or eight heads at three CTAs lose 5 to 25 %)
+    constexpr int HU = NP == 4 ? 3 : 4;
     __shared__ __align__(16) uint8_t stage[8][ANY_STG];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     prior_wait();
