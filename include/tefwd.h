@@ -315,8 +315,8 @@ te_status te_quant_rows(const void *x, int32_t xdt, int64_t ldx, int8_t *q, int6
 
 /* rownorm_quant: the pre-norm and the quantisation in one pass: quant_rows of
  *   v = Norm(pre * x) * w (+ b), times (1 + mod_scale) when given
- * (te_rownorm_mod's arithmetic; v stays f32, it is not rounded to bf16
- * between).  x may be f32 or bf16; b: LN only, or NULL; mod_scale f32 [d] or
+ * (te_rownorm_mod's f32 steps in its order, so the same bits from the same row
+ * statistics; v stays f32, it is not rounded to bf16 between).  x may be f32 or bf16; b: LN only, or NULL; mod_scale f32 [d] or
  * NULL.  Sizes and the other arguments as te_quant_rows. */
 te_status te_rownorm_quant(const void *x, int32_t xdt, int64_t ldx, const float *w, const float *b,
                            const float *mod_scale, int32_t kind, float eps, float pre, int8_t *q,

@@ -92,44 +92,24 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x, float *red, int slot, in
     return s;
 }
 
-// Both at once (the maximum returned as the value of its pattern).
-template <int WPR>
-__device__ __forceinline__ float2 row_both(float x, uint32_t y, float *red, int slot, int wr, int lane) {
-    x = warp_sum(x);
-    y = __reduce_max_sync(0xFFFFFFFFu, y);
-    if (WPR == 1) return make_float2(x, __uint_as_float(y));
-    if (lane == 0) {
-        red[2 * wr] = x;
-        red[2 * wr + 1] = __uint_as_float(y);
-    }
-    row_bar<WPR>(slot);
-    float s = red[0];
-    uint32_t m = __float_as_uint(red[1]);
-#pragma unroll
-    for (int i = 1; i < WPR; ++i) {
-        s += red[2 * i];
-        const uint32_t o = __float_as_uint(red[2 * i + 1]);
-        m = o > m ? o : m;
-    }
-    return make_float2(s, __uint_as_float(m));
-}
-
 // WPR warps a row (8 / WPR rows a CTA at a time, persistent over rows), at most
 // NV chunks of 8 columns a thread; the next row's loads are in flight while a
 // row is worked on.  Registers are held to 2-4 CTAs an SM: rows in flight are
-// what hides the row's chain of load, meeting, division and store (f32 8448 x
-// 3840 behind an RMS norm: 29.3 us, 5.5 TB/s; five CTAs with spills 41 us; one
-// row a CTA without the loop 35 us).
+// what hides the row's chain of load, meetings, division and store (f32 8448 x
+// 3840 behind an RMS norm: 28.0 us, 5.8 TB/s; LayerNorm 36.4; five CTAs with
+// spills 41, one row a CTA without the loop 35).  The norm's factor is known
+// before any value is scaled by it: a maximum found in the same meeting as the
+// sum, over x w alone, saves 1 us there and rounds in another order than the
+// norm does.
 template <typename Tin, int NV, int WPR, bool NORM>
 __global__ void __launch_bounds__(256, NV == 8 ? 2 : (NV == 4 || (NV == 2 && WPR == 1) ? 3 : 4))
     quant_kernel(const Tin *x, long long ldx, const float *w, const float *b, const float *ms, int kind, float eps, float pre,
                  int8_t *__restrict__ q, long long ldq, float *__restrict__ scale, int t, int d) {
     prior_wait();
     constexpr int TPR = 32 * WPR, RPC = 8 / WPR;
-    __shared__ float red[2][8 / WPR][2 * WPR];
+    __shared__ float red[2][8 / WPR][WPR];
     const int slot = threadIdx.x / TPR, tid = threadIdx.x % TPR;
     const int wr = tid >> 5, lane = tid & 31;
-    const float inv_d = 1.f / (float)d;
     int flip = 0;
     Raw8<Tin> nx[NV];
     auto fetch = [&](long long row) {
@@ -149,84 +129,62 @@ __global__ void __launch_bounds__(256, NV == 8 ? 2 : (NV == 4 || (NV == 2 && WPR
         for (int i = 0; i < NV; ++i) nx[i].get(v[i]);
         const long long after = row + (long long)gridDim.x * RPC;
         if (after < t) fetch(after);
-        float top = 0.f, inv = 1.f;
-        uint32_t mx;
-        if (NORM && pre != 1.f) {
+        if (NORM) {
+            // te_rownorm_mod's steps in its order, each rounded as there: x pre,
+            // (x - mean) inv, times w (plus b), times 1 + s
+            if (pre != 1.f) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+                for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] *= pre;
-        }
-        if (NORM && kind == TE_NORM_RMS) {
-            // v = (x w (1 + s)) inv: the largest |x w (1 + s)| is found together with
-            // the sum of squares, one meeting of the row's warps for both
-            float s2 = 0.f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * TPR + tid) * 8;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s2 = fmaf(v[i][e], v[i][e], s2);
-                if (c >= d) continue;
-                float wv[8];
-                load8_vec(w + c, wv);
-                if (ms) {
-                    float mv[8];
-                    load8_vec(ms + c, mv);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) wv[e] *= 1.f + mv[e];
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] *= wv[e];
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) top = max3_abs_nan(top, v[i][e], v[i][e + 1]);
+                    for (int e = 0; e < 8; ++e) v[i][e] *= pre;
             }
-            const float2 r = row_both<WPR>(s2, __float_as_uint(top) & 0x7FFFFFFFu, red[flip ^= 1][slot], slot, wr, lane);
-            inv = rsqrtf(fmaf(r.x, inv_d, eps));
-            // rounding keeps the order: the largest of the products with inv
-            mx = __float_as_uint(r.y * inv) & 0x7FFFFFFFu;
-        } else {
-            if (NORM) {
-                float s = 0.f, s2 = 0.f;
+            if (kind == TE_NORM_LN) {
+                float s = 0.f;
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) s += v[i][e];
-                const float mean = row_sum<WPR>(s, red[flip ^= 1][slot], slot, wr, lane) * inv_d;
+                const float mean = row_sum<WPR>(s, red[flip ^= 1][slot], slot, wr, lane) / (float)d;
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if ((i * TPR + tid) * 8 < d)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            v[i][e] -= mean;
-                            s2 = fmaf(v[i][e], v[i][e], s2);
-                        }
-                const float is = rsqrtf(fmaf(row_sum<WPR>(s2, red[flip ^= 1][slot], slot, wr, lane), inv_d, eps));
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int c = (i * TPR + tid) * 8;
-                    if (c >= d) continue;
-                    float wv[8];
-                    load8_vec(w + c, wv);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[i][e] *= is * wv[e];
-                    if (b) {
-                        load8_vec(b + c, wv);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[i][e] += wv[e];
-                    }
-                    if (ms) {
-                        load8_vec(ms + c, wv);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[i][e] *= 1.f + wv[e];
-                    }
-                }
+                        for (int e = 0; e < 8; ++e) v[i][e] -= mean;
             }
+            float s2 = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) top = max3_abs_nan(top, v[i][e], v[i][e + 1]);
-            mx = row_max<WPR>(__float_as_uint(top) & 0x7FFFFFFFu, red[flip ^= 1][slot], slot, wr, lane);
+                for (int e = 0; e < 8; ++e) s2 = fmaf(v[i][e], v[i][e], s2);
+            const float inv = rsqrtf(row_sum<WPR>(s2, red[flip ^= 1][slot], slot, wr, lane) / (float)d + eps);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TPR + tid) * 8;
+                if (c >= d) continue;
+                float wv[8];
+                load8_vec(w + c, wv);
+                if (b) {
+                    float bv[8];
+                    load8_vec(b + c, bv);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[i][e] = fmaf(v[i][e] * inv, wv[e], bv[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * inv * wv[e];
+                }
+                if (ms) {
+                    load8_vec(ms + c, wv);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[i][e] *= 1.f + wv[e];
+                }
+            }
         }
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) top = max3_abs_nan(top, v[i][e], v[i][e + 1]);
+        const uint32_t mx = row_max<WPR>(__float_as_uint(top) & 0x7FFFFFFFu, red[flip ^= 1][slot], slot, wr, lane);
         // below 2^-120 the row counts as zero (127 / a would leave f32's range);
         // from the infinity's pattern up it holds a value that is not finite
         const bool finite = mx < 0x7F800000u, zero = mx < 0x03800000u;
@@ -246,8 +204,7 @@ __global__ void __launch_bounds__(256, NV == 8 ? 2 : (NV == 4 || (NV == 2 && WPR
                 uint32_t r[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    r[e] = __float_as_uint(
-                        __fadd_rn(__fmul_rn(NORM ? __fmul_rn(v[i][4 * h + e], inv) : v[i][4 * h + e], up), 12582912.f));
+                    r[e] = __float_as_uint(__fadd_rn(__fmul_rn(v[i][4 * h + e], up), 12582912.f));
                 o[h] = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
             }
             *reinterpret_cast<uint2 *>(qr + c) = finite ? make_uint2(o[0], o[1]) : make_uint2(0u, 0u);
