@@ -338,12 +338,14 @@ def _marshalling():
     global _m
     if _m is None:
         import torch  # noqa: F401  (its libraries first)
-        lib()
+        L = lib()
         try:
             from . import _marshal as mod
         except ImportError as e:
             raise RuntimeError("_marshal.so is not built; run "
                                "python -m transformer_encoder_forward_gb300.build") from e
+        mod.bind(*(ctypes.cast(f, c_p).value for f in (L.te_quant_rows, L.te_rownorm_quant, L.te_i8_linear,
+                                                       L.te_i8_gated_linear, L.te_qk_rope_axes)))
         _m = mod
     return _m
 

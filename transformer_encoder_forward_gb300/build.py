@@ -4,7 +4,7 @@ binding's marshalling module next to it.
 Each CUDA translation unit compiles in parallel to an object under _build/,
 then one nvcc link produces the shared library (CUDA runtime linked
 statically).  The marshalling module (csrc/marshal.cpp: a CPython extension
-over PyTorch's headers) compiles beside them and links against it.  Run
+over PyTorch's headers) compiles beside them.  Run
 ``python -m transformer_encoder_forward_gb300.build``.
 """
 from __future__ import annotations
@@ -48,8 +48,7 @@ def _marshal_flags():
             "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
             "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"]]
     libs = os.path.join(root, "lib")
-    link = ["-L", PKG, "-ltefwd", "-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
-            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    link = ["-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{libs}"]
     return comp, link
 
 
@@ -92,7 +91,7 @@ def build(verbose: bool = False, force: bool = False, extra=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(jobs) or 1) as ex:
         list(ex.map(run, jobs))
     if force or cuda_jobs or _stale(LIB, objs):
-        run([cc, *ARCH, "-shared", "-Xlinker", "-soname=libtefwd.so", "-o", LIB + ".tmp", *objs])
+        run([cc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs])
         os.replace(LIB + ".tmp", LIB)
     if force or _stale(MARSHAL, [m_obj]):
         run([cxx, "-shared", "-o", MARSHAL + ".tmp", m_obj, *link])

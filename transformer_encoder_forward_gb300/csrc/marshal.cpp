@@ -3,6 +3,9 @@
 // PyTorch's C++ interface (a read of each through Python costs as much as a
 // launch), checks them and calls the C ABI.  Holds no arithmetic.  Every
 // function returns the te_status; the Python side raises for it.
+// The C ABI's functions are the ones of the library that the binding has
+// loaded: it hands over their addresses once (bind), so the module is linked
+// against no second copy.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -17,6 +20,14 @@
 #include "tefwd.h"
 
 namespace {
+
+struct {
+    decltype(&te_quant_rows) quant_rows;
+    decltype(&te_rownorm_quant) rownorm_quant;
+    decltype(&te_i8_linear) i8_linear;
+    decltype(&te_i8_gated_linear) i8_gated_linear;
+    decltype(&te_qk_rope_axes) qk_rope_axes;
+} abi;
 
 struct PyError {};   // a Python exception is set
 
@@ -151,8 +162,8 @@ PyObject *quant_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Arg x = want("quant_rows: x", a[0], F32 | BF16, 2, -1, -1);
         const Arg q = want("quant_rows: q", a[1], I8, 2, x.rows, x.cols);
         const Arg s = want("quant_rows: scale", a[2], F32, 1, 1, x.rows);
-        return te_quant_rows(x.ptr, x.dtype, x.ld, static_cast<int8_t *>(q.ptr), q.ld, static_cast<float *>(s.ptr),
-                             (int32_t)x.rows, (int32_t)x.cols, stream_of(a[3]));
+        return abi.quant_rows(x.ptr, x.dtype, x.ld, static_cast<int8_t *>(q.ptr), q.ld, static_cast<float *>(s.ptr),
+                              (int32_t)x.rows, (int32_t)x.cols, stream_of(a[3]));
     });
 }
 
@@ -166,10 +177,10 @@ PyObject *rownorm_quant(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Arg q = want("rownorm_quant: q", a[5], I8, 2, x.rows, x.cols);
         const Arg s = want("rownorm_quant: scale", a[6], F32, 1, 1, x.rows);
         const void *m = opt("rownorm_quant: mod_scale", a[8], F32, x.cols);
-        return te_rownorm_quant(x.ptr, x.dtype, x.ld, static_cast<const float *>(w), static_cast<const float *>(b),
-                                static_cast<const float *>(m), int32_of(a[3]), real(a[4]), real(a[7]),
-                                static_cast<int8_t *>(q.ptr), q.ld, static_cast<float *>(s.ptr), (int32_t)x.rows,
-                                (int32_t)x.cols, stream_of(a[9]));
+        return abi.rownorm_quant(x.ptr, x.dtype, x.ld, static_cast<const float *>(w), static_cast<const float *>(b),
+                                 static_cast<const float *>(m), int32_of(a[3]), real(a[4]), real(a[7]),
+                                 static_cast<int8_t *>(q.ptr), q.ld, static_cast<float *>(s.ptr), (int32_t)x.rows,
+                                 (int32_t)x.cols, stream_of(a[9]));
     });
 }
 
@@ -224,8 +235,8 @@ PyObject *i8_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         Py_DECREF(seq);
         size_t nb;
         void *ws = scratch("i8_linear", a[3], nb);
-        return te_i8_linear(static_cast<const int8_t *>(x.ptr), x.ld, static_cast<const float *>(s.ptr),
-                            (int32_t)x.rows, (int32_t)x.cols, items, (int32_t)z, ws, nb, stream_of(a[4]));
+        return abi.i8_linear(static_cast<const int8_t *>(x.ptr), x.ld, static_cast<const float *>(s.ptr),
+                             (int32_t)x.rows, (int32_t)x.cols, items, (int32_t)z, ws, nb, stream_of(a[4]));
     });
 }
 
@@ -240,9 +251,9 @@ PyObject *i8_gated_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Arg o = want("i8_gated_linear: out", a[5], BF16, 2, x.rows, wg.n);
         size_t nb;
         void *ws = scratch("i8_gated_linear", a[6], nb);
-        return te_i8_gated_linear(static_cast<const int8_t *>(x.ptr), x.ld, static_cast<const float *>(s.ptr),
-                                  (int32_t)x.rows, (int32_t)x.cols, &wg, &wu, int32_of(a[4]), o.ptr, o.ld, ws, nb,
-                                  stream_of(a[7]));
+        return abi.i8_gated_linear(static_cast<const int8_t *>(x.ptr), x.ld, static_cast<const float *>(s.ptr),
+                                   (int32_t)x.rows, (int32_t)x.cols, &wg, &wu, int32_of(a[4]), o.ptr, o.ld, ws, nb,
+                                   stream_of(a[7]));
     });
 }
 
@@ -262,14 +273,33 @@ PyObject *qk_rope_axes(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (end > src.cols || end > dst.cols)
             raise(PyExc_ValueError, "qk_rope_axes: the heads end at column " + std::to_string(end) + " of " +
                                         std::to_string(std::min(src.cols, dst.cols)));
-        return te_qk_rope_axes(src.ptr, lds, dst.ptr, ldd, src.dtype, q_off, k_off, nq, nkv, hd,
-                               static_cast<const float *>(opt("qk_rope_axes: qn", a[9], F32, hd)),
-                               static_cast<const float *>(opt("qk_rope_axes: kn", a[10], F32, hd)), real(a[11]), &plan,
-                               static_cast<const int32_t *>(pos.ptr), pos.ld, real(a[14]), rows, stream_of(a[16]));
+        return abi.qk_rope_axes(src.ptr, lds, dst.ptr, ldd, src.dtype, q_off, k_off, nq, nkv, hd,
+                                static_cast<const float *>(opt("qk_rope_axes: qn", a[9], F32, hd)),
+                                static_cast<const float *>(opt("qk_rope_axes: kn", a[10], F32, hd)), real(a[11]), &plan,
+                                static_cast<const int32_t *>(pos.ptr), pos.ld, real(a[14]), rows, stream_of(a[16]));
+    });
+}
+
+// bind(addresses of te_quant_rows, te_rownorm_quant, te_i8_linear, te_i8_gated_linear, te_qk_rope_axes)
+PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        count(n, 5);
+        void *f[5];
+        for (int i = 0; i < 5; ++i) {
+            f[i] = PyLong_AsVoidPtr(a[i]);
+            if (!f[i]) raise(PyExc_ValueError, "bind: not a function's address");
+        }
+        abi.quant_rows = reinterpret_cast<decltype(abi.quant_rows)>(f[0]);
+        abi.rownorm_quant = reinterpret_cast<decltype(abi.rownorm_quant)>(f[1]);
+        abi.i8_linear = reinterpret_cast<decltype(abi.i8_linear)>(f[2]);
+        abi.i8_gated_linear = reinterpret_cast<decltype(abi.i8_gated_linear)>(f[3]);
+        abi.qk_rope_axes = reinterpret_cast<decltype(abi.qk_rope_axes)>(f[4]);
+        return TE_OK;
     });
 }
 
 PyMethodDef methods[] = {
+    {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, nullptr},
     {"quant_rows", (PyCFunction)(void (*)(void))quant_rows, METH_FASTCALL, nullptr},
     {"rownorm_quant", (PyCFunction)(void (*)(void))rownorm_quant, METH_FASTCALL, nullptr},
     {"i8_linear", (PyCFunction)(void (*)(void))i8_linear, METH_FASTCALL, nullptr},
