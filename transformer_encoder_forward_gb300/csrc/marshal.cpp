@@ -1,8 +1,10 @@
 // Argument marshalling of the binding's calls whose device time is a few
 // microseconds: reads the tensors' addresses, sizes and types through
 // PyTorch's C++ interface (a read of each through Python costs as much as a
-// launch), checks them and calls the C ABI.  Holds no arithmetic.  Every
-// function returns the te_status; the Python side raises for it.
+// launch), checks them and calls the C ABI, without the interpreter's lock (a
+// launch may wait for room in its stream, behind a callback that needs the
+// lock).  Holds no arithmetic.  Every function returns the te_status; the Python
+// side raises for it.
 // The C ABI's functions are the ones of the library that the binding has
 // loaded: it hands over their addresses once (bind), so the module is linked
 // against no second copy.
@@ -155,6 +157,16 @@ PyObject *guarded(F f) {
     }
 }
 
+// Runs f, a call of the C ABI on arguments that were read before, while other
+// Python threads may run.
+template <typename F>
+te_status unlocked(F f) {
+    PyThreadState *state = PyEval_SaveThread();
+    const te_status st = f();
+    PyEval_RestoreThread(state);
+    return st;
+}
+
 // quant_rows(x, q, scale, stream)
 PyObject *quant_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
@@ -162,8 +174,11 @@ PyObject *quant_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Arg x = want("quant_rows: x", a[0], F32 | BF16, 2, -1, -1);
         const Arg q = want("quant_rows: q", a[1], I8, 2, x.rows, x.cols);
         const Arg s = want("quant_rows: scale", a[2], F32, 1, 1, x.rows);
-        return abi.quant_rows(x.ptr, x.dtype, x.ld, static_cast<int8_t *>(q.ptr), q.ld, static_cast<float *>(s.ptr),
-                              (int32_t)x.rows, (int32_t)x.cols, stream_of(a[3]));
+        te_stream stream = stream_of(a[3]);
+        return unlocked([&] {
+            return abi.quant_rows(x.ptr, x.dtype, x.ld, static_cast<int8_t *>(q.ptr), q.ld, static_cast<float *>(s.ptr),
+                                  (int32_t)x.rows, (int32_t)x.cols, stream);
+        });
     });
 }
 
@@ -177,10 +192,14 @@ PyObject *rownorm_quant(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Arg q = want("rownorm_quant: q", a[5], I8, 2, x.rows, x.cols);
         const Arg s = want("rownorm_quant: scale", a[6], F32, 1, 1, x.rows);
         const void *m = opt("rownorm_quant: mod_scale", a[8], F32, x.cols);
-        return abi.rownorm_quant(x.ptr, x.dtype, x.ld, static_cast<const float *>(w), static_cast<const float *>(b),
-                                 static_cast<const float *>(m), int32_of(a[3]), real(a[4]), real(a[7]),
-                                 static_cast<int8_t *>(q.ptr), q.ld, static_cast<float *>(s.ptr), (int32_t)x.rows,
-                                 (int32_t)x.cols, stream_of(a[9]));
+        const int32_t kind = int32_of(a[3]);
+        const float eps = real(a[4]), pre = real(a[7]);
+        te_stream stream = stream_of(a[9]);
+        return unlocked([&] {
+            return abi.rownorm_quant(x.ptr, x.dtype, x.ld, static_cast<const float *>(w), static_cast<const float *>(b),
+                                     static_cast<const float *>(m), kind, eps, pre, static_cast<int8_t *>(q.ptr), q.ld,
+                                     static_cast<float *>(s.ptr), (int32_t)x.rows, (int32_t)x.cols, stream);
+        });
     });
 }
 
@@ -235,8 +254,11 @@ PyObject *i8_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         Py_DECREF(seq);
         size_t nb;
         void *ws = scratch("i8_linear", a[3], nb);
-        return abi.i8_linear(static_cast<const int8_t *>(x.ptr), x.ld, static_cast<const float *>(s.ptr),
-                             (int32_t)x.rows, (int32_t)x.cols, items, (int32_t)z, ws, nb, stream_of(a[4]));
+        te_stream stream = stream_of(a[4]);
+        return unlocked([&] {
+            return abi.i8_linear(static_cast<const int8_t *>(x.ptr), x.ld, static_cast<const float *>(s.ptr),
+                                 (int32_t)x.rows, (int32_t)x.cols, items, (int32_t)z, ws, nb, stream);
+        });
     });
 }
 
@@ -251,9 +273,12 @@ PyObject *i8_gated_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Arg o = want("i8_gated_linear: out", a[5], BF16, 2, x.rows, wg.n);
         size_t nb;
         void *ws = scratch("i8_gated_linear", a[6], nb);
-        return abi.i8_gated_linear(static_cast<const int8_t *>(x.ptr), x.ld, static_cast<const float *>(s.ptr),
-                                   (int32_t)x.rows, (int32_t)x.cols, &wg, &wu, int32_of(a[4]), o.ptr, o.ld, ws, nb,
-                                   stream_of(a[7]));
+        const int32_t act = int32_of(a[4]);
+        te_stream stream = stream_of(a[7]);
+        return unlocked([&] {
+            return abi.i8_gated_linear(static_cast<const int8_t *>(x.ptr), x.ld, static_cast<const float *>(s.ptr),
+                                       (int32_t)x.rows, (int32_t)x.cols, &wg, &wu, act, o.ptr, o.ld, ws, nb, stream);
+        });
     });
 }
 
@@ -273,10 +298,14 @@ PyObject *qk_rope_axes(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (end > src.cols || end > dst.cols)
             raise(PyExc_ValueError, "qk_rope_axes: the heads end at column " + std::to_string(end) + " of " +
                                         std::to_string(std::min(src.cols, dst.cols)));
-        return abi.qk_rope_axes(src.ptr, lds, dst.ptr, ldd, src.dtype, q_off, k_off, nq, nkv, hd,
-                                static_cast<const float *>(opt("qk_rope_axes: qn", a[9], F32, hd)),
-                                static_cast<const float *>(opt("qk_rope_axes: kn", a[10], F32, hd)), real(a[11]), &plan,
-                                static_cast<const int32_t *>(pos.ptr), pos.ld, real(a[14]), rows, stream_of(a[16]));
+        const float *qn = static_cast<const float *>(opt("qk_rope_axes: qn", a[9], F32, hd));
+        const float *kn = static_cast<const float *>(opt("qk_rope_axes: kn", a[10], F32, hd));
+        const float eps = real(a[11]), q_mul = real(a[14]);
+        te_stream stream = stream_of(a[16]);
+        return unlocked([&] {
+            return abi.qk_rope_axes(src.ptr, lds, dst.ptr, ldd, src.dtype, q_off, k_off, nq, nkv, hd, qn, kn, eps, &plan,
+                                    static_cast<const int32_t *>(pos.ptr), pos.ld, q_mul, rows, stream);
+        });
     });
 }
 
