@@ -8,6 +8,9 @@
 // src/gpu_metal/zimage.rs" Enc::gemm, Enc::block SwiGLU; "cortiq-engine 0.8.39
 // src/gpu_metal/egemma2.rs" Prog::mm) with the activation narrowed as the
 // weights are.
+#include <atomic>
+#include <mutex>
+
 #include "common.cuh"
 
 namespace tefwd {
@@ -540,37 +543,41 @@ void mid_consider(MidPlan &best, int ftiles, int m, int nkb, const int *resident
 }
 
 // Resident clusters of 1, 2, 4 and 8 CTAs of the kernel on the current device,
-// asked for once (and its shared memory size set).
+// asked for once (and its shared memory size set).  A device's row is read only
+// once it is whole: first calls may come from several threads.
 template <int N, bool GATED>
 te_status mid_residents(const int *&out) {
     static int table[64][9] = {};
+    static std::atomic<bool> whole[64] = {};
+    static std::mutex filling;
     constexpr int smem = Mid<N>::BYTES + 1024;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cuda_fail(e, "i8_linear: device");
-    int *t = table[dev];
-    if (!t[1]) {
-        e = cudaFuncSetAttribute(i8_mid_kernel<N, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return cuda_fail(e, "i8_linear: set shared memory size");
-        for (int s = 8; s >= 1; s /= 2) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(8 * SMS, 1, 1);
-            cfg.blockDim = dim3(Mid<N>::THREADS, 1, 1);
-            cfg.dynamicSmemBytes = smem;
-            cudaLaunchAttribute attr;
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = s;
-            attr.val.clusterDim.y = 1;
-            attr.val.clusterDim.z = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            int n = 0;
-            e = cudaOccupancyMaxActiveClusters(&n, i8_mid_kernel<N, GATED>, &cfg);
-            if (e != cudaSuccess || n < 1) return cuda_fail(e, "i8_linear: cluster occupancy");
-            t[s] = n;
-        }
+    int *t = out = table[dev];
+    if (whole[dev].load(std::memory_order_acquire)) return TE_OK;
+    const std::lock_guard<std::mutex> lock(filling);
+    if (whole[dev].load(std::memory_order_relaxed)) return TE_OK;
+    e = cudaFuncSetAttribute(i8_mid_kernel<N, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_fail(e, "i8_linear: set shared memory size");
+    for (int s = 8; s >= 1; s /= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(8 * SMS, 1, 1);
+        cfg.blockDim = dim3(Mid<N>::THREADS, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = s;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, i8_mid_kernel<N, GATED>, &cfg);
+        if (e != cudaSuccess || n < 1) return cuda_fail(e, "i8_linear: cluster occupancy");
+        t[s] = n;
     }
-    out = t;
+    whole[dev].store(true, std::memory_order_release);
     return TE_OK;
 }
 
@@ -1070,7 +1077,7 @@ __global__ void __launch_bounds__(Res::THREADS, 1) i8_res_kernel(const __grid_co
 template <bool GATED>
 te_status res_launch(const I8Params &q, cudaStream_t s) {
     constexpr int F = GATED ? 64 : 128, smem = Res::BYTES + 1024;
-    static bool ready[64] = {};
+    static std::atomic<bool> ready[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cuda_fail(e, "i8_linear: device");

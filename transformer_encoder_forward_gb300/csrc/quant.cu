@@ -13,6 +13,8 @@
 // The maximum propagates NaNs, and its bit pattern, as an integer, orders like
 // the values with infinities and NaNs above every finite one: one maximum finds
 // the row's largest magnitude and whether any value is not finite.
+#include <atomic>
+
 #include "common.cuh"
 
 namespace tefwd {
@@ -217,7 +219,7 @@ template <typename Tin, auto KERN, int RPC>
 te_status go(const void *x, int64_t ldx, const float *w, const float *b, const float *ms, int kind, float eps,
              float pre, int8_t *q, int64_t ldq, float *scale, int t, int d, cudaStream_t s) {
     // resident CTAs of the whole device, asked for once a kernel and device
-    static int resident[64] = {};
+    static std::atomic<int> resident[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cuda_fail(e, "quant: device");
@@ -228,8 +230,8 @@ te_status go(const void *x, int64_t ldx, const float *w, const float *b, const f
         if (e != cudaSuccess || per < 1) return cuda_fail(e, "quant: occupancy");
         resident[dev] = sms * per;
     }
-    const long long need = ((long long)t + RPC - 1) / RPC;
-    e = launch_close(KERN, dim3((unsigned)(need < resident[dev] ? need : resident[dev])), 256, 0, s, 1,
+    const long long need = ((long long)t + RPC - 1) / RPC, most = resident[dev];
+    e = launch_close(KERN, dim3((unsigned)(need < most ? need : most)), 256, 0, s, 1,
                      static_cast<const Tin *>(x), ldx, w, b, ms, kind, eps, pre, q, ldq, scale, t, d);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "quant launch");
 }

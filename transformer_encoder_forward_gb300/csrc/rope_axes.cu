@@ -16,6 +16,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace tefwd {
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(256, NP == 4 ? 3 : 4) rope_any_kernel(const __
 template <auto KERN, bool FINE = false>
 te_status launch(RopeParams &p, int rows, int hpi, cudaStream_t s) {
     // resident CTAs of the whole device, asked for once a kernel and device
-    static int resident[64] = {};
+    static std::atomic<int> resident[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cuda_fail(e, "qk_rope_axes: device");
