@@ -554,7 +554,8 @@ te_status mid_residents(const int *&out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cuda_fail(e, "i8_linear: device");
-    int *t = out = table[dev];
+    int *t = table[dev];
+    out = t;
     if (whole[dev].load(std::memory_order_acquire)) return TE_OK;
     const std::lock_guard<std::mutex> lock(filling);
     if (whole[dev].load(std::memory_order_relaxed)) return TE_OK;
