@@ -389,7 +389,9 @@ typedef struct {
  *   freq != NULL: f_p = freq[p], p = 0..rot/2-1 in section order (finite, >= 0)
  *   whole == 0:   f = theta^(-2i/sections[a]) for pair i of axis a
  *   whole != 0:   f = theta^(-2p/rot), p counted over the whole head
- * (theta > 0).  Host only; no device is touched. */
+ * (theta > 0), each f_p an f64 (the powers as C's pow rounds them), however
+ * large; turn[p] is the word nearest to f_p / (2 pi).  TE_EINVAL where a power
+ * is past an f64.  Host only; no device is touched. */
 te_status te_rope_axes_init(te_rope_axes *plan, int32_t hd, int32_t axes, const int32_t *sections,
                             double theta, int32_t whole, int32_t pairing, const double *freq);
 
@@ -403,8 +405,8 @@ te_status te_rope_axes_init(te_rope_axes *plan, int32_t hd, int32_t axes, const 
  * (f32 [hd]); pair p then turns by pos[r, axis[p]] * f_p; q heads are
  * multiplied by q_mul.  f32 arithmetic, rounded once.
  * pos: int32 [rows, ldp] (device, ldp >= axes), any value, negative too: the
- * angle is reduced exactly (64-bit fixed point), so far positions lose
- * nothing.  It generalises te_qk_prep_rope ([EG2] EgQkv.sec, [ZI] Enc::block)
+ * angle is within 2^-31 turns of pos * f_p before f32 rounds it (64-bit fixed
+ * point), however far the position and whatever the f64 f_p.  It generalises te_qk_prep_rope ([EG2] EgQkv.sec, [ZI] Enc::block)
  * to sections of different widths, with no tables.
  * Rows (ld_src, ld_dst) and head offsets must be multiples of 16 bytes. */
 te_status te_qk_rope_axes(const void *src, int64_t ld_src, void *dst, int64_t ld_dst, int32_t dt,

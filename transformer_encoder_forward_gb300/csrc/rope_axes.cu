@@ -5,10 +5,11 @@
 // Angles are kept as 64-bit fixed-point fractions of a turn: f_p / (2 pi) as a
 // word of 2^-64 turns (te_rope_axes.turn), times the position, modulo 2^64.
 // The integer product wraps exactly where whole turns do, so the reduction
-// loses nothing however far the position (the word itself is within 2^-53 of
-// f_p, so 2^20 positions out an angle is off by about 2^-33 turns); its top
-// 32 bits, read as a signed fraction, give sine and cosine by sincospif.  No
-// table is read and no 64-bit float is touched on the device.
+// loses nothing however far the position.  The word is the nearest one to
+// f_p / (2 pi) for the f64 f_p of any size (see turn_word), so the product is within
+// 2^-34 turns of pos * f_p at the furthest int32 positions; its top 32 bits
+// (2^-32 turns), read as a signed fraction, give sine and cosine by sincospif.
+// No table is read and no 64-bit float is touched on the device.
 //
 // Generalises the 1-D and 2-D rotation of "cortiq-engine 0.8.39
 // src/gpu_metal/egemma2.rs" (Prog::qkv, EgQkv.sec) and "cortiq-engine 0.7.6
@@ -527,6 +528,32 @@ te_status run(RopeParams &p, const te_rope_axes &pl, int rows, cudaStream_t s) {
     return hd <= 128 ? launch<rope_any_kernel<T, 2>>(p, rows, 1, s) : launch<rope_any_kernel<T, 4>>(p, rows, 1, s);
 }
 
+// f / (2 pi) in 2^-64 turns, modulo whole turns, to the nearest (f finite, >= 0).
+// The method is Payne and Hanek's (1983): f = M 2^e with a 53-bit integer M, and
+// of the bits of 1 / (2 pi) those left of e give whole turns, those right of
+// e + 128 less than 2^-11 units; the 128 between, times M, are an exact integer
+// product.  A product in f64 would be off by 2^-53 of f: 1e-4 turns at f = 1000
+// and position 2^30.
+uint64_t turn_word(double f) {
+    // the fraction bits of 1 / (2 pi), first ones first (from Machin's formula)
+    static const uint64_t bits[18] = {
+        0x28be60db9391054aull, 0x7f09d5f47d4d3770ull, 0x36d8a5664f10e410ull, 0x7f9458eaf7aef158ull, 0x6dc91b8e909374b8ull,
+        0x01924bba82746487ull, 0x3f877ac72c4a69cfull, 0xba208d7d4baed121ull, 0x3a671c09ad17df90ull, 0x4e64758e60d4ce7dull,
+        0x272117e2ef7e4a0eull, 0xc7fe25fff7816603ull, 0xfbcbc462d6829b47ull, 0xdb4d9fb3c9f2c26dull, 0xd3d18fd9a797fa8bull,
+        0x5d49eeb1faf97c5eull, 0xcf41ce7de294a4baull, 0x9afed7ec47e35742ull};
+    int e;
+    const uint64_t m = (uint64_t)ldexp(frexp(f, &e), 53);
+    e -= 53;                                    // -1126 .. 971
+    unsigned __int128 x = 0;                    // bits e .. e + 127 behind the point, zero ahead of it
+    for (int i = 0; i < 18; ++i) {
+        const int sh = e + 64 - 64 * i;         // word i's place: its last bit is worth 2^sh
+        if (sh >= 128 || sh <= -64) continue;
+        x += sh >= 0 ? (unsigned __int128)bits[i] << sh : (unsigned __int128)(bits[i] >> -sh);
+    }
+    const unsigned __int128 prod = x * m;       // modulo 2^128: whole turns go
+    return (uint64_t)((prod + ((unsigned __int128)1 << 63)) >> 64);
+}
+
 // A plan whose fields the kernels may index by.
 te_status check_plan(const te_rope_axes *pl, int32_t hd) {
     if (pl->hd != hd) return fail(TE_ESHAPE, "qk_rope_axes: plan for hd=%d, heads of %d", pl->hd, hd);
@@ -571,23 +598,27 @@ extern "C" te_status te_rope_axes_init(te_rope_axes *plan, int32_t hd, int32_t a
         rot += sections[a];
     }
     if (rot > hd) return fail(TE_ESHAPE, "rope_axes_init: sections hold %lld channels, a head %d", (long long)rot, hd);
-    for (int p = 0; freq && p < rot / 2; ++p)
-        if (!(freq[p] >= 0.0 && freq[p] < HUGE_VAL))
-            return fail(TE_EINVAL, "rope_axes_init: freq[%d] must be finite and >= 0", p);
+    double f[TE_ROPE_MAX_PAIRS];
+    int p = 0;
+    for (int a = 0; a < axes; ++a)
+        for (int i = 0; i < sections[a] / 2; ++i, ++p) {
+            const double e = whole ? 2.0 * p / (double)rot : 2.0 * i / (double)sections[a];
+            f[p] = freq ? freq[p] : pow(theta, -e);
+            if (!(f[p] >= 0.0 && f[p] < HUGE_VAL))
+                return freq ? fail(TE_EINVAL, "rope_axes_init: freq[%d] must be finite and >= 0", p)
+                            : fail(TE_EINVAL, "rope_axes_init: theta^-%g is past an f64", e);
+        }
     memset(plan, 0, sizeof(*plan));
     plan->hd = hd;
     plan->axes = axes;
     plan->pairs = (int32_t)(rot / 2);
     plan->pairing = pairing;
-    int p = 0;
+    p = 0;
     for (int a = 0; a < axes; ++a) {
         plan->sections[a] = sections[a];
         for (int i = 0; i < sections[a] / 2; ++i, ++p) {
-            const double e = whole ? 2.0 * p / (double)rot : 2.0 * i / (double)sections[a];
-            const double f = freq ? freq[p] : pow(theta, -e);
-            const double turns = f * 0.15915494309189535;        // / 2 pi
             plan->axis[p] = (uint8_t)a;
-            plan->turn[p] = (uint64_t)ldexp(turns - floor(turns), 64);   // < 2^64: an f64 below 1
+            plan->turn[p] = turn_word(f[p]);
         }
     }
     return TE_OK;
