@@ -290,6 +290,12 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
                  : "memory");
 }
 
+__device__ __forceinline__ int ld_shared_cluster(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 template <int BN, bool GATED, int TPA, bool I8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     q8_gemm_kernel(const __grid_constant__ Params p) {
@@ -346,15 +352,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
         mbar_init(bar_done, 1);
         fence_mbar_init();
-        s_skip = *reinterpret_cast<volatile int *>(&g_gemm_err) != 0;
+        if (!I8) s_skip = *reinterpret_cast<volatile int *>(&g_gemm_err) != 0;
     }
     if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), L::TMEM_COLS);
+    if constexpr (I8) {
+        // this kernel may start before the one ahead of it has ended: the word,
+        // like all else, is read behind the wait
+        prior_wait();
+        if (threadIdx.x == 0) s_skip = *reinterpret_cast<volatile int *>(&g_gemm_err) != 0;
+    }
     tc_fence_before();
     cluster_sync();            // both CTAs' barriers exist before any remote arrival
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    if constexpr (I8) prior_wait();
-    bool ok = s_skip == 0;
+    // I8: both CTAs of the pair do as the leader read, even if a product of
+    // another stream fails between the two reads (one of them would wait alone)
+    const bool skip = (I8 ? ld_shared_cluster(mapa_shared(smem_u32(&s_skip), 0)) : s_skip) != 0;
+    bool ok = !skip;
     const int nunits = ok ? p.nunits : 0;
     // the leader's copies of the pair-wide barriers, as cluster addresses
     const uint32_t afull_ldr = mapa_shared(bar_afull, 0);
@@ -1129,7 +1143,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         bulk_wait_all();
         __syncwarp();
     }
-    if (!ok && s_skip == 0) atomicExch(&g_gemm_err, 1);
+    if (!ok && !(I8 ? skip : s_skip != 0)) atomicExch(&g_gemm_err, 1);
     tc_fence_before();
     __syncthreads();
     // the leader's MMAs write both CTAs' TMEM: both wait for them before freeing it
