@@ -1249,8 +1249,11 @@ te_status check_ws(const char *what, const void *ws, size_t have, size_t need) {
 
 using namespace tefwd;
 
-// the f16 activation of a call that widens it beforehand, whatever n
-static size_t workspace_of(int32_t m, int32_t k) { return m <= 8 || m > MAX_M ? 0 : ((size_t)m * k * 2 + 255) & ~(size_t)255; }
+// the f16 activation of a call that may widen it beforehand, whatever n: no
+// kernel for k <= 512 does
+static size_t workspace_of(int32_t m, int32_t k) {
+    return m <= 8 || m > MAX_M || k <= 512 ? 0 : ((size_t)m * k * 2 + 255) & ~(size_t)255;
+}
 
 extern "C" size_t te_i8_workspace(int32_t m, int32_t k, int32_t n) {
     return k < 64 || k > MAX_K || k % 64 || n < 32 ? 0 : workspace_of(m, k);
