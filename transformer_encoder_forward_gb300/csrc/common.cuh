@@ -42,6 +42,9 @@ te_status i8_gemm_linear(const void *xh, const float *ts, int32_t m, int32_t k, 
 te_status i8_gemm_gated(const void *xh, const float *ts, int32_t m, int32_t k, const te_q8w *wg, const te_q8w *wu,
                         int32_t act, void *out, int64_t ldm, cudaStream_t s);
 
+// SMs of the current device.
+int sm_count();
+
 // Bounded-wait error words: each translation unit with bounded waits owns one
 // and exposes a reader that returns and clears it (0 = nothing happened).
 int read_clear_gemm_error();

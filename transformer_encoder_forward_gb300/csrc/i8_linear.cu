@@ -17,7 +17,6 @@ namespace tefwd {
 namespace {
 
 constexpr int MAXZ = 4;
-constexpr int SMS = 152;      // GB300
 
 struct I8Item {
     const int8_t *w, *w2;          // w2: the up projection of the gated form
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(256) i8_small_kernel(const __grid_constant__ I
 template <int NT, int MT, bool GATED, int D>
 te_status small_go(I8Params &p, int groups, cudaStream_t s) {
     int ks = 1;
-    while (ks < 8 && (long long)groups * ks < SMS * 16 && 128 * D * ks < p.k) ks *= 2;
+    while (ks < 8 && (long long)groups * ks < sm_count() * 16 && 128 * D * ks < p.k) ks *= 2;
     const cudaError_t e = launch_close(i8_small_kernel<NT, MT, GATED, D>, dim3(groups), 32 * ks,
                                        ks * MT * 16 * NT * 8 * 4, s, 1, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
@@ -212,7 +211,7 @@ te_status small_launch(I8Params &p, cudaStream_t s) {
     const int ahead = (int)((14ll << 20) / ((long long)groups * 16 * MT)) & ~15;
     p.ahead = ahead < p.k ? ahead : p.k;
     if constexpr (NT * MT <= 2) {
-        if ((long long)groups * 8 < SMS * 16 && p.k > 128 * D * 8) return small_go<NT, MT, GATED, 2 * D>(p, groups, s);
+        if ((long long)groups * 8 < sm_count() * 16 && p.k > 128 * D * 8) return small_go<NT, MT, GATED, 2 * D>(p, groups, s);
     }
     return small_go<NT, MT, GATED, D>(p, groups, s);
 }
@@ -563,7 +562,7 @@ te_status mid_residents(const int *&out) {
     if (e != cudaSuccess) return cuda_fail(e, "i8_linear: set shared memory size");
     for (int s = 8; s >= 1; s /= 2) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(8 * SMS, 1, 1);
+        cfg.gridDim = dim3(8 * sm_count(), 1, 1);
         cfg.blockDim = dim3(Mid<N>::THREADS, 1, 1);
         cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute attr;
@@ -1118,7 +1117,8 @@ te_status res_launch(const I8Params &q, cudaStream_t s) {
     const long long units = (long long)p.ttiles * tiles;
     if (units > 0x7FFFFFFFll) return fail(TE_ESHAPE, "i8_linear: too many tiles");
     p.units = (int)units;
-    e = launch_close(i8_res_kernel<GATED>, dim3(p.units < SMS ? p.units : SMS), Res::THREADS, smem, s, 1, p);
+    const int sms = sm_count();
+    e = launch_close(i8_res_kernel<GATED>, dim3(p.units < sms ? p.units : sms), Res::THREADS, smem, s, 1, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
 }
 
@@ -1203,13 +1203,13 @@ te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
     const te_status st = mid_plan<GATED>(plan, tiles, p.m, p.k);
     if (st != TE_OK) return st;
     const int nkb = (p.k + 127) / 128;
-    const long long ttiles = (p.m + 127) / 128;
+    const long long ttiles = (p.m + 127) / 128, sms = sm_count();
     double other;
     if (path == RES) {
-        const long long rounds = (tiles * ttiles + SMS - 1) / SMS;
+        const long long rounds = (tiles * ttiles + sms - 1) / sms;
         other = 5.5 + rounds * (1.0 + 0.45 * nkb);
     } else {
-        const long long waves = ((tiles + 1) / 2 * ttiles + SMS / 2 - 1) / (SMS / 2);
+        const long long waves = ((tiles + 1) / 2 * ttiles + sms / 2 - 1) / (sms / 2);
         other = 7.0 + 0.39 * nkb * waves + (double)p.m * p.k * 3 / 6e6;
     }
     if (p.m <= 32 || plan.us < other) path = MID;

@@ -1208,8 +1208,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128, 1) mma_peak_ker
     }
 }
 
-int sm_count();
-
 template <int BN>
 te_status mma_peak_launch(int stages, float *ms, cudaStream_t stream) {
     constexpr int smem = 2 * (BN / 2 * BOX * 2) + 16 + 1024;
@@ -1236,19 +1234,6 @@ te_status mma_peak_launch(int stages, float *ms, cudaStream_t stream) {
 }
 
 // ------------------------------------------------------------------ host side
-
-int sm_count() {
-    static int count[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    if (!count[dev]) {
-        int c = 0;
-        if (cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || c < 1)
-            c = 148;
-        count[dev] = c;
-    }
-    return count[dev];
-}
 
 // Long K (re-widened weights): the token-tile width and the token tiles per
 // unit.  With two tiles a unit each widened weight stage feeds the MMAs of both,
@@ -1421,6 +1406,19 @@ static EncodeTiledFn encode_fn() {
             fn = reinterpret_cast<EncodeTiledFn>(f);
     });
     return fn;
+}
+
+int sm_count() {
+    static int count[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    if (!count[dev]) {
+        int c = 0;
+        if (cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || c < 1)
+            c = 148;
+        count[dev] = c;
+    }
+    return count[dev];
 }
 
 te_status make_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner,
