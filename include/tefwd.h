@@ -353,6 +353,32 @@ te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const float *x_scale,
  * values and n output features in all (0 for sizes they do not take). */
 size_t te_i8_workspace(int32_t m, int32_t k, int32_t n);
 
+/* The kernels of te_i8_linear and te_i8_gated_linear, and how one is cut:
+ *   TE_I8_FEW       to 32 tokens; tile = 8, 16 or 32 tokens, split = the
+ *                   128-byte slots a warp keeps in flight (1, 2 or 4)
+ *   TE_I8_MIDDLING  tile = 16, 32, 64 or 128 tokens, split = the CTAs that share
+ *                   a tile's k (1, 2, 4 or 8, at most one for every 128 of k)
+ *   TE_I8_RESIDENT  k <= 512; tile = 128, split = 1
+ *   TE_I8_LARGE     k > 512 and m > 8; tile = its tokens a tile and split = tiles a
+ *                   unit (of the first launch, if there are two) */
+typedef enum { TE_I8_FEW = 0, TE_I8_MIDDLING = 1, TE_I8_RESIDENT = 2, TE_I8_LARGE = 3 } te_i8_kernel;
+typedef struct {
+    int32_t kernel, tile, split;
+} te_i8_choice;
+
+/* i8_choice_of: what a te_i8_linear of m tokens, k values and z items of n[i]
+ * features (gated: a te_i8_gated_linear of n[0]; z = 1) takes on the current
+ * device, by the library's rule or this thread's te_i8_choose.  Nothing is
+ * launched. */
+te_status te_i8_choice_of(int32_t m, int32_t k, const int32_t *n, int32_t z, int32_t gated,
+                          te_i8_choice *choice);
+
+/* i8_choose: a measurement and test aid.  This thread's calls of te_i8_linear
+ * and te_i8_gated_linear take the given kernel (TE_I8_LARGE with tile = split = 0:
+ * it cuts itself) until the next i8_choose; choice == NULL: the rule again.  A call
+ * whose sizes the kernel does not take returns TE_ESHAPE. */
+te_status te_i8_choose(const te_i8_choice *choice);
+
 /* ---- rotary positions with several axes -------------------------------- */
 
 /* Which two channels of a head turn together.  The first rot = sum of the

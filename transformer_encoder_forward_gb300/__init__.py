@@ -21,6 +21,7 @@ TE_NORM_RMS, TE_NORM_LN = 0, 1
 TE_ACT_GELU_TANH, TE_ACT_SILU = 0, 1
 TE_RESID_PLAIN, TE_RESID_SANDWICH = 0, 1
 TE_EPI_NONE, TE_EPI_GELU_TANH, TE_EPI_SILU = 0, 1, 2
+TE_I8_FEW, TE_I8_MIDDLING, TE_I8_RESIDENT, TE_I8_LARGE = 0, 1, 2, 3
 TE_ROPE_SECTION_HALVES, TE_ROPE_HEAD_HALVES, TE_ROPE_ADJACENT = 0, 1, 2
 TE_ROPE_MAX_AXES, TE_ROPE_MAX_PAIRS = 4, 128
 # TE_STATIC_SCRATCH_BYTES of tefwd.h: the scratch array of te_encoder_block_fwd_static
@@ -69,6 +70,10 @@ class te_block_desc(ctypes.Structure):
                 ("prof_events", c_p)]
 
 
+class te_i8_choice(ctypes.Structure):
+    _fields_ = [("kernel", c_i32), ("tile", c_i32), ("split", c_i32)]
+
+
 class te_rope_axes(ctypes.Structure):
     _fields_ = [("hd", c_i32), ("axes", c_i32), ("pairs", c_i32), ("pairing", c_i32),
                 ("sections", c_i32 * TE_ROPE_MAX_AXES), ("axis", ctypes.c_uint8 * TE_ROPE_MAX_PAIRS),
@@ -114,6 +119,9 @@ EXPORTS = {
                                           ctypes.POINTER(te_q8w), c_i32, c_p, c_i64, c_p,
                                           ctypes.c_size_t, c_p]),
     "te_i8_workspace": (ctypes.c_size_t, [c_i32, c_i32, c_i32]),
+    "te_i8_choice_of": (ctypes.c_int, [c_i32, c_i32, ctypes.POINTER(c_i32), c_i32, c_i32,
+                                       ctypes.POINTER(te_i8_choice)]),
+    "te_i8_choose": (ctypes.c_int, [ctypes.POINTER(te_i8_choice)]),
     "te_rope_axes_init": (ctypes.c_int, [ctypes.POINTER(te_rope_axes), c_i32, c_i32,
                                          ctypes.POINTER(c_i32), ctypes.c_double, c_i32, c_i32,
                                          ctypes.POINTER(ctypes.c_double)]),
@@ -378,6 +386,20 @@ def i8_gated_linear(xq, x_scale, wg: te_q8w, wu: te_q8w, act, out, workspace, st
     """out (bf16) = act(x Wg^T) * (x Wu^T) from int8 tokens, rounded once;
     workspace of i8_workspace(m, k, 2 f) bytes."""
     _ok((_m or _marshalling()).i8_gated_linear(xq, x_scale, wg, wu, act, out, workspace, stream))
+
+
+def i8_choice_of(m: int, k: int, ns: Sequence[int], gated=False):
+    """(kernel, tile, split) that a product of m tokens of k values with weights of ns
+    features takes on the current device (te_i8_choice_of)."""
+    c = te_i8_choice()
+    _ok(lib().te_i8_choice_of(m, k, (c_i32 * len(ns))(*ns), len(ns), 1 if gated else 0, ctypes.byref(c)))
+    return c.kernel, c.tile, c.split
+
+
+def i8_choose(choice=None):
+    """This thread's products take the kernel (kernel, tile, split); None: the
+    library's rule again.  A measurement and test aid."""
+    _ok(lib().te_i8_choose(None if choice is None else ctypes.byref(te_i8_choice(*choice))))
 
 
 # ---------------------------------------- rotary positions with several axes

@@ -42,6 +42,9 @@ te_status i8_gemm_linear(const void *xh, const float *ts, int32_t m, int32_t k, 
 te_status i8_gemm_gated(const void *xh, const float *ts, int32_t m, int32_t k, const te_q8w *wg, const te_q8w *wu,
                         int32_t act, void *out, int64_t ldm, cudaStream_t s);
 
+// The token tile and the tiles a unit of their first launch.
+void i8_gemm_tile(int m, int k, int ftiles, int32_t &tokens, int32_t &tiles);
+
 // SMs of the current device.
 int sm_count();
 

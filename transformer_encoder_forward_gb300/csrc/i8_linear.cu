@@ -32,6 +32,7 @@ struct I8Params {
     const float *xs;
     long long ldx;
     int m, k, z;
+    int sms;                  // SMs of the device
     int ahead;                // small: bytes of each weight row asked for beforehand
     I8Item it[MAXZ];
 };
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(256) i8_small_kernel(const __grid_constant__ I
 template <int NT, int MT, bool GATED, int D>
 te_status small_go(I8Params &p, int groups, cudaStream_t s) {
     int ks = 1;
-    while (ks < 8 && (long long)groups * ks < sm_count() * 16 && 128 * D * ks < p.k) ks *= 2;
+    while (ks < 8 && (long long)groups * ks < p.sms * 16 && 128 * D * ks < p.k) ks *= 2;
     const cudaError_t e = launch_close(i8_small_kernel<NT, MT, GATED, D>, dim3(groups), 32 * ks,
                                        ks * MT * 16 * NT * 8 * 4, s, 1, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
@@ -199,22 +200,36 @@ te_status small_go(I8Params &p, int groups, cudaStream_t s) {
 // first 14 MB are asked into L2 before the previous kernel has ended (7 tokens,
 // k 3840: n 11520 10.9 -> 10.0 us, n 3840 6.2 -> 5.8; all 44 MB at once take
 // 12.3).  Sixteen warps a group: 10.7 -> 12.8 at k 10240.
-template <int NT, int MT, bool GATED>
-te_status small_launch(I8Params &p, cudaStream_t s) {
-    constexpr int F = GATED ? 16 : MT * 16;
-    constexpr int D = NT * MT == 1 ? 2 : 1;
+template <int NT, bool GATED>
+struct Small {
+    static constexpr int MT = GATED ? 2 : 1;            // tiles of 16 weight rows a group
+    static constexpr int D = NT * MT == 1 ? 2 : 1;      // slots in flight
+    static constexpr int D2 = NT * MT <= 2 ? 2 * D : D; // where warps are few
+};
+// The weight-row groups of all items; sets their places.
+template <bool GATED>
+int small_groups(I8Params &p) {
     int groups = 0;
     for (int i = 0; i < p.z; ++i) {
         p.it[i].tile0 = groups;
-        groups += p.it[i].n / F;
+        groups += p.it[i].n / 16;
     }
-    const int ahead = (int)((14ll << 20) / ((long long)groups * 16 * MT)) & ~15;
-    p.ahead = ahead < p.k ? ahead : p.k;
-    if constexpr (NT * MT <= 2) {
-        if ((long long)groups * 8 < sm_count() * 16 && p.k > 128 * D * 8) return small_go<NT, MT, GATED, 2 * D>(p, groups, s);
-    }
-    return small_go<NT, MT, GATED, D>(p, groups, s);
+    return groups;
 }
+template <int NT, bool GATED>
+int small_slots(const I8Params &p, int groups) {
+    using S = Small<NT, GATED>;
+    return (long long)groups * 8 < p.sms * 16 && p.k > 128 * S::D * 8 ? S::D2 : S::D;
+}
+template <int NT, bool GATED>
+te_status small_launch(I8Params &p, int slots, cudaStream_t s) {
+    using S = Small<NT, GATED>;
+    const int groups = small_groups<GATED>(p);
+    const int ahead = (int)((14ll << 20) / ((long long)groups * 16 * S::MT)) & ~15;
+    p.ahead = ahead < p.k ? ahead : p.k;
+    return slots == S::D ? small_go<NT, S::MT, GATED, S::D>(p, groups, s) : small_go<NT, S::MT, GATED, S::D2>(p, groups, s);
+}
+
 // --------------------------------------------------- a middling token count
 //
 // Up to a few hundred tokens, or more with few features, the products are
@@ -602,8 +617,11 @@ te_status mid_launch(const I8Params &q, int S, cudaStream_t s) {
     constexpr int F = GATED ? 64 : 128, smem = Mid<N>::BYTES + 1024;
     MidParams p;
     memset(&p, 0, sizeof(p));
-    te_status st = make_map_2d(&p.tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x, (uint64_t)q.k, (uint64_t)q.m, (uint64_t)q.ldx,
-                               128, N, CU_TENSOR_MAP_SWIZZLE_128B);
+    const int *residents;                       // asked for, so its shared memory size is set
+    te_status st = mid_residents<N, GATED>(residents);
+    if (st != TE_OK) return st;
+    st = make_map_2d(&p.tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.x, (uint64_t)q.k, (uint64_t)q.m, (uint64_t)q.ldx, 128, N,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
     int tiles = 0;
     for (int i = 0; i < q.z && st == TE_OK; ++i) {
         p.it[i] = q.it[i];
@@ -624,12 +642,6 @@ te_status mid_launch(const I8Params &q, int S, cudaStream_t s) {
     const int ttiles = (q.m + N - 1) / N;
     const cudaError_t e = launch_close(i8_mid_kernel<N, GATED>, dim3(tiles * S, ttiles), Mid<N>::THREADS, smem, s, S, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
-}
-template <bool GATED>
-te_status mid(const I8Params &p, const MidPlan &plan, cudaStream_t s) {
-    if (plan.n == 16) return mid_launch<16, GATED>(p, plan.split, s);
-    if (plan.n == 32) return mid_launch<32, GATED>(p, plan.split, s);
-    return plan.n == 64 ? mid_launch<64, GATED>(p, plan.split, s) : mid_launch<128, GATED>(p, plan.split, s);
 }
 
 // ------------------------------------------------ many tokens, short k (k <= 512)
@@ -1117,8 +1129,7 @@ te_status res_launch(const I8Params &q, cudaStream_t s) {
     const long long units = (long long)p.ttiles * tiles;
     if (units > 0x7FFFFFFFll) return fail(TE_ESHAPE, "i8_linear: too many tiles");
     p.units = (int)units;
-    const int sms = sm_count();
-    e = launch_close(i8_res_kernel<GATED>, dim3(p.units < sms ? p.units : sms), Res::THREADS, smem, s, 1, p);
+    e = launch_close(i8_res_kernel<GATED>, dim3(p.units < q.sms ? p.units : q.sms), Res::THREADS, smem, s, 1, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "i8_linear launch");
 }
 
@@ -1188,32 +1199,79 @@ constexpr int MAX_K = 65536, MAX_M = 0x7FFFFF00;   // token tiles end within an 
 // a kernel slower by more than 2 %, 11.3 against 12.1 us).  Resident against large at 16238 tokens (us): k 512, n 1536 bf16 27.9
 // and 34.2; n 512 f32 13.7 and 21.3; gated 2 x 2048 58.1 and 68.7; k 64, n 512
 // f32 10.1 and 19.0.
-enum Path { SMALL, MID, RES, LARGE };
 template <bool GATED>
-te_status path_of(const I8Params &p, Path &path, MidPlan &plan) {
+te_status rule(I8Params &p, te_i8_choice &c) {
     long long total = 0;
     int tiles = 0;                              // 128 weight rows (gated: 64 gate and 64 up)
     for (int i = 0; i < p.z; ++i) {
         total += GATED ? 2ll * p.it[i].n : p.it[i].n;
         tiles += GATED ? (p.it[i].n + 63) / 64 : (p.it[i].n + 127) / 128;
     }
-    path = SMALL;
-    if (p.m <= 8 || (p.m <= 16 && total * p.k <= (40 << 20)) || (p.m <= 32 && total * p.k <= (2 << 20))) return TE_OK;
-    path = p.k <= 512 ? RES : LARGE;
+    if (p.m <= 8 || (p.m <= 16 && total * p.k <= (40 << 20)) || (p.m <= 32 && total * p.k <= (2 << 20))) {
+        const int groups = small_groups<GATED>(p);
+        if (p.m <= 8) c = {TE_I8_FEW, 8, small_slots<1, GATED>(p, groups)};
+        else if (p.m <= 16) c = {TE_I8_FEW, 16, small_slots<2, GATED>(p, groups)};
+        else c = {TE_I8_FEW, 32, small_slots<4, GATED>(p, groups)};
+        return TE_OK;
+    }
+    MidPlan plan;
     const te_status st = mid_plan<GATED>(plan, tiles, p.m, p.k);
     if (st != TE_OK) return st;
     const int nkb = (p.k + 127) / 128;
-    const long long ttiles = (p.m + 127) / 128, sms = sm_count();
+    const long long ttiles = (p.m + 127) / 128, sms = p.sms;
     double other;
-    if (path == RES) {
+    if (p.k <= 512) {
+        c = {TE_I8_RESIDENT, 128, 1};
         const long long rounds = (tiles * ttiles + sms - 1) / sms;
         other = 5.5 + rounds * (1.0 + 0.45 * nkb);
     } else {
+        c = {TE_I8_LARGE, 0, 0};
         const long long waves = ((tiles + 1) / 2 * ttiles + sms / 2 - 1) / (sms / 2);
         other = 7.0 + 0.39 * nkb * waves + (double)p.m * p.k * 3 / 6e6;
     }
-    if (p.m <= 32 || plan.us < other) path = MID;
+    if (p.m <= 32 || plan.us < other) c = {TE_I8_MIDDLING, plan.n, plan.split};
     return TE_OK;
+}
+
+// te_i8_choose's choice, of this thread's calls.
+thread_local bool g_chosen = false;
+thread_local te_i8_choice g_choice;
+
+// Whether a chosen kernel takes these sizes (the fields are a choice's, see te_i8_choose).
+template <bool GATED>
+te_status takes(const I8Params &p, const te_i8_choice &c) {
+    bool ok;
+    if (c.kernel == TE_I8_FEW) {
+        ok = p.m <= c.tile && (c.tile == 8    ? c.split == Small<1, GATED>::D || c.split == Small<1, GATED>::D2
+                               : c.tile == 16 ? c.split == Small<2, GATED>::D || c.split == Small<2, GATED>::D2
+                                              : c.split == Small<4, GATED>::D);
+    } else if (c.kernel == TE_I8_MIDDLING) {
+        ok = c.split <= (p.k + 127) / 128 && ((long long)p.m + c.tile - 1) / c.tile <= 65535;
+    } else {
+        ok = c.kernel == TE_I8_RESIDENT ? p.k <= 512 : p.k > 512 && p.m > 8;
+    }
+    return ok ? TE_OK
+              : fail(TE_ESHAPE, "i8_linear: the chosen kernel (%d, %d, %d) does not take m=%d k=%d", c.kernel, c.tile,
+                     c.split, p.m, p.k);
+}
+template <bool GATED>
+te_status choice_of(I8Params &p, te_i8_choice &c) {
+    if (!g_chosen) return rule<GATED>(p, c);
+    c = g_choice;
+    return takes<GATED>(p, c);
+}
+
+// Launches the chosen kernel unless it is the large pipeline (the caller's).
+template <bool GATED>
+te_status go(I8Params &p, const te_i8_choice &c, cudaStream_t s) {
+    if (c.kernel == TE_I8_RESIDENT) return res_launch<GATED>(p, s);
+    if (c.kernel == TE_I8_FEW)
+        return c.tile == 8    ? small_launch<1, GATED>(p, c.split, s)
+               : c.tile == 16 ? small_launch<2, GATED>(p, c.split, s)
+                              : small_launch<4, GATED>(p, c.split, s);
+    if (c.tile == 16) return mid_launch<16, GATED>(p, c.split, s);
+    if (c.tile == 32) return mid_launch<32, GATED>(p, c.split, s);
+    return c.tile == 64 ? mid_launch<64, GATED>(p, c.split, s) : mid_launch<128, GATED>(p, c.split, s);
 }
 te_status check_x(const char *what, const void *x, int64_t ldx, const float *xs, int32_t m, int32_t k) {
     if (m > 0 && (!x || !xs)) return fail(TE_EINVAL, "%s: NULL x or x_scale", what);
@@ -1274,6 +1332,7 @@ extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_s
     p.m = m;
     p.k = k;
     p.z = z;
+    p.sms = sm_count();
     int64_t n = 0;
     for (int i = 0; i < z; ++i) {
         const te_q8_item &src = items[i];
@@ -1311,17 +1370,11 @@ extern "C" te_status te_i8_linear(const int8_t *x, int64_t ldx, const float *x_s
     if ((st = check_ws("i8_linear", workspace, ws_bytes, workspace_of(m, k))) != TE_OK) return st;
     if (m == 0) return TE_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    Path path;
-    MidPlan plan;
-    if ((st = path_of<false>(p, path, plan)) != TE_OK) return st;
-    if (path == MID) return mid<false>(p, plan, s);
-    if (path == RES) return res_launch<false>(p, s);
-    if (path == LARGE) {
-        if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
-        return i8_gemm_linear(workspace, x_scale, m, k, items, z, s);
-    }
-    if (m <= 8) return small_launch<1, 1, false>(p, s);
-    return m <= 16 ? small_launch<2, 1, false>(p, s) : small_launch<4, 1, false>(p, s);
+    te_i8_choice c;
+    if ((st = choice_of<false>(p, c)) != TE_OK) return st;
+    if (c.kernel != TE_I8_LARGE) return go<false>(p, c, s);
+    if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
+    return i8_gemm_linear(workspace, x_scale, m, k, items, z, s);
 }
 
 extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const float *x_scale, int32_t m,
@@ -1350,6 +1403,7 @@ extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const floa
     p.m = m;
     p.k = k;
     p.z = 1;
+    p.sms = sm_count();
     I8Item &d = p.it[0];
     d.w = wg->q;
     d.w2 = wu->q;
@@ -1362,15 +1416,50 @@ extern "C" te_status te_i8_gated_linear(const int8_t *x, int64_t ldx, const floa
     d.n = f;
     d.ydt = TE_BF16;
     d.act = act;
-    Path path;
-    MidPlan plan;
-    if ((st = path_of<true>(p, path, plan)) != TE_OK) return st;
-    if (path == MID) return mid<true>(p, plan, s);
-    if (path == RES) return res_launch<true>(p, s);
-    if (path == LARGE) {
-        if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
-        return i8_gemm_gated(workspace, x_scale, m, k, wg, wu, act, out, ldm, s);
+    te_i8_choice c;
+    if ((st = choice_of<true>(p, c)) != TE_OK) return st;
+    if (c.kernel != TE_I8_LARGE) return go<true>(p, c, s);
+    if ((st = widen(x, ldx, workspace, m, k, s)) != TE_OK) return st;
+    return i8_gemm_gated(workspace, x_scale, m, k, wg, wu, act, out, ldm, s);
+}
+
+extern "C" te_status te_i8_choose(const te_i8_choice *choice) {
+    if (choice) {
+        const int32_t t = choice->tile, s = choice->split;
+        bool ok = false;
+        if (choice->kernel == TE_I8_FEW) ok = (t == 8 || t == 16 || t == 32) && (s == 1 || s == 2 || s == 4);
+        if (choice->kernel == TE_I8_MIDDLING)
+            ok = (t == 16 || t == 32 || t == 64 || t == 128) && (s == 1 || s == 2 || s == 4 || s == 8);
+        if (choice->kernel == TE_I8_RESIDENT) ok = t == 128 && s == 1;
+        if (choice->kernel == TE_I8_LARGE) ok = t == 0 && s == 0;
+        if (!ok) return fail(TE_EINVAL, "i8_choose: no kernel (%d, %d, %d)", choice->kernel, t, s);
+        g_choice = *choice;
     }
-    if (m <= 8) return small_launch<1, 2, true>(p, s);
-    return m <= 16 ? small_launch<2, 2, true>(p, s) : small_launch<4, 2, true>(p, s);
+    g_chosen = choice != nullptr;
+    return TE_OK;
+}
+
+extern "C" te_status te_i8_choice_of(int32_t m, int32_t k, const int32_t *n, int32_t z, int32_t gated,
+                                     te_i8_choice *choice) {
+    if (!n || !choice) return fail(TE_EINVAL, "i8_choice_of: NULL n or choice");
+    if (z < 1 || z > (gated ? 1 : MAXZ) || m < 1 || m > MAX_M || k < 64 || k > MAX_K || k % 64)
+        return fail(TE_ESHAPE, "i8_choice_of: m=%d k=%d z=%d", m, k, z);
+    I8Params p;
+    memset(&p, 0, sizeof(p));
+    p.m = m;
+    p.k = k;
+    p.z = z;
+    p.sms = sm_count();
+    int ftiles = 0;
+    for (int i = 0; i < z; ++i) {
+        if (n[i] < 32 || n[i] % 32 || n[i] > 0x3FFFFFFF) return fail(TE_ESHAPE, "i8_choice_of: n=%d", n[i]);
+        p.it[i].n = n[i];
+        ftiles += gated ? (n[i] + 63) / 64 : (n[i] + 127) / 128;
+    }
+    te_i8_choice c;
+    const te_status st = gated ? choice_of<true>(p, c) : choice_of<false>(p, c);
+    if (st != TE_OK) return st;
+    if (c.kernel == TE_I8_LARGE) i8_gemm_tile(m, k, ftiles, c.tile, c.split);
+    *choice = c;
+    return TE_OK;
 }

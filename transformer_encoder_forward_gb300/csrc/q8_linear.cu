@@ -1584,6 +1584,12 @@ te_status i8_gemm_gated(const void *xh, const float *ts, int32_t m, int32_t k, c
     return gated_parts<true>(p, xh, k, wg->q, wu->q, out, ldm, s);
 }
 
+void i8_gemm_tile(int m, int k, int ftiles, int32_t &tokens, int32_t &tiles) {
+    const TilePlan t = tile_for(m, k, ftiles);
+    tokens = t.bn;
+    tiles = t.tpa;
+}
+
 te_status gemm_error_word(int **word) {
     const cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_gemm_err);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "gemm error word");
