@@ -350,7 +350,7 @@ def _marshalling():
         try:
             from . import _marshal as mod
         except ImportError as e:
-            raise RuntimeError("_marshal.so is not built; run "
+            raise RuntimeError(f"_marshal.so is not built, or for another PyTorch or Python ({e}); run "
                                "python -m transformer_encoder_forward_gb300.build") from e
         mod.bind(*(ctypes.cast(f, c_p).value for f in (L.te_quant_rows, L.te_rownorm_quant, L.te_i8_linear,
                                                        L.te_i8_gated_linear, L.te_qk_rope_axes)))

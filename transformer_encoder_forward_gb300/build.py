@@ -52,6 +52,19 @@ def _marshal_flags():
     return comp, link
 
 
+def _marshal_key(cxx, comp, link) -> str:
+    import torch
+    return "\n".join([torch.__version__, str(torch.version.git_version), sys.version, cxx, *comp, *link])
+
+
+def _read(path: str) -> str:
+    try:
+        with open(path) as f:
+            return f.read()
+    except FileNotFoundError:
+        return ""
+
+
 def _stale(out: str, deps) -> bool:
     if not os.path.exists(out):
         return True
@@ -76,7 +89,11 @@ def build(verbose: bool = False, force: bool = False, extra=()) -> str:
     comp, link = _marshal_flags()
     cxx = os.environ.get("CXX") or "g++"
     m_src, m_obj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.o")
-    if force or _stale(m_obj, [m_src, os.path.join(INCLUDE, "tefwd.h")]):
+    # what the module's object and binary were made for: another PyTorch or
+    # Python, which neither file's time shows, makes them anew
+    m_key, key = os.path.join(BUILD, "marshal.key"), _marshal_key(cxx, comp, link)
+    m_new = force or _read(m_key) != key
+    if m_new or _stale(m_obj, [m_src, os.path.join(INCLUDE, "tefwd.h")]):
         jobs.append([cxx, *comp, "-c", m_src, "-o", m_obj])
 
     def run(cmd):
@@ -93,9 +110,11 @@ def build(verbose: bool = False, force: bool = False, extra=()) -> str:
     if force or cuda_jobs or _stale(LIB, objs):
         run([cc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs])
         os.replace(LIB + ".tmp", LIB)
-    if force or _stale(MARSHAL, [m_obj]):
+    if m_new or _stale(MARSHAL, [m_obj]):
         run([cxx, "-shared", "-o", MARSHAL + ".tmp", m_obj, *link])
         os.replace(MARSHAL + ".tmp", MARSHAL)
+        with open(m_key, "w") as f:
+            f.write(key)
     return LIB
 
 
