@@ -47,3 +47,11 @@ def test_another_torch_makes_the_module_anew(made, monkeypatch):
     monkeypatch.setattr(torch, "__version__", "0.0.1+other")
     assert made() == MODULE
     assert made() == set()
+
+
+def test_the_library_is_built_without_torch(made, monkeypatch):
+    import sys
+    monkeypatch.setitem(sys.modules, "torch", None)          # an import of it fails
+    first = made()
+    assert "libtefwd.so.tmp" in first and not first & MODULE
+    assert made() == set()

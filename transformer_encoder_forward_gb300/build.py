@@ -4,7 +4,7 @@ binding's marshalling module next to it.
 Each CUDA translation unit compiles in parallel to an object under _build/,
 then one nvcc link produces the shared library (CUDA runtime linked
 statically).  The marshalling module (csrc/marshal.cpp: a CPython extension
-over PyTorch's headers) compiles beside them.  Run
+over PyTorch's headers) compiles beside them where PyTorch is installed.  Run
 ``python -m transformer_encoder_forward_gb300.build``.
 """
 from __future__ import annotations
@@ -34,6 +34,14 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def _have_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
 
 
 def _marshal_flags():
@@ -86,15 +94,19 @@ def build(verbose: bool = False, force: bool = False, extra=()) -> str:
         if force or _stale(o, [s, *headers]):
             jobs.append([cc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o])
     cuda_jobs = len(jobs)
-    comp, link = _marshal_flags()
-    cxx = os.environ.get("CXX") or "g++"
-    m_src, m_obj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.o")
-    # what the module's object and binary were made for: another PyTorch or
-    # Python, which neither file's time shows, makes them anew
-    m_key, key = os.path.join(BUILD, "marshal.key"), _marshal_key(cxx, comp, link)
-    m_new = force or _read(m_key) != key
-    if m_new or _stale(m_obj, [m_src, os.path.join(INCLUDE, "tefwd.h")]):
-        jobs.append([cxx, *comp, "-c", m_src, "-o", m_obj])
+    # The library needs no PyTorch; where there is none, neither does anybody
+    # call the module.
+    with_module = _have_torch()
+    if with_module:
+        comp, link = _marshal_flags()
+        cxx = os.environ.get("CXX") or "g++"
+        m_src, m_obj = os.path.join(CSRC, "marshal.cpp"), os.path.join(BUILD, "marshal.o")
+        # what the module's object and binary were made for: another PyTorch or
+        # Python, which neither file's time shows, makes them anew
+        m_key, key = os.path.join(BUILD, "marshal.key"), _marshal_key(cxx, comp, link)
+        m_new = force or _read(m_key) != key
+        if m_new or _stale(m_obj, [m_src, os.path.join(INCLUDE, "tefwd.h")]):
+            jobs.append([cxx, *comp, "-c", m_src, "-o", m_obj])
 
     def run(cmd):
         if verbose:
@@ -110,7 +122,7 @@ def build(verbose: bool = False, force: bool = False, extra=()) -> str:
     if force or cuda_jobs or _stale(LIB, objs):
         run([cc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs])
         os.replace(LIB + ".tmp", LIB)
-    if m_new or _stale(MARSHAL, [m_obj]):
+    if with_module and (m_new or _stale(MARSHAL, [m_obj])):
         run([cxx, "-shared", "-o", MARSHAL + ".tmp", m_obj, *link])
         os.replace(MARSHAL + ".tmp", MARSHAL)
         with open(m_key, "w") as f:
