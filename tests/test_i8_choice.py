@@ -60,3 +60,25 @@ def test_choice_of_rejects_bad_sizes(L):
     c = te.te_i8_choice()
     assert _call(L, "te_i8_choice_of", 5, 64, None, 1, 0, ctypes.byref(c))[0] == te.TE_EINVAL
     assert FAKE
+
+
+def test_the_marshalling_module_calls_nothing_before_it_is_bound(L):
+    import os
+    import subprocess
+    import sys
+    from tests.test_abi import ROOT
+    script = """
+import torch
+from transformer_encoder_forward_gb300 import _marshal
+try:
+    _marshal.quant_rows(1, 2, 3, None)
+except RuntimeError as e:
+    print(e)
+for bad in ((1, 2), (0, 0, 0, 0, 0), (1, 2, 3, 4, "5")):
+    try:
+        _marshal.bind(*bad)
+    except (TypeError, ValueError):
+        print("refused")
+"""
+    r = subprocess.run([sys.executable, "-c", script], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.split("\n")[:4] == ["the library's functions have not been bound"] + ["refused"] * 3

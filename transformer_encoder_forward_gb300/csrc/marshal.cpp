@@ -143,6 +143,11 @@ T structure(const char *what, PyObject *o) {
 void count(Py_ssize_t have, Py_ssize_t need) {
     if (have != need) raise(PyExc_TypeError, "wrong number of arguments");
 }
+// The same for a call of the C ABI.
+void call_args(Py_ssize_t have, Py_ssize_t need) {
+    if (!abi.quant_rows) raise(PyExc_RuntimeError, "the library's functions have not been bound");
+    count(have, need);
+}
 
 // Runs f (a te_status), turning C++ exceptions into Python ones.
 template <typename F>
@@ -170,7 +175,7 @@ te_status unlocked(F f) {
 // quant_rows(x, q, scale, stream)
 PyObject *quant_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
-        count(n, 4);
+        call_args(n, 4);
         const Arg x = want("quant_rows: x", a[0], F32 | BF16, 2, -1, -1);
         const Arg q = want("quant_rows: q", a[1], I8, 2, x.rows, x.cols);
         const Arg s = want("quant_rows: scale", a[2], F32, 1, 1, x.rows);
@@ -185,7 +190,7 @@ PyObject *quant_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // rownorm_quant(x, w, b, kind, eps, q, scale, pre, mod_scale, stream)
 PyObject *rownorm_quant(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
-        count(n, 10);
+        call_args(n, 10);
         const Arg x = want("rownorm_quant: x", a[0], F32 | BF16, 2, -1, -1);
         const void *w = want("rownorm_quant: w", a[1], F32, 1, 1, x.cols).ptr;
         const void *b = opt("rownorm_quant: b", a[2], F32, x.cols);
@@ -214,7 +219,7 @@ PyObject *K_W, *K_Y, *K_LDY, *K_RESIDUAL, *K_LDR, *K_EPILOGUE;
 // i8_linear(xq, x_scale, items, workspace, stream)
 PyObject *i8_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
-        count(n, 5);
+        call_args(n, 5);
         const Arg x = want("i8_linear: xq", a[0], I8, 2, -1, -1);
         const Arg s = want("i8_linear: x_scale", a[1], F32, 1, 1, x.rows);
         PyObject *seq = PySequence_Fast(a[2], "i8_linear: items must be a sequence");
@@ -265,7 +270,7 @@ PyObject *i8_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // i8_gated_linear(xq, x_scale, wg, wu, act, out, workspace, stream)
 PyObject *i8_gated_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
-        count(n, 8);
+        call_args(n, 8);
         const Arg x = want("i8_gated_linear: xq", a[0], I8, 2, -1, -1);
         const Arg s = want("i8_gated_linear: x_scale", a[1], F32, 1, 1, x.rows);
         const te_q8w wg = structure<te_q8w>("i8_gated_linear: wg", a[2]);
@@ -285,7 +290,7 @@ PyObject *i8_gated_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // qk_rope_axes(src, ld_src, dst, ld_dst, q_off, k_off, nq, nkv, hd, qn, kn, eps, plan, pos, q_mul, rows, stream)
 PyObject *qk_rope_axes(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
-        count(n, 17);
+        call_args(n, 17);
         const int32_t rows = int32_of(a[15]), hd = int32_of(a[8]);
         const Arg src = want("qk_rope_axes: src", a[0], F32 | BF16, 2, rows, -1);
         const Arg dst = want("qk_rope_axes: dst", a[2], src.dtype == TE_F32 ? F32 : BF16, 2, rows, -1);

@@ -1585,7 +1585,8 @@ te_status i8_gemm_gated(const void *xh, const float *ts, int32_t m, int32_t k, c
 }
 
 void i8_gemm_tile(int m, int k, int ftiles, int32_t &tokens, int32_t &tiles) {
-    const TilePlan t = tile_for(m, k, ftiles);
+    const int most = 0x7FFFFFFF - 512;          // rounding up to whole units stays an int
+    const TilePlan t = tile_for(m < most ? m : most, k, ftiles);
     tokens = t.bn;
     tiles = t.tpa;
 }
