@@ -316,8 +316,9 @@ te_status te_quant_rows(const void *x, int32_t xdt, int64_t ldx, int8_t *q, int6
 /* rownorm_quant: the pre-norm and the quantisation in one pass: quant_rows of
  *   v = Norm(pre * x) * w (+ b), times (1 + mod_scale) when given
  * (te_rownorm_mod's f32 steps in its order, so the same bits from the same row
- * statistics; v stays f32, it is not rounded to bf16 between).  x may be f32 or bf16; b: LN only, or NULL; mod_scale f32 [d] or
- * NULL.  Sizes and the other arguments as te_quant_rows. */
+ * statistics; v stays f32, it is not rounded to bf16 between).  x may be f32 or
+ * bf16; b: LN only, or NULL; mod_scale f32 [d] or NULL.  Sizes and the other
+ * arguments as te_quant_rows. */
 te_status te_rownorm_quant(const void *x, int32_t xdt, int64_t ldx, const float *w, const float *b,
                            const float *mod_scale, int32_t kind, float eps, float pre, int8_t *q,
                            int64_t ldq, float *scale, int32_t t, int32_t d, te_stream stream);
@@ -329,10 +330,11 @@ te_status te_rownorm_quant(const void *x, int32_t xdt, int64_t ldx, const float 
  * and col NULL); an item's epilogue activation is applied to the f32 value.
  * The sum runs over exact integer products in f32 accumulators: exact whenever
  * no partial sum passes 2^24 in magnitude (any int8 values to k = 1024, and in
- * practice sums of both signs at every k).  Beyond, the tensor cores drop what an accumulator cannot hold at every step: a sum is
- * within (k / 16) 2^-23 of its largest partial sum, and nearer zero rather
- * than rounded (one-signed sums measured 3.8e-5 short of themselves at k = 10240,
- * 1.6e-4 at 65536), by an amount that the kernel taken, so m, may change.
+ * practice sums of both signs at every k).  Beyond, the tensor cores drop what
+ * an accumulator cannot hold at every step: a sum is within (k / 16) 2^-23 of
+ * its largest partial sum, and nearer zero rather than rounded (one-signed sums
+ * measured 3.8e-5 short of themselves at k = 10240, 1.6e-4 at 65536), by an
+ * amount that the kernel taken, so m, may change.
  * Sizes: 0 <= m <= 2^31 - 256, 64 <= k <= 65536, k % 64 == 0, 1 <= z <= 4.
  * workspace: te_i8_workspace(m, k, n) bytes or more with n the sum of the
  * items' n, 256-byte aligned (may be NULL when that is 0).  It holds nothing
