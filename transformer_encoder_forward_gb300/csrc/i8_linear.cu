@@ -276,6 +276,12 @@ struct Mid {
     static_assert(N * 128 * 4 <= B_OFF, "the partial sums reuse the ring");
     static_assert(N + 64 * NA <= TMEM, "TMEM columns");
     static_assert(BYTES + 1024 <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
+    // A CTA waits for its cluster's others while it holds TMEM.  So its SM must
+    // have TMEM for all that fit there, or they end by themselves: two of these
+    // (or one and attention's, which waits for nobody) have 256 columns each, and
+    // beside the pairs of q8_gemm_kernel (from 179 KB) and mma_peak_kernel (160
+    // KB), which hold 512 and wait for one another, there is no room for one.
+    static_assert(BYTES + 1024 > 80 * 1024, "no CTA beside a pair's");
 };
 
 struct MidParams {

@@ -1210,10 +1210,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(128, 1) mma_peak_ker
 
 template <int BN>
 te_status mma_peak_launch(int stages, float *ms, cudaStream_t stream) {
-    constexpr int smem = 2 * (BN / 2 * BOX * 2) + 16 + 1024;
+    // More than the operands need, so that no CTA of another stream's product
+    // fits beside one of these: a pair that holds all of one SM's TMEM while it
+    // waits for the other's, which a cluster of the 8-bit products holds
+    // (i8_linear.cu: from 85 KB a CTA) while it waits for the first, would wait
+    // for ever.
+    constexpr int smem = 160 * 1024;
+    static_assert(smem >= 2 * (BN / 2 * BOX * 2) + 16 + 1024 && smem + 80 * 1024 > 228 * 1024, "alone on its SMs");
     const int clusters = sm_count() / 2;
     cudaEvent_t e0, e1;
-    cudaError_t e = cudaEventCreate(&e0);
+    cudaError_t e = cudaFuncSetAttribute(mma_peak_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return cuda_fail(e, "mma_peak: set shared memory size");
+    e = cudaEventCreate(&e0);
     if (e != cudaSuccess) return cuda_fail(e, "mma_peak: event");
     e = cudaEventCreate(&e1);
     if (e != cudaSuccess) {
