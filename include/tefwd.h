@@ -32,7 +32,7 @@
  *     asynchronous work surface as TE_ECUDA from te_check().
  *   - Work is enqueued on `stream` (NULL = the legacy default stream); the
  *     calls return before it completes.  te_q8_linear, te_q8_gated_linear,
- *     te_attn_varlen_fwd,
+ *     te_attn_varlen_fwd, te_attn_sink_fwd, te_attn_relbias_fwd,
  *     the row ops, te_quant_rows, te_rownorm_quant, te_i8_linear,
  *     te_i8_gated_linear, te_qk_rope_axes and te_encoder_block_fwd are
  *     capturable in a CUDA graph (no host synchronisation, no allocation).
@@ -189,6 +189,64 @@ te_status te_attn_items_fwd(const void *qkv, int64_t ld, int32_t q_off, int32_t 
                             int32_t nitems, int32_t rows, int32_t nq_heads, int32_t nkv_heads,
                             int32_t hd, int32_t window, float scale, void *out, int64_t ldo,
                             te_stream stream);
+
+/* attn_sink_fwd: te_attn_varlen_fwd with a window of its own to either side
+ * and a few first tokens that stay visible (sinks).  Key j of a sequence is
+ * visible to its row i iff
+ *     j <= i + right  and  (j >= i - left  or  j < sinks)
+ * with rows and keys counted within the sequence; left, right: >= 0, or -1 for
+ * no limit (right = 0: causal); sinks >= 0.  A row always sees itself.
+ * Values in masked places have no influence, not even where they are infinite
+ * or NaN (a row with such a key of its own sequence next to its window is summed
+ * in another order and takes longer).  scale in [2^-100, 2^100]; a sequence has at most 2^29 rows; rows of
+ * out behind the last sequence are not touched.  Otherwise as
+ * te_attn_varlen_fwd.  [EG2] att_plan's windowed span, extended. */
+te_status te_attn_sink_fwd(const void *qkv, int64_t ld, int32_t q_off, int32_t k_off, int32_t v_off,
+                           const int32_t *cu_host, const int32_t *cu_dev, int32_t nseq,
+                           int32_t nq_heads, int32_t nkv_heads, int32_t hd, int32_t left,
+                           int32_t right, int32_t sinks, float scale, void *out, int64_t ldo,
+                           te_stream stream);
+
+#define TE_RELPOS_MAX_BUCKETS 512
+#define TE_RELPOS_MAX_DISTANCE 2048
+
+/* The buckets of relative positions, filled by te_relpos_init and kept by the
+ * caller (host memory; plain data).  first[b] is the smallest distance of
+ * bucket b of one side; from `reach` on all distances share the last one. */
+typedef struct {
+    int32_t buckets, max_distance, two_sided, reach;
+    float grow;
+    int32_t first[TE_RELPOS_MAX_BUCKETS];
+} te_relpos;
+
+/* relpos_init: fills *plan.  Two-sided: each side (j <= i, j > i) has
+ * side = buckets / 2 buckets, those of j > i behind the others; one-sided
+ * (two_sided = 0): side = buckets for j <= i, and every j > i is in bucket 0.
+ * With a = |j - i|, exact = side / 2 (whole) and n = side - exact, a's bucket is
+ *     a                                                        where a < exact
+ *     exact + min(n - 1, floor(n log(a / exact) / log(max_distance / exact)))   else
+ * taken exactly (whole numbers decide at the borders).  side >= 2, buckets <=
+ * TE_RELPOS_MAX_BUCKETS and even when two-sided; exact < max_distance <=
+ * TE_RELPOS_MAX_DISTANCE.  Host only; no device is touched.  The pages have
+ * rotary positions only. */
+te_status te_relpos_init(te_relpos *plan, int32_t buckets, int32_t max_distance, int32_t two_sided);
+
+/* sizeof(te_relpos) as this library was compiled (for a binding). */
+size_t te_relpos_size(void);
+
+/* attn_relbias_fwd: te_attn_sink_fwd with a learned bias of relative position
+ * added to the scores,
+ *     out[i, h*hd + c] = sum_j softmax_j(scale * q_i . k_j + table[bucket(j - i), h]) v_j[c]
+ * table: f32 [plan->buckets, nq_heads] (device, 4-byte aligned, rows ldt >=
+ * nq_heads floats apart).  A bias of -inf masks its bucket, one of f32's lowest
+ * value leaves a row whose keys all have it their mean; a row with nothing left
+ * is 0.  (left = right = -1 and sinks = 0: every key of the sequence.) */
+te_status te_attn_relbias_fwd(const void *qkv, int64_t ld, int32_t q_off, int32_t k_off,
+                              int32_t v_off, const int32_t *cu_host, const int32_t *cu_dev,
+                              int32_t nseq, int32_t nq_heads, int32_t nkv_heads, int32_t hd,
+                              int32_t left, int32_t right, int32_t sinks, float scale,
+                              const te_relpos *plan, const float *table, int64_t ldt, void *out,
+                              int64_t ldo, te_stream stream);
 
 /* rownorm: y = Norm(pre * x) per row.
  *   RMS: v / sqrt(mean(v^2) + eps) * w            ([EG2] Prog::rms)

@@ -24,6 +24,7 @@ TE_EPI_NONE, TE_EPI_GELU_TANH, TE_EPI_SILU = 0, 1, 2
 TE_I8_FEW, TE_I8_MIDDLING, TE_I8_RESIDENT, TE_I8_LARGE = 0, 1, 2, 3
 TE_ROPE_SECTION_HALVES, TE_ROPE_HEAD_HALVES, TE_ROPE_ADJACENT = 0, 1, 2
 TE_ROPE_MAX_AXES, TE_ROPE_MAX_PAIRS = 4, 128
+TE_RELPOS_MAX_BUCKETS, TE_RELPOS_MAX_DISTANCE = 512, 2048
 # TE_STATIC_SCRATCH_BYTES of tefwd.h: the scratch array of te_encoder_block_fwd_static
 TE_STATIC_SCRATCH_BYTES = 32 << 20
 # TE_BLOCK_PROF_EVENTS of tefwd.h: the step-boundary events of te_block_desc.prof_events
@@ -80,6 +81,11 @@ class te_rope_axes(ctypes.Structure):
                 ("turn", ctypes.c_uint64 * TE_ROPE_MAX_PAIRS)]
 
 
+class te_relpos(ctypes.Structure):
+    _fields_ = [("buckets", c_i32), ("max_distance", c_i32), ("two_sided", c_i32), ("reach", c_i32),
+                ("grow", c_f32), ("first", c_i32 * TE_RELPOS_MAX_BUCKETS)]
+
+
 _lib = None
 
 EXPORTS = {
@@ -90,6 +96,13 @@ EXPORTS = {
                                           c_i32, c_i32, c_i32, c_f32, c_p, c_i64, c_p]),
     "te_attn_items_fwd": (ctypes.c_int, [c_p, c_i64, c_i32, c_i32, c_i32, c_p, c_p, c_i32, c_i32,
                                          c_i32, c_i32, c_i32, c_i32, c_f32, c_p, c_i64, c_p]),
+    "te_attn_sink_fwd": (ctypes.c_int, [c_p, c_i64, c_i32, c_i32, c_i32, c_p, c_p, c_i32, c_i32, c_i32,
+                                        c_i32, c_i32, c_i32, c_i32, c_f32, c_p, c_i64, c_p]),
+    "te_attn_relbias_fwd": (ctypes.c_int, [c_p, c_i64, c_i32, c_i32, c_i32, c_p, c_p, c_i32, c_i32,
+                                           c_i32, c_i32, c_i32, c_i32, c_i32, c_f32,
+                                           ctypes.POINTER(te_relpos), c_p, c_i64, c_p, c_i64, c_p]),
+    "te_relpos_init": (ctypes.c_int, [ctypes.POINTER(te_relpos), c_i32, c_i32, c_i32]),
+    "te_relpos_size": (ctypes.c_size_t, []),
     "te_rownorm": (ctypes.c_int, [c_p, c_i32, c_i64, c_p, c_p, c_i32, c_f32, c_f32, c_p, c_i32,
                                   c_i64, c_i32, c_i32, c_p]),
     "te_add_norm": (ctypes.c_int, [c_p, c_p, c_p, c_f32, c_p, c_p, c_i32, c_f32, c_p, c_i32, c_i32,
@@ -353,7 +366,8 @@ def _marshalling():
             raise RuntimeError(f"_marshal.so is not built, or for another PyTorch or Python ({e}); run "
                                "python -m transformer_encoder_forward_gb300.build") from e
         mod.bind(*(ctypes.cast(f, c_p).value for f in (L.te_quant_rows, L.te_rownorm_quant, L.te_i8_linear,
-                                                       L.te_i8_gated_linear, L.te_qk_rope_axes)))
+                                                       L.te_i8_gated_linear, L.te_qk_rope_axes,
+                                                       L.te_attn_sink_fwd, L.te_attn_relbias_fwd)))
         _m = mod
     return _m
 
@@ -427,6 +441,37 @@ def qk_rope_axes(src, ld_src, dst, ld_dst, q_off, k_off, nq, nkv, hd, qn, kn, ep
     dst (dst may be src); pos int32 [rows, axes] on the device."""
     _ok((_m or _marshalling()).qk_rope_axes(src, ld_src, dst, ld_dst, q_off, k_off, nq, nkv, hd, qn, kn, eps,
                                         plan, pos, q_mul, rows, stream))
+
+
+# ------------------------- attention with sinks and relative position bias
+
+def _offsets(cu_host):
+    import numpy as np
+    return np.ascontiguousarray(cu_host, dtype=np.int32)
+
+
+def attn_sink_fwd(qkv, ld, q_off, k_off, v_off, cu_host, cu_dev, nq, nkv, hd, left, right, sinks,
+                  scale, out, ldo, stream=None):
+    """attn_varlen_fwd with limits of its own to either side (-1: none) and
+    `sinks` first tokens that the left limit does not hide."""
+    _ok((_m or _marshalling()).attn_sink_fwd(qkv, ld, q_off, k_off, v_off, _offsets(cu_host), cu_dev, nq, nkv, hd,
+                                             left, right, sinks, scale, out, ldo, stream))
+
+
+def relpos_plan(buckets, max_distance, two_sided=True) -> te_relpos:
+    """The buckets of relative positions: exact for small distances, then
+    logarithmic to max_distance; two-sided: half of them for j > i."""
+    plan = te_relpos()
+    _ok(lib().te_relpos_init(ctypes.byref(plan), buckets, max_distance, 1 if two_sided else 0))
+    return plan
+
+
+def attn_relbias_fwd(qkv, ld, q_off, k_off, v_off, cu_host, cu_dev, nq, nkv, hd, left, right, sinks,
+                     scale, plan: te_relpos, table, out, ldo, stream=None):
+    """attn_sink_fwd with table[bucket(j - i), head] (f32 [buckets, nq]) added to
+    the scores."""
+    _ok((_m or _marshalling()).attn_relbias_fwd(qkv, ld, q_off, k_off, v_off, _offsets(cu_host), cu_dev, nq, nkv, hd,
+                                                left, right, sinks, scale, plan, table, out, ldo, stream))
 
 
 def block_workspace(desc: te_block_desc, t: int) -> int:

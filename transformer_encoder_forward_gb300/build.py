@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtefwd.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
-SOURCES = ["rowops.cu", "q8_linear.cu", "attn.cu", "block.cu", "block_static.cu", "codecs.cu",
+SOURCES = ["rowops.cu", "q8_linear.cu", "attn.cu", "attn_span.cu", "block.cu", "block_static.cu", "codecs.cu",
            "quant.cu", "i8_linear.cu", "rope_axes.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -100,20 +100,6 @@ struct ALayout {
     static_assert(O_COL + TL * HD <= COLS, "TMEM budget");
 };
 
-// Shared-memory descriptor of an MN-major operand stored as 64-element-wide
-// boxes with the 128-byte swizzle: rows (along K) 128 bytes apart, 8-row
-// groups 1024 bytes apart (stride byte offset), 64-element groups along MN
-// `lbo` bytes apart (leading byte offset).
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
-
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -52,6 +52,7 @@ int sm_count();
 // and exposes a reader that returns and clears it (0 = nothing happened).
 int read_clear_gemm_error();
 int read_clear_attn_error();
+int read_clear_attn_span_error();
 // Device address of the products' error word, for kernels of other
 // translation units that report there.
 te_status gemm_error_word(int **word);
@@ -515,6 +516,20 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
     d |= (uint64_t)(1024u >> 4) << 32;                 // stride byte offset: 8 rows
     d |= (uint64_t)1 << 46;                            // descriptor version
     d |= (uint64_t)2 << 61;                            // 128-byte swizzle
+    return d;
+}
+
+// Shared-memory descriptor of an MN-major operand stored as 64-element-wide
+// boxes with the 128-byte swizzle: rows (along K) 128 bytes apart, 8-row
+// groups 1024 bytes apart (stride byte offset), 64-element groups along MN
+// `lbo` bytes apart (leading byte offset).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
     return d;
 }
 

@@ -29,6 +29,8 @@ struct {
     decltype(&te_i8_linear) i8_linear;
     decltype(&te_i8_gated_linear) i8_gated_linear;
     decltype(&te_qk_rope_axes) qk_rope_axes;
+    decltype(&te_attn_sink_fwd) attn_sink_fwd;
+    decltype(&te_attn_relbias_fwd) attn_relbias_fwd;
 } abi;
 
 struct PyError {};   // a Python exception is set
@@ -314,12 +316,88 @@ PyObject *qk_rope_axes(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// bind(addresses of te_quant_rows, te_rownorm_quant, te_i8_linear, te_i8_gated_linear, te_qk_rope_axes)
+// The packed batch of an attention call: the panel, the output, and the
+// sequences' offsets on the host (a contiguous int32 buffer, released at the end).
+struct Batch {
+    Arg qkv, out, cu_dev;
+    Py_buffer cu;
+    const int32_t *offsets;
+    int32_t nseq;
+    Batch(const std::string &name, PyObject *panel, PyObject *host, PyObject *dev, PyObject *o) {
+        if (PyObject_GetBuffer(host, &cu, PyBUF_CONTIG_RO | PyBUF_FORMAT) != 0) throw PyError();
+        try {
+            const std::string f = cu.format ? cu.format : "B";
+            if (cu.ndim != 1 || cu.itemsize != 4 || (f != "i" && f != "=i" && f != "<i" && f != "l" && f != "<l"))
+                raise(PyExc_TypeError, name + ": cu_host: not a vector of int32");
+            if (cu.shape[0] < 2 || cu.shape[0] > 2147483647) raise(PyExc_ValueError, name + ": cu_host: no sequence");
+            offsets = static_cast<const int32_t *>(cu.buf);
+            nseq = (int32_t)(cu.shape[0] - 1);
+            cu_dev = want((name + ": cu_dev").c_str(), dev, I32, 1, 1, nseq + 1);
+            qkv = want((name + ": qkv").c_str(), panel, BF16, 2, -1, -1);
+            out = want((name + ": out").c_str(), o, BF16, 2, -1, -1);
+            if (qkv.rows < offsets[nseq] || out.rows < offsets[nseq])
+                raise(PyExc_ValueError, name + ": the sequences end at row " + std::to_string(offsets[nseq]) + " of " +
+                                            std::to_string(std::min(qkv.rows, out.rows)));
+        } catch (...) {
+            PyBuffer_Release(&cu);
+            throw;
+        }
+    }
+    Batch(const Batch &) = delete;
+    ~Batch() { PyBuffer_Release(&cu); }
+};
+
+void inside(const char *what, int64_t end, const Arg &t) {
+    if (end > t.cols)
+        raise(PyExc_ValueError, std::string(what) + ": the heads end at column " + std::to_string(end) + " of " + std::to_string(t.cols));
+}
+
+// attn_sink_fwd(qkv, ld, q_off, k_off, v_off, cu_host, cu_dev, nq, nkv, hd, left, right, sinks, scale, out, ldo, stream)
+// attn_relbias_fwd(..., scale, plan, table, out, ldo, stream)
+template <bool BIAS>
+PyObject *attn_span(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        call_args(n, BIAS ? 19 : 17);
+        const char *name = BIAS ? "attn_relbias_fwd" : "attn_sink_fwd";
+        PyObject *const *t = a + (BIAS ? 16 : 14);   // out, ldo, stream
+        const int32_t q_off = int32_of(a[2]), k_off = int32_of(a[3]), v_off = int32_of(a[4]);
+        const int32_t nq = int32_of(a[7]), nkv = int32_of(a[8]), hd = int32_of(a[9]);
+        const int32_t left = int32_of(a[10]), right = int32_of(a[11]), sinks = int32_of(a[12]);
+        const float scale = real(a[13]);
+        const int64_t ld = integer(a[1]), ldo = integer(t[1]);
+        te_stream stream = stream_of(t[2]);
+        te_relpos plan;
+        Arg table;
+        if (BIAS) {
+            plan = structure<te_relpos>("attn_relbias_fwd: plan", a[14]);
+            table = want("attn_relbias_fwd: table", a[15], F32, 2, plan.buckets, -1);
+            if (table.cols < nq) raise(PyExc_ValueError, "attn_relbias_fwd: table: fewer columns than heads");
+        }
+        const Batch b(name, a[0], a[5], a[6], t[0]);
+        leading(name, b.qkv, ld);
+        leading(name, b.out, ldo);
+        inside(name, std::max(q_off + (int64_t)nq * hd, std::max(k_off, v_off) + (int64_t)nkv * hd), b.qkv);
+        inside(name, (int64_t)nq * hd, b.out);
+        return unlocked([&] {
+            if (BIAS)
+                return abi.attn_relbias_fwd(b.qkv.ptr, ld, q_off, k_off, v_off, b.offsets,
+                                            static_cast<const int32_t *>(b.cu_dev.ptr), b.nseq, nq, nkv, hd, left, right,
+                                            sinks, scale, &plan, static_cast<const float *>(table.ptr), table.ld, b.out.ptr,
+                                            ldo, stream);
+            return abi.attn_sink_fwd(b.qkv.ptr, ld, q_off, k_off, v_off, b.offsets,
+                                     static_cast<const int32_t *>(b.cu_dev.ptr), b.nseq, nq, nkv, hd, left, right, sinks,
+                                     scale, b.out.ptr, ldo, stream);
+        });
+    });
+}
+
+// bind(addresses of te_quant_rows, te_rownorm_quant, te_i8_linear, te_i8_gated_linear, te_qk_rope_axes,
+//      te_attn_sink_fwd, te_attn_relbias_fwd)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
-        count(n, 5);
-        void *f[5];
-        for (int i = 0; i < 5; ++i) {
+        count(n, 7);
+        void *f[7];
+        for (int i = 0; i < 7; ++i) {
             f[i] = PyLong_AsVoidPtr(a[i]);
             if (!f[i]) raise(PyExc_ValueError, "bind: not a function's address");
         }
@@ -328,6 +406,8 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
         abi.i8_linear = reinterpret_cast<decltype(abi.i8_linear)>(f[2]);
         abi.i8_gated_linear = reinterpret_cast<decltype(abi.i8_gated_linear)>(f[3]);
         abi.qk_rope_axes = reinterpret_cast<decltype(abi.qk_rope_axes)>(f[4]);
+        abi.attn_sink_fwd = reinterpret_cast<decltype(abi.attn_sink_fwd)>(f[5]);
+        abi.attn_relbias_fwd = reinterpret_cast<decltype(abi.attn_relbias_fwd)>(f[6]);
         return TE_OK;
     });
 }
@@ -339,6 +419,8 @@ PyMethodDef methods[] = {
     {"i8_linear", (PyCFunction)(void (*)(void))i8_linear, METH_FASTCALL, nullptr},
     {"i8_gated_linear", (PyCFunction)(void (*)(void))i8_gated_linear, METH_FASTCALL, nullptr},
     {"qk_rope_axes", (PyCFunction)(void (*)(void))qk_rope_axes, METH_FASTCALL, nullptr},
+    {"attn_sink_fwd", (PyCFunction)(void (*)(void))attn_span<false>, METH_FASTCALL, nullptr},
+    {"attn_relbias_fwd", (PyCFunction)(void (*)(void))attn_span<true>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument marshalling of libtefwd's calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -893,7 +893,8 @@ te_status te_check(te_stream stream) {
         cudaMemcpyToSymbol(g_rowop_err, &zero, sizeof(int));
     }
     const int gemm = read_clear_gemm_error();
-    const int attn = read_clear_attn_error();
+    const int attn_err = read_clear_attn_error(), span_err = read_clear_attn_span_error();
+    const int attn = attn_err < 0 || span_err < 0 ? -1 : attn_err | span_err;
     if (gemm < 0 || attn < 0) return fail(TE_ECUDA, "te_check: could not read device error words");
     if (rowop || gemm || attn)
         return fail(TE_EDEVICE, "device error words: rowops=%d gemm=%d attn=%d "
