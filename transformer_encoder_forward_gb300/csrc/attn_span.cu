@@ -35,16 +35,17 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 
 namespace tefwd {
 namespace {
 
-constexpr int BQ = 128;     // queries per tile (= TMEM lanes); TL tiles per CTA
-constexpr int BKV = 128;    // keys per tile
+constexpr int BQ = 128;     // queries per tile (= TMEM lanes)
+constexpr int BKV = 64;     // keys per tile
 constexpr int MAX_WORK = 640;   // work list entries carried in the launch parameters
-constexpr int PAD = 160;    // distances past `reach` that a tile near it can still touch (158)
+constexpr int PAD = 96;     // distances past `reach` that 32 rows and 64 keys near it can still touch (94)
 // as in attn.cu: K and V bytes that the CTA order treats as one group of heads
 constexpr long long KV_ALL_BYTES = 48ll << 20;
 constexpr long long KV_GROUP_BYTES = 24ll << 20;
@@ -52,7 +53,7 @@ constexpr long long KV_GROUP_BYTES = 24ll << 20;
 __device__ int g_span_err;
 
 struct SpanParams {
-    CUtensorMap map;           // the bf16 q|k|v panel [T, ld], box 64 x 128
+    CUtensorMap map;           // the bf16 q|k|v panel [T, ld], box 64 x 64
     __nv_bfloat16 *out;
     const __nv_bfloat16 *qkv;
     const int *cu;
@@ -68,28 +69,57 @@ struct SpanParams {
     const float *table;        // [buckets, ldt]
     long long ldt;
     int side, exact, reach, two_sided;   // buckets of a side, those of one distance each; clipped reach
+    int nbuf;                  // spread biases in shared memory
     float grow;                // logarithmic buckets per unit of log2(distance / exact)
     uint16_t first[TE_RELPOS_MAX_BUCKETS];   // smallest distance of each bucket of a side
 };
 
-template <int HD, int TL>
+// Several query tiles a CTA, four softmax warps each, and four warps that feed them.
+template <int HD>
 struct SLayout {
     static constexpr int NB = HD / 64;              // 64-column boxes per tile row
-    static constexpr int TILE = 128 * HD * 2;       // one 128-row tile
-    static constexpr int Q_OFF = 0;                 // Q[TL]
-    static constexpr int K_OFF = TL * TILE;         // K[2]
-    static constexpr int V_OFF = K_OFF + 2 * TILE;  // V[2]
-    static constexpr int BAR_OFF = V_OFF + 2 * TILE;
-    static constexpr int NTHREADS = 32 * (4 * TL + 2);   // softmax warps, MMA warp, TMA warp
-    static constexpr int MMA_WARP = 4 * TL, TMA_WARP = 4 * TL + 1;
-    static constexpr int NBAR = 1 + 2 + 2 + 2 + 2 + 2 + 2 + 1 + 2 + 1;
-    static constexpr int TAB_OFF = BAR_OFF + 8 * NBAR + 16;   // the head's table column, then the spread bias
-    static constexpr int S_COL = 0;                 // S: TL x 128 f32 columns
-    static constexpr int P_COL = TL == 1 ? 128 : 0; // TL = 1: 64 columns of its own; TL = 2: over S
-    static constexpr int O_COL = TL == 1 ? 192 : TL * 128;   // O: TL x HD f32 columns
-    static constexpr int COLS = TL == 1 ? 256 : 512;
-    static_assert(TL == 2 || HD == 64, "one tile a CTA is the hd = 64 form");
-    static_assert(O_COL + TL * HD <= COLS, "TMEM budget");
+    static constexpr int NT = HD == 64 ? 3 : 2;     // query tiles
+    static constexpr int NQ = HD == 64 ? 2 : 1;     // Q buffers: the next item's Q beside this one's
+    static constexpr int R = HD == 64 ? 4 : 3;      // K and V tiles in flight
+    static constexpr int QTILE = BQ * HD * 2, TILE = BKV * HD * 2;
+    static constexpr int QBOX = BQ * 128, BOX = BKV * 128;   // 64 columns of them
+    static constexpr int Q_OFF = 0;                 // Q[NQ][NT]
+    static constexpr int K_OFF = NQ * NT * QTILE;   // K[R]
+    static constexpr int V_OFF = K_OFF + R * TILE;  // V[R]
+    static constexpr int STG_OFF = V_OFF + R * TILE;         // a softmax warp's 32 rows of 32 outputs
+    static constexpr int STG_WARP = 32 * 64;
+    // warps: softmax (4 a query tile), 2 that issue MMAs, TMA, bias
+    static constexpr int SOFTMAX_WARPS = 4 * NT, MMA_WARP = SOFTMAX_WARPS, TMA_WARP = MMA_WARP + 2;
+    static constexpr int NTHREADS = 32 * (SOFTMAX_WARPS + 4);
+    // registers a thread at launch, and after the softmax warps took over what the others do not need
+    static constexpr int LAUNCH_REGS = HD == 64 ? 128 : 168, SOFTMAX_REGS = HD == 64 ? 144 : 208, OTHER_REGS = HD == 64 ? 80 : 88;
+    static_assert(NT * SOFTMAX_REGS + OTHER_REGS <= (NT + 1) * LAUNCH_REGS && LAUNCH_REGS * NTHREADS <= 65536, "register split");
+    static constexpr int BAR_OFF = STG_OFF + SOFTMAX_WARPS * STG_WARP;
+    // barriers
+    static constexpr int BAR_Q = 0;                      // [NQ][NT] Q loaded, per buffer and query tile
+    static constexpr int BAR_QE = BAR_Q + NT * NQ;       // [NQ][NT] Q read by the item's last S
+    static constexpr int BAR_KF = BAR_QE + NT * NQ;      // [R] K loaded
+    static constexpr int BAR_KE = BAR_KF + R;            // [R] K read by both MMA warps
+    static constexpr int BAR_VF = BAR_KE + R;            // [R] V loaded
+    static constexpr int BAR_VE = BAR_VF + R;            // [R] V read by both
+    static constexpr int BAR_SF = BAR_VE + R;            // [NT] S ready
+    static constexpr int BAR_SFREE = BAR_SF + NT;        // [NT] S is in registers
+    static constexpr int BAR_PF = BAR_SFREE + NT;        // [NT] P written
+    static constexpr int BAR_PV = BAR_PF + NT;           // [NT] its PV done
+    static constexpr int BAR_OFREE = BAR_PV + NT;        // [NT] O is in registers
+    static constexpr int BAR_REC = BAR_OFREE + NT;       // [4] item record written
+    static constexpr int BAR_RECE = BAR_REC + 4;         // [4] item record read
+    static constexpr int BAR_CLC = BAR_RECE + 4;         // the next CTA's place taken over, or not
+    static constexpr int BAR_BF = BAR_CLC + 1;           // [2] bias spread
+    static constexpr int BAR_BE = BAR_BF + 2;            // [2] bias no longer read
+    static constexpr int BAR_FIN = BAR_BE + 2;           // [2] every MMA and commit of an MMA warp is done
+    static constexpr int NBAR = BAR_FIN + 2;
+    static constexpr int REC_OFF = (BAR_OFF + 8 * NBAR + 15) / 16 * 16;   // 4 records of 16 bytes, the taken place
+    static constexpr int SLOT_OFF = REC_OFF + 80;        // TMEM base
+    static constexpr int TAB_OFF = SLOT_OFF + 16;        // the head's table column, then the spread biases
+    // TMEM columns of a query tile: S (64 f32), P (64 bf16), O (HD f32)
+    static constexpr int P_COL = 64, O_COL = 96, TILE_COLS = 96 + HD;
+    static_assert(NT * TILE_COLS <= 512, "TMEM budget");
     // the widest bias: every distance to TE_RELPOS_MAX_DISTANCE to either side
     static_assert(TAB_OFF + 4 * (TE_RELPOS_MAX_BUCKETS + 2 * (TE_RELPOS_MAX_DISTANCE + PAD) + 1) + 1024 <= 227 * 1024,
                   "shared memory per CTA");
@@ -100,6 +130,9 @@ struct SLayout {
 struct KeyTiles {
     int sink, first, end;
     __device__ __forceinline__ bool has(int t) const { return t < end && (t >= first || t < sink); }
+    __device__ __forceinline__ int count() const { return sink + end - first; }
+    // the j-th of them
+    __device__ __forceinline__ int tile(int j) const { return j < sink ? j : j + first - sink; }
 };
 __device__ __forceinline__ KeyTiles key_tiles(const SpanParams &p, int r0, int r1, int len) {
     const int lo = r0 > p.left ? r0 - p.left : 0;
@@ -145,7 +178,7 @@ __device__ __forceinline__ void add_bias(uint32_t (&v)[64], uint64_t c2, const f
 // tiled form computes, without products of masked values.  It ends at once when
 // all of the row is lost.
 template <int HD, bool BIAS>
-__device__ __noinline__ void mend_row(const SpanParams &p, const float *bias, int off, int len, int h, int qi) {
+__device__ __forceinline__ void mend_row(const SpanParams &p, const float *bias, int off, int len, int h, int qi) {
     constexpr int C = HD / 32;
     const int lane = threadIdx.x & 31, g = h / p.group;
     const __nv_bfloat16 *q = p.qkv + (long long)(off + qi) * p.ld + p.q_off + h * HD;
@@ -202,54 +235,16 @@ __device__ __noinline__ void mend_row(const SpanParams &p, const float *bias, in
     for (int c = 0; c < C; ++c) orow[c] = __float2bfloat16_rn(l == 0.f ? 0.f : o[c] / l);
 }
 
-template <int HD, int TL, bool BIAS>
-__global__ void __launch_bounds__(SLayout<HD, TL>::NTHREADS, TL == 1 ? 2 : 1)
-    attn_span_kernel(const __grid_constant__ SpanParams p) {
-    using L = SLayout<HD, TL>;
-    constexpr int QB = TL * BQ;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    const uint32_t sb = smem_u32(smem);
-    const uint32_t bar_q = sb + L::BAR_OFF;
-    const uint32_t bar_kf = bar_q + 8;             // [2] K loaded
-    const uint32_t bar_vf = bar_kf + 16;           // [2] V loaded
-    const uint32_t bar_kve = bar_vf + 16;          // [2] K and V read (TL = 1: V)
-    const uint32_t bar_sf = bar_kve + 16;          // [2] S ready, per query tile
-    const uint32_t bar_pf = bar_sf + 16;           // [2] P written, per query tile
-    const uint32_t bar_pv = bar_pf + 16;           // [2] PV done, per query tile
-    const uint32_t bar_fin = bar_pv + 16;
-    const uint32_t bar_ke = bar_fin + 8;           // [2] TL = 1: K(j) read by S(j)
-    const uint32_t bar_sfree = bar_ke + 16;        // TL = 1: the softmax has read S(j)
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::BAR_OFF + 8 * L::NBAR);
-    float *tab = reinterpret_cast<float *>(smem + L::TAB_OFF);
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == L::TMA_WARP && lane == 0) {
-        tma_prefetch_desc(&p.map);
-        mbar_init(bar_q, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar_kf + 8 * i, 1);
-            mbar_init(bar_vf + 8 * i, 1);
-            mbar_init(bar_kve + 8 * i, 1);
-            mbar_init(bar_sf + 8 * i, 1);
-            mbar_init(bar_pf + 8 * i, 4);
-            mbar_init(bar_pv + 8 * i, 1);
-            mbar_init(bar_ke + 8 * i, 1);
-        }
-        mbar_init(bar_sfree, 4);
-        mbar_init(bar_fin, 1);
-        fence_mbar_init();
-    }
-    if (warp == L::MMA_WARP) tmem_alloc(smem_u32(tmem_slot), L::COLS);
-    // from here on global memory is touched
-    prior_wait();
-
+// The work of CTA `b` of the grid: which rows of which sequence, and the head.
+struct Item {
+    int off, len, q0, h;    // len 0: nothing
+};
+template <int QB>
+__device__ __forceinline__ Item item_of(const SpanParams &p, int b, int lane) {
     int seq, qblk, h;
     if (p.nwork) {
         // CTAs take the heads in groups of hgroup: within a group, work items in
-        // list order (most key tiles first), the group's heads fastest
-        const int b = blockIdx.x;
+        // list order (most keys first), the group's heads fastest
         const int per = p.hgroup * p.nwork;
         const int g = b / per;
         const int r = b - g * per;
@@ -263,8 +258,8 @@ __global__ void __launch_bounds__(SLayout<HD, TL>::NTHREADS, TL == 1 ? 2 : 1)
     } else {
         // many blocks: sequence s has the slots from cu[s] / QB + s on, at least
         // as many as it has query blocks
-        const int slot = blockIdx.x / p.nq;
-        h = blockIdx.x - slot * p.nq;
+        const int slot = b / p.nq;
+        h = b - slot * p.nq;
         int lo = 0, hi = p.nseq;
         while (hi - lo > 1) {
             const int step = (hi - lo + 31) / 32;
@@ -277,298 +272,554 @@ __global__ void __launch_bounds__(SLayout<HD, TL>::NTHREADS, TL == 1 ? 2 : 1)
         seq = lo;
         qblk = slot - (p.cu[seq] / QB + seq);
     }
-    const int off = p.cu[seq], len = p.cu[seq + 1] - off;
-    const int q0 = qblk * QB;
+    const int off = p.cu[seq], len = p.cu[seq + 1] - off, q0 = qblk * QB;
     // else: nothing to do, or a device table that is not the host's
-    bool live = off >= 0 && len >= 1 && (long long)off + len <= p.total && qblk >= 0 && q0 < len;
-    const int g = h / p.group;
-    const int ntile = TL == 2 && q0 + BQ < len ? 2 : 1;   // tile B exists
-    const int last_row = (q0 + QB < len ? q0 + QB : len) - 1;
-    const KeyTiles all = key_tiles(p, q0, last_row, len);
-    const int n = all.sink + all.end - all.first;
-    auto tile_of = [&](int j) { return j < all.sink ? j : all.first + (j - all.sink); };
-    // the key tiles of query tile w (TL = 1: every one)
-    auto tiles_of = [&](int w) {
-        const int r0 = q0 + w * BQ, r1 = r0 + BQ - 1;
-        return TL == 1 ? all : key_tiles(p, r0, r1 < len ? r1 : len - 1, len);
-    };
+    const bool live = off >= 0 && len >= 1 && (long long)off + len <= p.total && qblk >= 0 && q0 < len;
+    return {off, live ? len : 0, q0, h};
+}
 
+// Takes over the place of a CTA of this grid that has not started yet; the
+// answer (16 bytes) lands at dst and completes 16 bytes on bar.
+__device__ __forceinline__ void take_next(uint32_t dst, uint32_t bar, uint32_t e) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n\t}" ::"r"(dst),
+        "r"(bar), "r"(e)
+        : "memory");
+}
+// The block index taken over, or -1: none was left.
+__device__ __forceinline__ int taken(uint32_t src) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(src)
+        : "memory");
+    return got ? (int)x : -1;
+}
+
+template <int HD, bool BIAS>
+__global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(const __grid_constant__ SpanParams p) {
+    using L = SLayout<HD>;
+    constexpr int NT = L::NT, QB = NT * BQ, R = L::R;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem);
+    auto bar = [&](int i) { return sb + L::BAR_OFF + 8 * i; };
+    volatile int4 *rec = reinterpret_cast<volatile int4 *>(smem + L::REC_OFF);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::SLOT_OFF);
+    float *tab = reinterpret_cast<float *>(smem + L::TAB_OFF);
+    const int nb = p.two_sided ? 2 * p.side : p.side, width = p.reach + PAD;
+    // the distance 0 of spread bias i
+    auto spread_of = [&](int i) { return tab + nb + width + i * (2 * width + 1); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == L::TMA_WARP && lane == 0) {
-        // an earlier CTA gave up a wait: one thread's reading holds for the CTA
-        live = live && *reinterpret_cast<volatile int *>(&g_span_err) == 0;
-        tmem_slot[1] = live;
-        if (live) mbar_arrive_expect_tx(bar_q, ntile * L::TILE);
-        for (int w = 0; w < ntile && live; ++w)
-            for (int c = 0; c < L::NB; ++c)
-                tma_load_2d(sb + L::Q_OFF + w * L::TILE + c * 16384, &p.map, bar_q, p.q_off + h * HD + 64 * c,
-                            off + q0 + w * BQ);
+        tma_prefetch_desc(&p.map);
+        for (int i = 0; i < 2 * NT * L::NQ; ++i) mbar_init(bar(L::BAR_Q + i), 1);
+        for (int i = 0; i < R; ++i) {
+            mbar_init(bar(L::BAR_KF + i), 1);
+            mbar_init(bar(L::BAR_KE + i), 2);
+            mbar_init(bar(L::BAR_VF + i), 1);
+            mbar_init(bar(L::BAR_VE + i), 2);
+        }
+        for (int i = 0; i < NT; ++i) {
+            mbar_init(bar(L::BAR_SF + i), 1);
+            mbar_init(bar(L::BAR_SFREE + i), 4);
+            mbar_init(bar(L::BAR_PF + i), 4);
+            mbar_init(bar(L::BAR_PV + i), 1);
+            mbar_init(bar(L::BAR_OFREE + i), 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(L::BAR_REC + i), 1);
+            mbar_init(bar(L::BAR_RECE + i), L::SOFTMAX_WARPS + 2 + (BIAS ? 1 : 0));
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(L::BAR_BF + i), 1);
+            mbar_init(bar(L::BAR_BE + i), L::SOFTMAX_WARPS);
+            mbar_init(bar(L::BAR_FIN + i), 1);
+        }
+        mbar_init(bar(L::BAR_CLC), 1);
+        fence_mbar_init();
     }
+    if (warp == L::MMA_WARP) tmem_alloc(smem_u32(tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // from here on global memory is touched
+    prior_wait();
     next_go();
     const uint32_t tbase = tmem_slot[0];
-    live = tmem_slot[1] != 0;
     bool ok = true;
+    // waits of a whole warp; false: given up
+    auto wait = [&](int b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar(b), parity & 1)) != 0; };
+    // The same in two parts: test looks without waiting, settle comes once the
+    // answer is needed; a look at a barrier costs its latency, which the work
+    // between the two hides.
+    auto test = [&](int b, uint32_t parity) { return mbar_test(bar(b), parity & 1); };
+    auto settle = [&](bool there, int b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, there) || wait(b, parity); };
+    // the record of the CTA's item number it, read by a whole warp
+    auto get_record = [&](int it) {
+        const volatile int4 *q = rec + (it & 3);
+        return Item{q->x, q->y, q->z, q->w};
+    };
+    auto let_record = [&](int it) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::BAR_RECE + (it & 3)));
+    };
+    auto read_record = [&](int it, Item &r) {
+        if (!wait(L::BAR_REC + (it & 3), it >> 2)) return false;
+        r = get_record(it);
+        let_record(it);
+        return true;
+    };
+    // the key tiles of an item in the order they are taken, and those of its query tile w
+    auto tiles_of = [&](const Item &r) {
+        return key_tiles(p, r.q0, r.q0 + QB < r.len ? r.q0 + QB - 1 : r.len - 1, r.len);
+    };
+    auto tiles_of_w = [&](const Item &r, int w) {
+        const int r0 = r.q0 + w * BQ;
+        return r0 < r.len ? key_tiles(p, r0, r0 + BQ < r.len ? r0 + BQ - 1 : r.len - 1, r.len) : KeyTiles{0, 0, 0};
+    };
+    // place and phase in a ring of R
+    struct Ring {
+        int at;
+        uint32_t phase;
+        __device__ __forceinline__ void step() {
+            if (++at == R) { at = 0; phase ^= 1; }
+        }
+    };
 
-    if (!live) {
-    } else if (warp == L::TMA_WARP) {
-        // ------------------------------------------------------ TMA producer
-        // (the whole warp in step, one elected lane issues)
-        const uint32_t e = elect_one();
-        // K(i) into ring slot i & 1 once its previous occupant K(i - 2) is
-        // free (TL = 1: read by S(i - 2); TL = 2: K and V free together after
-        // PV(i - 2)); V(i) once PV(i - 2) is done
-        auto load_k = [&](int i) -> bool {
-            const int st = i & 1;
-            const uint32_t fb = TL == 1 ? bar_ke : bar_kve;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(fb + 8 * st, ((i >> 1) & 1) ^ 1))) return false;
-            mbar_arrive_expect_tx_e(bar_kf + 8 * st, L::TILE, e);
-            for (int c = 0; c < L::NB; ++c)
-                tma_load_2d_e(sb + L::K_OFF + st * L::TILE + c * 16384, &p.map, bar_kf + 8 * st,
-                              p.k_off + g * HD + 64 * c, off + tile_of(i) * BKV, e);
-            return true;
-        };
-        auto load_v = [&](int i) -> bool {
-            const int st = i & 1;
-            if (TL == 1 && !__all_sync(0xFFFFFFFFu, mbar_wait(bar_kve + 8 * st, ((i >> 1) & 1) ^ 1))) return false;
-            mbar_arrive_expect_tx_e(bar_vf + 8 * st, L::TILE, e);
-            for (int c = 0; c < L::NB; ++c)
-                tma_load_2d_e(sb + L::V_OFF + st * L::TILE + c * 16384, &p.map, bar_vf + 8 * st,
-                              p.v_off + g * HD + 64 * c, off + tile_of(i) * BKV, e);
-            return true;
-        };
-        int nk = 0, nv = 0;   // K and V tiles issued
-        if (TL == 1) {
-            // K runs one tile ahead of V: S(j + 1) needs it while PV(j) waits for P(j)
-            if (n > 0 && (ok = load_k(0))) nk = 1;
-            for (; nv < n && ok; ++nv) {
-                if (nk < n) {
-                    if (!(ok = load_k(nk))) break;
-                    ++nk;
-                }
-                if (!(ok = load_v(nv))) break;
-            }
-        } else {
-            for (; nv < n && ok; ++nv) {
-                if (!(ok = load_k(nv))) break;
-                ++nk;
-                ok = load_v(nv);
-            }
-        }
-        // no copy of ours may still be landing when the CTA exits
-        mbar_wait(bar_q, 0, 20000000ull);
-        for (int i = nk - 2 < 0 ? 0 : nk - 2; i < nk; ++i) mbar_wait(bar_kf + 8 * (i & 1), (i >> 1) & 1, 20000000ull);
-        for (int i = nv - 2 < 0 ? 0 : nv - 2; i < nv; ++i) mbar_wait(bar_vf + 8 * (i & 1), (i >> 1) & 1, 20000000ull);
-    } else if (warp == L::MMA_WARP) {
-        // ------------------------------------------------------- MMA issuer
-        // (the whole warp in step, one elected lane issues)
-        const uint32_t e = elect_one();
-        constexpr uint32_t idesc_s = idesc_bf16_f32(128, BKV);
-        constexpr uint32_t idesc_pv = idesc_bf16_f32(128, HD) | (1u << 16);   // B MN-major
-        const uint64_t kd0 = smem_desc_sw128(sb + L::K_OFF), kd1 = smem_desc_sw128(sb + L::K_OFF + L::TILE);
-        const uint64_t vd0 = smem_desc_mn_sw128(sb + L::V_OFF, 16384);
-        const uint64_t vd1 = smem_desc_mn_sw128(sb + L::V_OFF + L::TILE, 16384);
-        auto issue_s = [&](int w, int j) -> bool {
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_kf + 8 * (j & 1), (j >> 1) & 1))) return false;
-            tc_fence_after();
-            const uint64_t k0 = (j & 1) ? kd1 : kd0;
-            const uint64_t q0d = smem_desc_sw128(sb + L::Q_OFF + w * L::TILE);
+    if (warp >= L::SOFTMAX_WARPS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::OTHER_REGS));
+        if (warp == L::TMA_WARP) {
+            // ------------------------------------- scheduling and TMA producer
+            // (the whole warp in step, one elected lane issues)
+            const uint32_t e = elect_one();
+            int next = *reinterpret_cast<volatile int *>(&g_span_err) == 0 ? (int)blockIdx.x : -1;
+            next = __shfl_sync(0xFFFFFFFFu, next, 0);
+            Ring kr = {0, 0}, vr = {0, 0};
+            int kn = 0, vn = 0;                          // K and V tiles issued in all
+            int asked = 0;                               // places asked for
+            uint32_t qn[NT];                             // Q loads of each query tile
 #pragma unroll
-            for (int k = 0; k < HD / 16; ++k) {
-                const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                mma_ss_bf16_e(tbase + L::S_COL + w * 128, q0d + o, k0 + o, idesc_s, k > 0, e);
-            }
-            mma_commit_e(bar_sf + 8 * w, e);
-            if (TL == 1) mma_commit_e(bar_ke + 8 * (j & 1), e);   // K(j) read
-            return true;
-        };
-        auto issue_pv = [&](int w, int j, bool more) {
-            const uint64_t v0 = (j & 1) ? vd1 : vd0;
-#pragma unroll
-            for (int s2 = 0; s2 < BKV / 16; ++s2)
-                mma_ts_bf16_e(tbase + L::O_COL + w * HD, tbase + L::P_COL + w * 128 + 8 * s2,
-                              v0 + (uint64_t)(128 * s2), idesc_pv, more || s2 != 0, e);
-            mma_commit_e(bar_pv + 8 * w, e);
-        };
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_q, 0));
-        if (TL == 1) {
-            ok = ok && issue_s(0, 0);
-            // S(j+1) as soon as the softmax has read S(j) (P has columns of
-            // its own), then PV(j) once P(j) is written
-            for (int j = 0; j < n && ok; ++j) {
-                if (j + 1 < n) {
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_sfree, j & 1))) { ok = false; break; }
-                    tc_fence_after();
-                    if (!(ok = issue_s(0, j + 1))) break;
-                }
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_vf + 8 * (j & 1), (j >> 1) & 1)) ||
-                    !__all_sync(0xFFFFFFFFu, mbar_wait(bar_pf, j & 1))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                issue_pv(0, j, j > 0);
-                mma_commit_e(bar_kve + 8 * (j & 1), e);   // V(j) read
-            }
-        } else {
-            // PV_A(j), S_A(j+1), PV_B(j), S_B(j+1), each only where the query
-            // tile sees the key tile; S_w overwrites the P_w that PV_w reads
-            // (not ordered by the tensor pipe): it waits for PV_w
-            const KeyTiles kw[2] = {tiles_of(0), ntile == 2 ? tiles_of(1) : KeyTiles{0, 0, 0}};
-            int done[2] = {0, 0};   // key tiles of each query tile whose PV is issued
-            for (int w = 0; w < 2 && ok; ++w)
-                if (kw[w].has(tile_of(0))) ok = issue_s(w, 0);
-            for (int j = 0; j < n && ok; ++j) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_vf + 8 * (j & 1), (j >> 1) & 1))) { ok = false; break; }
-                const int t = tile_of(j), tn = tile_of(j + 1);
-                const bool b_too = kw[1].has(t);
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if (ok && kw[w].has(t)) {
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_pf + 8 * w, done[w] & 1))) { ok = false; break; }
-                        tc_fence_after();
-                        issue_pv(w, j, done[w] > 0);
-                        ++done[w];
-                    }
-                    // K(j), V(j) are free once the last PV(j) is done
-                    if (ok && w == (b_too ? 1 : 0)) mma_commit_e(bar_kve + 8 * (j & 1), e);
-                    if (ok && j + 1 < n && kw[w].has(tn))
-                        ok = (done[w] == 0 || __all_sync(0xFFFFFFFFu, mbar_wait(bar_pv + 8 * w, (done[w] - 1) & 1))) &&
-                             issue_s(w, j + 1);
-                }
-            }
-        }
-        mma_commit_e(bar_fin, e);
-        __all_sync(0xFFFFFFFFu, mbar_wait(bar_fin, 0, 20000000ull));
-    } else if (warp < 4 * ntile) {
-        // ---------------------------------------- softmax, one query per thread
-        const int w = warp >> 2;                         // query tile of this warpgroup
-        const int wq = warp & 3;                         // TMEM lane quadrant
-        const int r0 = q0 + w * BQ + 32 * wq;            // the warp's first row
-        const int qi = r0 + lane;
-        const int rl = r0 + 31 < len - 1 ? r0 + 31 : len - 1;   // its last row
-        const uint32_t tl = (uint32_t)(32 * wq) << 16;
-        const uint32_t scol = tbase + tl + L::S_COL + w * 128;
-        const uint32_t pcol = tbase + tl + L::P_COL + w * 128;
-        const uint32_t ocol = tbase + tl + L::O_COL + w * HD;
-        const float c = p.scale_log2;
-        const KeyTiles mine = tiles_of(w);
-        const float *bias = nullptr;                     // bias[d]: distance d, -(reach + PAD) .. reach + PAD
-        if constexpr (BIAS) {
-            // spread the head's bias over the distances while Q and K(0) are on their way
-            const int nb = p.two_sided ? 2 * p.side : p.side, width = p.reach + PAD, nt = 128 * ntile;
-            for (int b = threadIdx.x; b < nb; b += nt) {
-                // log2 units; a finite bias stays finite (the type's lowest value still masks softly)
-                const float t = p.table[(long long)b * p.ldt + h], t2 = t * 1.4426950408889634f;
-                tab[b] = fabsf(t) <= FLT_MAX ? fminf(fmaxf(t2, -FLT_MAX), FLT_MAX) : t;
-            }
-            asm volatile("bar.sync 1, %0;" ::"r"(nt) : "memory");
-            float *spread = tab + nb + width;
-            for (int d = (int)threadIdx.x - width; d <= width; d += nt)
-                spread[d] = bias_of(p, tab, d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d));
-            asm volatile("bar.sync 1, %0;" ::"r"(nt) : "memory");
-            bias = spread;
-        }
-        float m_used = -INFINITY, l = 0.f;
-        int jj = 0;                                      // key tiles done
-        for (int j = 0; j < n; ++j) {
-            const int t = tile_of(j);
-            if (TL == 2 && !mine.has(t)) continue;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_sf + 8 * w, jj & 1));
-            if (!ok) break;
-            // TL = 2: S_w landed, so the PV_w before it is done: P_w and O_w may
-            // be touched.  TL = 1: see below.
-            tc_fence_after();
-            const int kv0 = t * BKV;
-            // the S row once into registers for all passes
-            uint32_t v0[64], v1[64];
-            tmem_ld64(scol, v0);
-            tmem_ld64(scol + 64, v1);
-            tmem_wait_ld();
-            if (TL == 1) {
-                // S(j) is in registers: the tensor core may compute S(j+1)
-                tc_fence_before();
+            for (int w = 0; w < NT; ++w) qn[w] = 0;
+            // asks for the place of a CTA that has not started; after answer(), which reads it
+            auto ask = [&]() {
+                // the answer before was read: order that before it is overwritten
+                fence_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_sfree);
-            }
-            // scores in log2 units are s * cs + cb
-            float cs = c, cb = 0.f;
-            if constexpr (BIAS) {
-                const int dlo = kv0 - (r0 + 31), dhi = kv0 + BKV - 1 - r0;   // the warp's distances
-                const bool before = dhi <= -p.reach, behind = dlo >= p.reach;
-                const uint64_t c2 = f2_pack(c, c);
-                const float far = before || behind ? bias[before ? -p.reach : p.reach] : 0.f;
-                if ((before || behind) && fabsf(far) <= 8192.f) {
-                    cb = far;
-                } else if (before || behind) {
-                    // so large that it takes the scores' own digits, as it does beside a near tile
-                    add_bias<true>(v0, c2, nullptr, far);
-                    add_bias<true>(v1, c2, nullptr, far);
-                    cs = 1.f;
-                } else {
-                    add_bias<false>(v0, c2, bias + (kv0 - qi), 0.f);
-                    add_bias<false>(v1, c2, bias + (kv0 - qi) + 64, 0.f);
-                    cs = 1.f;
+                mbar_arrive_expect_tx_e(bar(L::BAR_CLC), 16, e);
+                take_next(sb + L::REC_OFF + 64, bar(L::BAR_CLC), e);
+                ++asked;
+            };
+            auto answer = [&]() {
+                if (!wait(L::BAR_CLC, asked - 1)) { ok = false; return -1; }
+                const int b = taken(sb + L::REC_OFF + 64);
+                __syncwarp();
+                return b;
+            };
+            // The next item with rows, from block `next` on; publishes its record
+            // (len 0: no more) as the CTA's item number it.
+            auto publish = [&](int it, Item &r) {
+                r = {0, 0, 0, 0};
+                while (next >= 0 && ok) {
+                    r = item_of<QB>(p, next, lane);
+                    ask();
+                    if (r.len > 0) break;
+                    next = answer();
                 }
-            }
-            // some row of the warp does not see some key of the tile
-            const bool whole = kv0 + BKV <= len && kv0 + BKV - 1 <= r0 + p.right &&
-                               (kv0 >= rl - p.left || kv0 + BKV <= p.sinks);
-            if (!whole) {
-                const int hi = (qi + p.right < len ? qi + p.right + 1 : len) - kv0;   // keys below it are not too far
-                const int lo = qi - p.left - kv0, sk = p.sinks - kv0;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const uint32_t see =
-                        bits_below(hi - 32 * x) & (~bits_below(lo - 32 * x) | bits_below(sk - 32 * x));
-                    uint32_t *v = x < 2 ? v0 + 32 * x : v1 + 32 * (x - 2);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!(see >> e & 1)) v[e] = 0xFF800000u;   // -inf
+                if (!ok || !wait(L::BAR_RECE + (it & 3), (it >> 2) ^ 1)) { ok = false; return; }
+                if (lane == 0) {
+                    volatile int4 *q = rec + (it & 3);
+                    q->x = r.off;
+                    q->y = r.len;
+                    q->z = r.q0;
+                    q->w = r.h;
+                    mbar_arrive(bar(L::BAR_REC + (it & 3)));
                 }
-            }
-            // pass 1: the row maximum, eight partial ones
-            float m8[8];
+                __syncwarp();
+            };
+            Item r;
+            publish(0, r);
+            for (int it = 0; ok && r.len > 0; ++it) {
+                const int g = r.h / p.group;
+                const KeyTiles tiles = tiles_of(r);
+                const int n = tiles.count();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m8[i] = fmaxf(__uint_as_float(v0[i]), __uint_as_float(v1[i]));
-#pragma unroll
-            for (int e = 8; e < 64; ++e) m8[e & 7] = fmax3(m8[e & 7], __uint_as_float(v0[e]), __uint_as_float(v1[e]));
-            const float mx = fmaf(fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                        fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))), cs, cb);
-            if (TL == 1 && jj > 0) {
-                // P and O are free once the PV before is done
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_pv, (jj - 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
-            }
-            const bool resc = mx > m_used + 8.f;
-            if (__any_sync(0xFFFFFFFFu, resc)) {
-                const float alpha = resc ? hw_exp2(m_used - mx) : 1.f;
-                if (resc) m_used = mx;
-                l *= alpha;
-                if (jj > 0) {
-#pragma unroll
-                    for (int cc = 0; cc < HD / 32; ++cc) {
-                        uint32_t v[32];
-                        tmem_ld32(ocol + 32 * cc, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-                        tmem_st32(ocol + 32 * cc, v);
+                for (int w = 0; w < NT; ++w) {
+                    if (!ok || r.q0 + w * BQ >= r.len) break;
+                    const int qb = L::NQ == 2 ? NT * (qn[w] & 1) + w : w;
+                    if (!wait(L::BAR_QE + qb, (L::NQ == 2 ? qn[w] >> 1 : qn[w]) ^ 1)) { ok = false; break; }
+                    ++qn[w];
+                    mbar_arrive_expect_tx_e(bar(L::BAR_Q + qb), L::QTILE, e);
+                    for (int c = 0; c < 2 * L::NB; ++c)   // 64 columns, 64 rows a box
+                        tma_load_2d_e(sb + L::Q_OFF + qb * L::QTILE + c * L::BOX, &p.map, bar(L::BAR_Q + qb),
+                                      p.q_off + r.h * HD + 64 * (c >> 1), r.off + r.q0 + w * BQ + BKV * (c & 1), e);
+                }
+                auto load_k = [&](int j) -> bool {
+                    if (!wait(L::BAR_KE + kr.at, kr.phase ^ 1)) return false;
+                    mbar_arrive_expect_tx_e(bar(L::BAR_KF + kr.at), L::TILE, e);
+                    for (int c = 0; c < L::NB; ++c)
+                        tma_load_2d_e(sb + L::K_OFF + kr.at * L::TILE + c * L::BOX, &p.map, bar(L::BAR_KF + kr.at),
+                                      p.k_off + g * HD + 64 * c, r.off + tiles.tile(j) * BKV, e);
+                    kr.step();
+                    ++kn;
+                    return true;
+                };
+                auto load_v = [&](int j) -> bool {
+                    if (!wait(L::BAR_VE + vr.at, vr.phase ^ 1)) return false;
+                    mbar_arrive_expect_tx_e(bar(L::BAR_VF + vr.at), L::TILE, e);
+                    for (int c = 0; c < L::NB; ++c)
+                        tma_load_2d_e(sb + L::V_OFF + vr.at * L::TILE + c * L::BOX, &p.map, bar(L::BAR_VF + vr.at),
+                                      p.v_off + g * HD + 64 * c, r.off + tiles.tile(j) * BKV, e);
+                    vr.step();
+                    ++vn;
+                    return true;
+                };
+                // K runs one tile ahead of V: S(j + 1) comes before PV(j)
+                Item r2 = {0, 0, 0, 0};
+                if (ok) ok = load_k(0);
+                for (int j = 0; j < n && ok; ++j) {
+                    if (j + 1 < n && !(ok = load_k(j + 1))) break;
+                    if (!(ok = load_v(j))) break;
+                    if (j == 0) {
+                        // the next item, well before this one ends
+                        next = answer();
+                        if (ok) publish(it + 1, r2);
                     }
-                    tmem_wait_st();
+                }
+                r = r2;
+            }
+            if (!ok) {
+                // no copy of ours may still be landing when the CTA exits
+#pragma unroll
+                for (int w = 0; w < NT; ++w)
+                    for (int x = 0; x < L::NQ; ++x)
+                        if ((int)qn[w] > x) {
+                            const uint32_t u = qn[w] - 1 - x;
+                            mbar_wait(bar(L::BAR_Q + (L::NQ == 2 ? NT * (u & 1) + w : w)), (L::NQ == 2 ? u >> 1 : u) & 1, 20000000ull);
+                        }
+                for (int i = kn - R < 0 ? 0 : kn - R; i < kn; ++i) mbar_wait(bar(L::BAR_KF + i % R), (i / R) & 1, 20000000ull);
+                for (int i = vn - R < 0 ? 0 : vn - R; i < vn; ++i) mbar_wait(bar(L::BAR_VF + i % R), (i / R) & 1, 20000000ull);
+                if (asked) mbar_wait(bar(L::BAR_CLC), (asked - 1) & 1, 20000000ull);
+            }
+        } else if (warp < L::TMA_WARP) {
+            // ------------- MMA issuer of query tiles w0 .. w0 + U - 1 (the second may not exist)
+            // (the whole warp in step, one elected lane issues)
+            constexpr int U = (NT + 1) / 2;
+            const int w0 = (warp - L::MMA_WARP) * U;
+            const uint32_t e = elect_one();
+            constexpr uint32_t idesc_s = idesc_bf16_f32(BQ, BKV);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(BQ, HD) | (1u << 16);   // B MN-major
+            const uint64_t kd = smem_desc_sw128(sb + L::K_OFF);
+            const uint64_t vd = smem_desc_mn_sw128(sb + L::V_OFF, L::BOX);
+            const uint64_t qd = smem_desc_sw128(sb + L::Q_OFF);
+            uint32_t sc[U], pc[U], items[U], qn[U];      // S and PV issued, items begun (as PV, as Q see them)
+#pragma unroll
+            for (int u = 0; u < U; ++u) sc[u] = pc[u] = items[u] = qn[u] = 0;
+            Ring kr = {0, 0}, vr = {0, 0};               // the K tile whose S, the V tile whose PV comes next
+            auto lane_arrive = [&](int b) {
+                asm volatile(
+                    "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar(b)),
+                    "r"(e)
+                    : "memory");
+            };
+            // S = Q K^T of the next K tile, key tile t, for the query tiles that see it
+            auto step_s = [&](const KeyTiles (&kw)[U], int t) -> bool {
+                if (!wait(L::BAR_KF + kr.at, kr.phase)) return false;
+                const uint64_t k0 = kd + (uint64_t)(kr.at * (L::TILE >> 4));
+                bool any = false;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (!kw[u].has(t)) continue;
+                    const int w = w0 + u;
+                    // the softmax has the last S in registers
+                    if (sc[u] > 0 && !wait(L::BAR_SFREE + w, sc[u] - 1)) return false;
+                    tc_fence_after();
+                    const int qb = L::NQ == 2 ? NT * ((qn[u] - 1) & 1) + w : w;
+                    const uint64_t q0 = qd + (uint64_t)(qb * (L::QTILE >> 4));
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k)
+                        mma_ss_bf16_e(tbase + w * L::TILE_COLS, q0 + (((k >> 2) * L::QBOX + (k & 3) * 32) >> 4),
+                                      k0 + (((k >> 2) * L::BOX + (k & 3) * 32) >> 4), idesc_s, k > 0, e);
+                    mma_commit_e(bar(L::BAR_SF + w), e);
+                    ++sc[u];
+                    any = true;
+                }
+                if (any) mma_commit_e(bar(L::BAR_KE + kr.at), e);
+                else lane_arrive(L::BAR_KE + kr.at);
+                kr.step();
+                return true;
+            };
+            // O += P V of the next V tile, key tile t; `fresh`: query tiles whose item has had none
+            auto step_pv = [&](const KeyTiles (&kw)[U], int t, uint32_t &fresh) -> bool {
+                if (!wait(L::BAR_VF + vr.at, vr.phase)) return false;
+                const uint64_t v0 = vd + (uint64_t)(vr.at * (L::TILE >> 4));
+                bool any = false;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (!kw[u].has(t)) continue;
+                    const int w = w0 + u;
+                    const bool first = fresh >> u & 1;
+                    // an item's first overwrites O, whose last rows have been read
+                    if (first && items[u] > 0 && !wait(L::BAR_OFREE + w, items[u] - 1)) return false;
+                    if (first) ++items[u];
+                    fresh &= ~(1u << u);
+                    if (!wait(L::BAR_PF + w, pc[u])) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < BKV / 16; ++k)
+                        mma_ts_bf16_e(tbase + w * L::TILE_COLS + L::O_COL, tbase + w * L::TILE_COLS + L::P_COL + 8 * k,
+                                      v0 + (uint64_t)(128 * k), idesc_pv, !first || k != 0, e);
+                    mma_commit_e(bar(L::BAR_PV + w), e);
+                    ++pc[u];
+                    any = true;
+                }
+                if (any) mma_commit_e(bar(L::BAR_VE + vr.at), e);
+                else lane_arrive(L::BAR_VE + vr.at);
+                vr.step();
+                return true;
+            };
+            KeyTiles all = {0, 0, 0}, kw[U];
+            // every S of the item is issued: its Q may be overwritten behind them
+            auto q_read = [&]() {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (kw[u].end > 0) mma_commit_e(bar(L::BAR_QE + (L::NQ == 2 ? NT * ((qn[u] - 1) & 1) : 0) + w0 + u), e);
+            };
+            // takes item number it: waits for its Q, issues its first S
+            auto begin = [&](int it) -> bool {
+                Item r;
+                if (!read_record(it, r)) return false;
+                all = {0, 0, 0};
+#pragma unroll
+                for (int u = 0; u < U; ++u) kw[u] = {0, 0, 0};
+                if (r.len == 0) return true;
+                all = tiles_of(r);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int w = w0 + u;
+                    if (w < NT) kw[u] = tiles_of_w(r, w);
+                    if (kw[u].end > 0) {
+                        if (!wait(L::BAR_Q + (L::NQ == 2 ? NT * (qn[u] & 1) : 0) + w, L::NQ == 2 ? qn[u] >> 1 : qn[u])) return false;
+                        ++qn[u];
+                    }
+                }
+                if (!step_s(kw, all.tile(0))) return false;
+                if (all.count() == 1) q_read();
+                return true;
+            };
+            ok = begin(0);
+            for (int it = 0; ok && all.end > 0; ++it) {
+                const KeyTiles now = all;
+                KeyTiles mine[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) mine[u] = kw[u];
+                const int n = now.count();
+                uint32_t fresh = ~0u;
+                for (int j = 0; j < n && ok; ++j) {
+                    // S of the next key tile, or the next item's first, then this one's PV
+                    if (j + 1 == n) {
+                        ok = begin(it + 1);
+                    } else {
+                        ok = step_s(mine, now.tile(j + 1));
+                        if (j + 2 == n) q_read();
+                    }
+                    ok = ok && step_pv(mine, now.tile(j), fresh);
                 }
             }
-            // pass 2: P = 2^(s cs + cb - m) as bf16 and its row sum over the f32 values
-            const float nm = cb - (m_used == -INFINITY ? 0.f : m_used);
-            const uint64_t c2 = f2_pack(cs, cs), nm2 = f2_pack(nm, nm);
-            uint64_t r4[4];
+            // nothing of ours may still be running when TMEM is given back
+            mma_commit_e(bar(L::BAR_FIN + warp - L::MMA_WARP), e);
+            mbar_wait(bar(L::BAR_FIN + warp - L::MMA_WARP), 0, 20000000ull);
+        } else if (BIAS) {
+            // -------------------------------- the heads' biases, ahead of their items
+            int head = -1, built = 0;
+            for (int it = 0; ok; ++it) {
+                Item r;
+                if (!(ok = read_record(it, r)) || r.len == 0) break;
+                if (r.h == head) continue;
+                head = r.h;
+                const int buf = p.nbuf == 2 ? built & 1 : 0, use = p.nbuf == 2 ? built >> 1 : built;
+                if (!(ok = wait(L::BAR_BE + buf, use ^ 1))) break;
+                for (int b = lane; b < nb; b += 32) {
+                    // log2 units; a finite bias stays finite (the type's lowest value still masks softly)
+                    const float v = p.table[(long long)b * p.ldt + head], v2 = v * 1.4426950408889634f;
+                    tab[b] = fabsf(v) <= FLT_MAX ? fminf(fmaxf(v2, -FLT_MAX), FLT_MAX) : v;
+                }
+                __syncwarp();
+                float *spread = spread_of(buf);
+#pragma unroll 4
+                for (int d = lane - width; d <= width; d += 32)
+                    spread[d] = bias_of(p, tab, d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::BAR_BF + buf));
+                ++built;
+            }
+        }
+    } else {
+        // ---------------------------------------- softmax, one query per thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::SOFTMAX_REGS));
+        const int w = warp >> 2;                         // query tile
+        const int wq = warp & 3;                         // TMEM lane quadrant: rows 32 wq ..
+        const uint32_t scol = tbase + ((uint32_t)(32 * wq) << 16) + w * L::TILE_COLS;
+        const float c = p.scale_log2;
+        uint32_t done = 0;                               // key tiles of this query tile, of all items
+        uint32_t vbase = 0;                              // key tiles of the CTA's items before this one
+        int head = -1, built = 0;                        // as in the bias warp
+        const float *bias = nullptr;                     // bias[d]: distance d, -(reach + PAD) .. reach + PAD
+        for (int it = 0; ok; ++it) {
+            if (!(ok = wait(L::BAR_REC + (it & 3), it >> 2))) break;
+            Item r = get_record(it);                     // held until the item's end
+            if (r.len == 0) break;
+            const int len = r.len;
+            if constexpr (BIAS) {
+                if (r.h != head) {
+                    // let go of the last head's bias, take this one's
+                    if (head >= 0 && lane == 0) mbar_arrive(bar(L::BAR_BE + (p.nbuf == 2 ? (built - 1) & 1 : 0)));
+                    head = r.h;
+                    const int buf = p.nbuf == 2 ? built & 1 : 0;
+                    if (!(ok = wait(L::BAR_BF + buf, p.nbuf == 2 ? built >> 1 : built))) break;
+                    bias = spread_of(buf);
+                    ++built;
+                }
+            }
+            const uint32_t vlast = vbase + tiles_of(r).count() - 1;   // the V tile of the item's last key tile
+            vbase = vlast + 1;
+            const int r0 = r.q0 + w * BQ + 32 * wq;      // the warp's first row
+            if (r.q0 + w * BQ >= len) {                  // the item has no rows of this query tile
+                let_record(it);
+                continue;
+            }
+            const int qi = r0 + lane;
+            const KeyTiles mine = tiles_of_w(r, w);
+            float m_used = -INFINITY;
+            uint64_t r4[4];                              // partial row sums
 #pragma unroll
             for (int i = 0; i < 4; ++i) r4[i] = f2_pack(0.f, 0.f);
+            // Tiles whose first key is in [whole_from, whole_to], or which end within
+            // the sinks, are seen whole by every row of the warp.  Near tiles begin
+            // in (near_from, near_to); the others have one bias for all pairs.
+            const int whole_from = (r0 + 31 < len - 1 ? r0 + 31 : len - 1) - p.left;
+            const int whole_to = (r0 + p.right + 1 < len ? r0 + p.right + 1 : len) - BKV;
+            const int near_from = r0 - (BKV - 1) - p.reach, near_to = r0 + 31 + p.reach;
+            float far_before = 0.f, far_behind = 0.f;
+            if constexpr (BIAS) {
+                far_before = bias[-p.reach];
+                far_behind = bias[p.reach];
+            }
+            // what the tile that begins at key kv0 needs: its mask, its bias
+            bool whole, add, each;
+            float cb;
+            auto look = [&](int kv0) {
+                whole = kv0 <= whole_to && (kv0 >= whole_from || kv0 + BKV <= p.sinks);
+                add = false;
+                each = false;
+                cb = 0.f;
+                if constexpr (BIAS) {
+                    each = kv0 > near_from && kv0 < near_to;
+                    cb = kv0 <= near_from ? far_before : far_behind;
+                    // so large that it takes the scores' own digits, as it does in a near tile
+                    add = each || !(fabsf(cb) <= 8192.f);
+                }
+            };
+            int t = mine.sink > 0 ? 0 : mine.first;
+            look(t * BKV);
+            bool begun = false, s_there = false, more = true;
+            while (more) {
+                if (!(ok = settle(s_there, L::BAR_SF + w, done))) break;
+                tc_fence_after();
+                const int kv0 = t * BKV;
+                // the S row once into registers for all passes
+                uint32_t v[64];
+                tmem_ld64(scol, v);
+                tmem_wait_ld();
+                // the tensor core may compute the next S
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::BAR_SFREE + w));
+                // scores in log2 units are s * cs + cb
+                float cs = c;
+                if constexpr (BIAS) {
+                    if (add) {
+                        const uint64_t c2 = f2_pack(c, c);
+                        if (each) add_bias<false>(v, c2, bias + (kv0 - qi), 0.f);
+                        else add_bias<true>(v, c2, nullptr, cb);
+                        cs = 1.f;
+                        cb = 0.f;
+                    }
+                }
+                if (!whole) {
+                    const int hi = (qi + p.right < len ? qi + p.right + 1 : len) - kv0;   // keys below it are not too far
+                    const int lo = qi - p.left - kv0, sk = p.sinks - kv0;
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const uint32_t (&v)[64] = hh ? v1 : v0;
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t see =
+                            bits_below(hi - 32 * x) & (~bits_below(lo - 32 * x) | bits_below(sk - 32 * x));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see >> e & 1)) v[32 * x + e] = 0xFF800000u;   // -inf
+                    }
+                }
+                // pass 1: the row maximum, eight partial ones
+                float m8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m8[i] = fmaxf(__uint_as_float(v[i]), __uint_as_float(v[8 + i]));
+#pragma unroll
+                for (int i = 16; i < 64; i += 2)
+                    m8[(i >> 1) & 7] = fmax3(m8[(i >> 1) & 7], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                const float mx = fmaf(fmaxf(fmax3(fmax3(m8[0], m8[1], m8[2]), m8[3], m8[4]), fmax3(m8[5], m8[6], m8[7])), cs, cb);
+                // the reference moves when a row grew by more than 2^8
+                const bool resc = mx > m_used + 8.f;
+                if (__any_sync(0xFFFFFFFFu, resc)) {
+                    const float alpha = resc ? hw_exp2(m_used - mx) : 1.f;
+                    if (resc) m_used = mx;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r4[i] = f2_mul(r4[i], f2_pack(alpha, alpha));
+                    if (begun) {
+                        // O is whole once the PV before is done
+                        if (!(ok = wait(L::BAR_PV + w, done - 1))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int cc = 0; cc < HD / 16; ++cc) {   // (few columns at once: S holds the registers)
+                            uint32_t o[16];
+                            tmem_ld16(scol + L::O_COL + 16 * cc, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st16(scol + L::O_COL + 16 * cc, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                if (kv0 + BKV > len) {
+                    // the last tile: V's rows behind the sequence become zeros, each
+                    // warp its share of them (a row is 128 bytes of each box)
+                    const uint32_t slot = vlast % R;
+                    if (!(ok = wait(L::BAR_VF + slot, vlast / R))) break;
+                    for (int x = len - kv0 + 4 * wq + (lane >> 3); x < BKV; x += 16)
+#pragma unroll
+                        for (int cc = 0; cc < L::NB; ++cc)
+                            *reinterpret_cast<uint4 *>(smem + L::V_OFF + slot * L::TILE + cc * L::BOX + x * 128 + (lane & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                }
+                // pass 2: P = 2^(s cs + cb - m) as bf16 and its row sum over the f32
+                // values.  What the next tile needs is worked out beside it.
+                const float nm = cb - (m_used == -INFINITY ? 0.f : m_used);
+                const uint64_t c2 = f2_pack(cs, cs), nm2 = f2_pack(nm, nm);
+                // P is free once its last PV is done
+                const bool p_free = begun ? test(L::BAR_PV + w, done - 1) : true;
+                t = t + 1 == mine.sink ? mine.first : t + 1;
+                more = t < mine.end;
+                look(t * BKV);
                 uint32_t pk[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
@@ -578,63 +829,73 @@ __global__ void __launch_bounds__(SLayout<HD, TL>::NTHREADS, TL == 1 ? 2 : 1)
                     r4[e & 3] = f2_add(r4[e & 3], f2_pack(p0, p1));
                     pk[e] = pack_bf16x2(p0, p1);
                 }
-                tmem_st32(pcol + 32 * hh, pk);
+                if (begun) {
+                    if (!(ok = settle(p_free, L::BAR_PV + w, done - 1))) break;
+                    tc_fence_after();
+                }
+                tmem_st32(scol + L::P_COL, pk);
+                s_there = test(L::BAR_SF + w, done + 1);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::BAR_PF + w));
+                begun = true;
+                ++done;
             }
+            if (!ok) break;
+            // ---- epilogue: O / l, one row per thread (0 where nothing is visible)
             float r8[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) f2_unpack(r4[i], r8[2 * i], r8[2 * i + 1]);
-            l += ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
-            if (kv0 + BKV > len) {
-                // the last tile: V's rows behind the sequence become zeros, each
-                // warp its share of them (a row is 128 bytes of each box)
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_vf + 8 * (j & 1), (j >> 1) & 1));
-                if (!ok) break;
-                for (int r = len - kv0 + 4 * wq + (lane >> 3); r < BKV; r += 16)
-#pragma unroll
-                    for (int cc = 0; cc < L::NB; ++cc)
-                        *reinterpret_cast<uint4 *>(smem + L::V_OFF + (j & 1) * L::TILE + cc * 16384 + r * 128 +
-                                                   (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                fence_async_smem();
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_pf + 8 * w);
-            ++jj;
-        }
-        // ---- epilogue: O / l, one row per thread (0 where nothing is visible)
-        if (ok && jj > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar_pv + 8 * w, (jj - 1) & 1));
-        if (ok) {
-            tc_fence_after();
+            const float l = ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
             const float inv = 1.f / l;
             float finite = l;                            // NaN once a value of the row is not finite
-            __nv_bfloat16 *orow = p.out + (long long)(off + (qi < len ? qi : 0)) * p.ldo + h * HD;
+            r = get_record(it);
+            let_record(it);
+            // rows go out through shared memory, so that a store of the warp writes 8
+            // pieces of 64 bytes instead of 32 of 16
+            uint4 *stage = reinterpret_cast<uint4 *>(smem + L::STG_OFF + warp * L::STG_WARP);
+            const int orow = lane >> 2, ochunk = lane & 3;   // what this lane stores: rows orow + 8 i
+            __nv_bfloat16 *out = p.out + (long long)(r.off + r0 + orow) * p.ldo + r.h * HD + 8 * ochunk;
+            if (!(ok = wait(L::BAR_PV + w, done - 1))) break;
+            tc_fence_after();
 #pragma unroll
             for (int cc = 0; cc < HD / 32; ++cc) {
-                uint32_t v[32];
-                tmem_ld32(ocol + 32 * cc, v);
+                uint32_t o[32];
+                tmem_ld32(scol + L::O_COL + 32 * cc, o);
                 tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) finite = fmaf(__uint_as_float(v[e]), 0.f, finite);
-                if (qi < len) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint4 u;
-                        u.x = pack_bf16x2(__uint_as_float(v[8 * e + 0]) * inv, __uint_as_float(v[8 * e + 1]) * inv);
-                        u.y = pack_bf16x2(__uint_as_float(v[8 * e + 2]) * inv, __uint_as_float(v[8 * e + 3]) * inv);
-                        u.z = pack_bf16x2(__uint_as_float(v[8 * e + 4]) * inv, __uint_as_float(v[8 * e + 5]) * inv);
-                        u.w = pack_bf16x2(__uint_as_float(v[8 * e + 6]) * inv, __uint_as_float(v[8 * e + 7]) * inv);
-                        *reinterpret_cast<uint4 *>(orow + 32 * cc + 8 * e) = u;
-                    }
+                if (cc == HD / 32 - 1) {
+                    // O is in registers: the next item's first PV may overwrite it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::BAR_OFREE + w));
                 }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) finite = fmaf(__uint_as_float(o[e]), 0.f, finite);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint4 u;
+                    u.x = pack_bf16x2(__uint_as_float(o[8 * e + 0]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
+                    u.y = pack_bf16x2(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
+                    u.z = pack_bf16x2(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
+                    u.w = pack_bf16x2(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
+                    stage[4 * lane + (e ^ (lane >> 1 & 3))] = u;   // no bank twice in eight lanes
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = orow + 8 * i;
+                    const uint4 u = stage[4 * x + (ochunk ^ (x >> 1 & 3))];
+                    if (r0 + x < len) *reinterpret_cast<uint4 *>(out + (long long)(8 * i) * p.ldo + 32 * cc) = u;
+                }
+                __syncwarp();
             }
             // rows whose sum is 0 or not finite, or that hold a value that is not
             uint32_t mend = __ballot_sync(0xFFFFFFFFu, qi < len && !(finite > 0.f && finite <= FLT_MAX));
-            __syncwarp();
             while (mend) {
-                const int r = __ffs(mend) - 1;
+                const int x = __ffs(mend) - 1;
                 mend &= mend - 1;
-                mend_row<HD, BIAS>(p, bias, off, len, h, r0 + r);
+                mend_row<HD, BIAS>(p, bias, r.off, len, r.h, r0 + x);
             }
         }
     }
@@ -643,29 +904,34 @@ __global__ void __launch_bounds__(SLayout<HD, TL>::NTHREADS, TL == 1 ? 2 : 1)
     __syncthreads();
     if (warp == L::MMA_WARP) {
         tc_fence_after();
-        tmem_dealloc(tbase, L::COLS);
+        tmem_dealloc(tbase, 512);
     }
 }
 
-template <int HD, int TL, bool BIAS>
-te_status launch(const SpanParams &p, cudaStream_t stream) {
-    using L = SLayout<HD, TL>;
-    constexpr int most = L::TAB_OFF + 1024 +
-                         (BIAS ? 4 * (TE_RELPOS_MAX_BUCKETS + 2 * (TE_RELPOS_MAX_DISTANCE + PAD) + 1) : 0);
-    const int nb = p.two_sided ? 2 * p.side : p.side;
-    const int smem = L::TAB_OFF + 1024 + (BIAS ? 4 * (nb + 2 * (p.reach + PAD) + 1) : 0);
+template <int HD, bool BIAS>
+te_status launch(SpanParams &p, cudaStream_t stream) {
+    using L = SLayout<HD>;
+    constexpr int most = BIAS ? 227 * 1024 : L::TAB_OFF + 1024;
+    int smem = L::TAB_OFF + 1024;
+    if (BIAS) {
+        // two spread biases, the next head's beside this one's, where they fit
+        const int nb = p.two_sided ? 2 * p.side : p.side, spread = 4 * (2 * (p.reach + PAD) + 1);
+        smem += 4 * nb + spread;
+        p.nbuf = smem + spread <= most ? 2 : 1;
+        if (p.nbuf == 2) smem += spread;
+    }
     static std::atomic<bool> ready[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cuda_fail(e, "attn: device");
     if (!ready[dev]) {
-        e = cudaFuncSetAttribute(attn_span_kernel<HD, TL, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        e = cudaFuncSetAttribute(attn_span_kernel<HD, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return cuda_fail(e, "attn: set shared memory size");
         ready[dev] = true;
     }
-    const int64_t slots = p.nwork ? p.nwork : (int64_t)p.total / (TL * BQ) + p.nseq;
+    const int64_t slots = p.nwork ? p.nwork : (int64_t)p.total / (L::NT * BQ) + p.nseq;
     if (slots * p.nq > 2147483647) return fail(TE_ESHAPE, "attn: too many query blocks and heads");
-    e = launch_close(attn_span_kernel<HD, TL, BIAS>, dim3((unsigned)(slots * p.nq)), L::NTHREADS, smem, stream, 1, p);
+    e = launch_close(attn_span_kernel<HD, BIAS>, dim3((unsigned)(slots * p.nq)), L::NTHREADS, smem, stream, 1, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "attn launch");
 }
 
@@ -725,7 +991,7 @@ int build_work(const int32_t *cu, int32_t nseq, const SpanParams &p, int qb, uin
         n += (cu[s + 1] - cu[s] + qb - 1) / qb;
         if (n > MAX_WORK) return 0;
     }
-    uint64_t key[MAX_WORK];   // (most - cost) << 32 | place in packed order: a stable order by cost
+    uint64_t key[MAX_WORK];   // (most - keys) << 20 | place in packed order: a stable order by keys
     uint32_t at[MAX_WORK];
     int k = 0;
     for (int32_t s = 0; s < nseq; ++s) {
@@ -734,8 +1000,7 @@ int build_work(const int32_t *cu, int32_t nseq, const SpanParams &p, int qb, uin
             const int64_t r0 = (int64_t)b * qb, r1 = std::min<int64_t>(r0 + qb, len) - 1;
             const int64_t lo = std::max<int64_t>(0, r0 - p.left), hi = std::min<int64_t>(len, r1 + p.right + 1);
             const int64_t keys = hi - lo + std::min<int64_t>(p.sinks, lo);
-            const uint64_t cost = (uint64_t)(keys * std::min<int64_t>(r1 - r0 + 1, BQ));   // < 2^38
-            key[k] = (((1ull << 40) - cost) << 20) | (uint64_t)k;
+            key[k] = (((1ull << 40) - (uint64_t)keys) << 20) | (uint64_t)k;
             at[k] = ((uint32_t)s << 16) | (uint32_t)b;
         }
     }
@@ -781,7 +1046,7 @@ te_status span_fwd(const char *name, const void *qkv, int64_t ld, int32_t q_off,
     SpanParams p;
     memset(&p, 0, sizeof(p));
     st = make_map_2d(&p.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, qkv, (uint64_t)ld, (uint64_t)total, (uint64_t)ld * 2,
-                     64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+                     64, BKV, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != TE_OK) return st;
     p.out = reinterpret_cast<__nv_bfloat16 *>(out);
     p.qkv = reinterpret_cast<const __nv_bfloat16 *>(qkv);
@@ -811,9 +1076,7 @@ te_status span_fwd(const char *name, const void *qkv, int64_t ld, int32_t q_off,
         p.grow = plan->grow;
         for (int b = 0; b < p.side; ++b) p.first[b] = (uint16_t)plan->first[b];
     }
-    // hd = 64: one 128-query tile a CTA, two CTAs an SM; hd = 128: two tiles a CTA
-    const int tl = hd == 64 ? 1 : 2;
-    p.nwork = build_work(cu_host, nseq, p, tl * BQ, p.work);
+    p.nwork = build_work(cu_host, nseq, p, (hd == 64 ? SLayout<64>::NT : SLayout<128>::NT) * BQ, p.work);
     // heads per group: all when every head's K and V fit in KV_ALL_BYTES
     // together, else the kv heads whose K and V make about KV_GROUP_BYTES
     const int64_t kv_head = (int64_t)total * hd * 4;
@@ -821,8 +1084,8 @@ te_status span_fwd(const char *name, const void *qkv, int64_t ld, int32_t q_off,
     if (kv_head * nkv > KV_ALL_BYTES) hg = std::min<int64_t>(nq, std::max<int64_t>(1, KV_GROUP_BYTES / kv_head) * p.group);
     p.hgroup = (int)hg;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (hd == 64) return plan ? launch<64, 1, true>(p, s) : launch<64, 1, false>(p, s);
-    return plan ? launch<128, 2, true>(p, s) : launch<128, 2, false>(p, s);
+    if (hd == 64) return plan ? launch<64, true>(p, s) : launch<64, false>(p, s);
+    return plan ? launch<128, true>(p, s) : launch<128, false>(p, s);
 }
 
 }  // namespace
