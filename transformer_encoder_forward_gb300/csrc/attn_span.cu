@@ -69,7 +69,6 @@ struct SpanParams {
     const float *table;        // [buckets, ldt]
     long long ldt;
     int side, exact, reach, two_sided;   // buckets of a side, those of one distance each; clipped reach
-    int nbuf;                  // spread biases in shared memory
     float grow;                // logarithmic buckets per unit of log2(distance / exact)
     uint16_t first[TE_RELPOS_MAX_BUCKETS];   // smallest distance of each bucket of a side
 };
@@ -80,16 +79,16 @@ struct SLayout {
     static constexpr int NB = HD / 64;              // 64-column boxes per tile row
     static constexpr int NT = HD == 64 ? 3 : 2;     // query tiles
     static constexpr int NQ = HD == 64 ? 2 : 1;     // Q buffers: the next item's Q beside this one's
-    static constexpr int R = HD == 64 ? 4 : 3;      // K and V tiles in flight
+    static constexpr int R = HD == 64 ? 4 : 3;      // pairs of a K and a V tile in flight
     static constexpr int QTILE = BQ * HD * 2, TILE = BKV * HD * 2;
     static constexpr int QBOX = BQ * 128, BOX = BKV * 128;   // 64 columns of them
     static constexpr int Q_OFF = 0;                 // Q[NQ][NT]
-    static constexpr int K_OFF = NQ * NT * QTILE;   // K[R]
-    static constexpr int V_OFF = K_OFF + R * TILE;  // V[R]
-    static constexpr int STG_OFF = V_OFF + R * TILE;         // a softmax warp's 32 rows of 32 outputs
+    static constexpr int K_OFF = NQ * NT * QTILE;   // [R] K, V
+    static constexpr int STG_OFF = K_OFF + R * 2 * TILE;     // a softmax warp's 32 rows of 32 outputs
     static constexpr int STG_WARP = 32 * 64;
-    // warps: softmax (4 a query tile), 2 that issue MMAs, TMA, bias
-    static constexpr int SOFTMAX_WARPS = 4 * NT, MMA_WARP = SOFTMAX_WARPS, TMA_WARP = MMA_WARP + 2;
+    // warps: softmax (4 a query tile), one a query tile that issues its MMAs, and in
+    // the same warpgroup one that schedules, loads and spreads the biases
+    static constexpr int SOFTMAX_WARPS = 4 * NT, MMA_WARP = SOFTMAX_WARPS, TMA_WARP = MMA_WARP + 3;
     static constexpr int NTHREADS = 32 * (SOFTMAX_WARPS + 4);
     // registers a thread at launch, and after the softmax warps took over what the others do not need
     static constexpr int LAUNCH_REGS = HD == 64 ? 128 : 168, SOFTMAX_REGS = HD == 64 ? 144 : 208, OTHER_REGS = HD == 64 ? 80 : 88;
@@ -98,11 +97,9 @@ struct SLayout {
     // barriers
     static constexpr int BAR_Q = 0;                      // [NQ][NT] Q loaded, per buffer and query tile
     static constexpr int BAR_QE = BAR_Q + NT * NQ;       // [NQ][NT] Q read by the item's last S
-    static constexpr int BAR_KF = BAR_QE + NT * NQ;      // [R] K loaded
-    static constexpr int BAR_KE = BAR_KF + R;            // [R] K read by both MMA warps
-    static constexpr int BAR_VF = BAR_KE + R;            // [R] V loaded
-    static constexpr int BAR_VE = BAR_VF + R;            // [R] V read by both
-    static constexpr int BAR_SF = BAR_VE + R;            // [NT] S ready
+    static constexpr int BAR_KV = BAR_QE + NT * NQ;      // [R] K and V loaded
+    static constexpr int BAR_KVE = BAR_KV + R;           // [R] K and V read by every query tile
+    static constexpr int BAR_SF = BAR_KVE + R;           // [NT] S ready
     static constexpr int BAR_SFREE = BAR_SF + NT;        // [NT] S is in registers
     static constexpr int BAR_PF = BAR_SFREE + NT;        // [NT] P written
     static constexpr int BAR_PV = BAR_PF + NT;           // [NT] its PV done
@@ -112,16 +109,16 @@ struct SLayout {
     static constexpr int BAR_CLC = BAR_RECE + 4;         // the next CTA's place taken over, or not
     static constexpr int BAR_BF = BAR_CLC + 1;           // [2] bias spread
     static constexpr int BAR_BE = BAR_BF + 2;            // [2] bias no longer read
-    static constexpr int BAR_FIN = BAR_BE + 2;           // [2] every MMA and commit of an MMA warp is done
-    static constexpr int NBAR = BAR_FIN + 2;
+    static constexpr int BAR_FIN = BAR_BE + 2;           // [NT] every MMA and commit of an MMA warp is done
+    static constexpr int NBAR = BAR_FIN + NT;
     static constexpr int REC_OFF = (BAR_OFF + 8 * NBAR + 15) / 16 * 16;   // 4 records of 16 bytes, the taken place
     static constexpr int SLOT_OFF = REC_OFF + 80;        // TMEM base
-    static constexpr int TAB_OFF = SLOT_OFF + 16;        // the head's table column, then the spread biases
+    static constexpr int TAB_OFF = SLOT_OFF + 16;        // a head's table column, then two spread biases
     // TMEM columns of a query tile: S (64 f32), P (64 bf16), O (HD f32)
     static constexpr int P_COL = 64, O_COL = 96, TILE_COLS = 96 + HD;
     static_assert(NT * TILE_COLS <= 512, "TMEM budget");
     // the widest bias: every distance to TE_RELPOS_MAX_DISTANCE to either side
-    static_assert(TAB_OFF + 4 * (TE_RELPOS_MAX_BUCKETS + 2 * (TE_RELPOS_MAX_DISTANCE + PAD) + 1) + 1024 <= 227 * 1024,
+    static_assert(TAB_OFF + 4 * (TE_RELPOS_MAX_BUCKETS + 2 * (2 * (TE_RELPOS_MAX_DISTANCE + PAD) + 1)) + 1024 <= 227 * 1024,
                   "shared memory per CTA");
 };
 
@@ -161,16 +158,55 @@ __device__ __forceinline__ float bias_of(const SpanParams &p, const float *col, 
     return col[p.two_sided && d > 0 ? b + p.side : b];
 }
 
-// Scores of 64 keys to log2 units with their bias: v = v c + b[e] (ONE: + one).
+// Arrives where `on` is set, without a branch.
+__device__ __forceinline__ void arrive_if(uint32_t bar, bool on) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"((uint32_t)on)
+                 : "memory");
+}
+
+// Scores of 32 keys to log2 units with their bias: v = v c + b[e] (ONE: + one).
 template <bool ONE>
-__device__ __forceinline__ void add_bias(uint32_t (&v)[64], uint64_t c2, const float *b, float one) {
+__device__ __forceinline__ void add_bias(uint32_t (&v)[32], uint64_t c2, const float *b, float one) {
 #pragma unroll
-    for (int e = 0; e < 64; e += 2) {
+    for (int e = 0; e < 32; e += 2) {
         const uint64_t b2 = ONE ? f2_pack(one, one) : f2_pack(b[e], b[e + 1]);
         float x, y;
         f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2, b2), x, y);
         v[e] = __float_as_uint(x);
         v[e + 1] = __float_as_uint(y);
+    }
+}
+
+// Waits for this thread's TMEM loads; the registers go through it, so that no use
+// of theirs can come before.
+__device__ __forceinline__ void wait_loaded(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+// Scores of 32 keys whose bit of `see` is 0 become -inf.
+__device__ __forceinline__ void hide(uint32_t (&v)[32], uint32_t see) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (!(see >> e & 1)) v[e] = 0xFF800000u;
+}
+
+// P = 2^(s cs + nm) of 32 keys as bf16, and its sums into r2.
+__device__ __forceinline__ void exp_pass(const uint32_t (&v)[32], uint64_t c2, uint64_t nm2, uint64_t (&r2)[2],
+                                         uint32_t (&pk)[16]) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        float a0, a1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), c2, nm2), a0, a1);
+        const float p0 = hw_exp2(a0), p1 = hw_exp2(a1);
+        r2[e & 1] = f2_add(r2[e & 1], f2_pack(p0, p1));
+        pk[e] = pack_bf16x2(p0, p1);
     }
 }
 
@@ -325,10 +361,8 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
         tma_prefetch_desc(&p.map);
         for (int i = 0; i < 2 * NT * L::NQ; ++i) mbar_init(bar(L::BAR_Q + i), 1);
         for (int i = 0; i < R; ++i) {
-            mbar_init(bar(L::BAR_KF + i), 1);
-            mbar_init(bar(L::BAR_KE + i), 2);
-            mbar_init(bar(L::BAR_VF + i), 1);
-            mbar_init(bar(L::BAR_VE + i), 2);
+            mbar_init(bar(L::BAR_KV + i), 1);
+            mbar_init(bar(L::BAR_KVE + i), NT);
         }
         for (int i = 0; i < NT; ++i) {
             mbar_init(bar(L::BAR_SF + i), 1);
@@ -336,15 +370,15 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             mbar_init(bar(L::BAR_PF + i), 4);
             mbar_init(bar(L::BAR_PV + i), 1);
             mbar_init(bar(L::BAR_OFREE + i), 4);
+            mbar_init(bar(L::BAR_FIN + i), 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(L::BAR_REC + i), 1);
-            mbar_init(bar(L::BAR_RECE + i), L::SOFTMAX_WARPS + 2 + (BIAS ? 1 : 0));
+            mbar_init(bar(L::BAR_RECE + i), L::SOFTMAX_WARPS + NT);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::BAR_BF + i), 1);
             mbar_init(bar(L::BAR_BE + i), L::SOFTMAX_WARPS);
-            mbar_init(bar(L::BAR_FIN + i), 1);
         }
         mbar_init(bar(L::BAR_CLC), 1);
         fence_mbar_init();
@@ -372,7 +406,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
     };
     auto let_record = [&](int it) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::BAR_RECE + (it & 3)));
+        arrive_if(bar(L::BAR_RECE + (it & 3)), lane == 0);
     };
     auto read_record = [&](int it, Item &r) {
         if (!wait(L::BAR_REC + (it & 3), it >> 2)) return false;
@@ -405,8 +439,9 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             const uint32_t e = elect_one();
             int next = *reinterpret_cast<volatile int *>(&g_span_err) == 0 ? (int)blockIdx.x : -1;
             next = __shfl_sync(0xFFFFFFFFu, next, 0);
-            Ring kr = {0, 0}, vr = {0, 0};
-            int kn = 0, vn = 0;                          // K and V tiles issued in all
+            Ring kv = {0, 0};
+            int kvn = 0;                                 // pairs of K and V issued in all
+            int head = -1, built = 0;                    // the head whose bias was spread last, biases spread
             int asked = 0;                               // places asked for
             uint32_t qn[NT];                             // Q loads of each query tile
 #pragma unroll
@@ -447,6 +482,26 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 }
                 __syncwarp();
             };
+            // Spreads the head's bias over the distances, in log2 units, ahead of its first item.
+            auto spread_bias = [&](int h) {
+                if (h == head) return;
+                head = h;
+                const int buf = built & 1;
+                if (!wait(L::BAR_BE + buf, (built >> 1) ^ 1)) { ok = false; return; }
+                for (int b = lane; b < nb; b += 32) {
+                    // a finite bias stays finite (the type's lowest value still masks softly)
+                    const float v = p.table[(long long)b * p.ldt + h], v2 = v * 1.4426950408889634f;
+                    tab[b] = fabsf(v) <= FLT_MAX ? fminf(fmaxf(v2, -FLT_MAX), FLT_MAX) : v;
+                }
+                __syncwarp();
+                float *spread = spread_of(buf);
+#pragma unroll 4
+                for (int d = lane - width; d <= width; d += 32)
+                    spread[d] = bias_of(p, tab, d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d));
+                __syncwarp();
+                arrive_if(bar(L::BAR_BF + buf), lane == 0);
+                ++built;
+            };
             Item r;
             publish(0, r);
             for (int it = 0; ok && r.len > 0; ++it) {
@@ -464,37 +519,28 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                         tma_load_2d_e(sb + L::Q_OFF + qb * L::QTILE + c * L::BOX, &p.map, bar(L::BAR_Q + qb),
                                       p.q_off + r.h * HD + 64 * (c >> 1), r.off + r.q0 + w * BQ + BKV * (c & 1), e);
                 }
-                auto load_k = [&](int j) -> bool {
-                    if (!wait(L::BAR_KE + kr.at, kr.phase ^ 1)) return false;
-                    mbar_arrive_expect_tx_e(bar(L::BAR_KF + kr.at), L::TILE, e);
-                    for (int c = 0; c < L::NB; ++c)
-                        tma_load_2d_e(sb + L::K_OFF + kr.at * L::TILE + c * L::BOX, &p.map, bar(L::BAR_KF + kr.at),
-                                      p.k_off + g * HD + 64 * c, r.off + tiles.tile(j) * BKV, e);
-                    kr.step();
-                    ++kn;
-                    return true;
-                };
-                auto load_v = [&](int j) -> bool {
-                    if (!wait(L::BAR_VE + vr.at, vr.phase ^ 1)) return false;
-                    mbar_arrive_expect_tx_e(bar(L::BAR_VF + vr.at), L::TILE, e);
-                    for (int c = 0; c < L::NB; ++c)
-                        tma_load_2d_e(sb + L::V_OFF + vr.at * L::TILE + c * L::BOX, &p.map, bar(L::BAR_VF + vr.at),
-                                      p.v_off + g * HD + 64 * c, r.off + tiles.tile(j) * BKV, e);
-                    vr.step();
-                    ++vn;
-                    return true;
-                };
-                // K runs one tile ahead of V: S(j + 1) comes before PV(j)
                 Item r2 = {0, 0, 0, 0};
-                if (ok) ok = load_k(0);
                 for (int j = 0; j < n && ok; ++j) {
-                    if (j + 1 < n && !(ok = load_k(j + 1))) break;
-                    if (!(ok = load_v(j))) break;
+                    if (!(ok = wait(L::BAR_KVE + kv.at, kv.phase ^ 1))) break;
+                    const uint32_t to = sb + L::K_OFF + kv.at * 2 * L::TILE, b = bar(L::BAR_KV + kv.at);
+                    const int row = r.off + tiles.tile(j) * BKV;
+                    mbar_arrive_expect_tx_e(b, 2 * L::TILE, e);
+#pragma unroll
+                    for (int c = 0; c < L::NB; ++c)
+                        tma_load_2d_e(to + c * L::BOX, &p.map, b, p.k_off + g * HD + 64 * c, row, e);
+#pragma unroll
+                    for (int c = 0; c < L::NB; ++c)
+                        tma_load_2d_e(to + L::TILE + c * L::BOX, &p.map, b, p.v_off + g * HD + 64 * c, row, e);
+                    kv.step();
+                    ++kvn;
                     if (j == 0) {
+                        if (BIAS && it == 0) spread_bias(r.h);
                         // the next item, well before this one ends
-                        next = answer();
+                        if (ok) next = answer();
                         if (ok) publish(it + 1, r2);
                     }
+                    // its bias once some tiles are on their way
+                    if (BIAS && ok && r2.len > 0 && (j == 2 || (j < 2 && j + 1 == n))) spread_bias(r2.h);
                 }
                 r = r2;
             }
@@ -507,162 +553,112 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                             const uint32_t u = qn[w] - 1 - x;
                             mbar_wait(bar(L::BAR_Q + (L::NQ == 2 ? NT * (u & 1) + w : w)), (L::NQ == 2 ? u >> 1 : u) & 1, 20000000ull);
                         }
-                for (int i = kn - R < 0 ? 0 : kn - R; i < kn; ++i) mbar_wait(bar(L::BAR_KF + i % R), (i / R) & 1, 20000000ull);
-                for (int i = vn - R < 0 ? 0 : vn - R; i < vn; ++i) mbar_wait(bar(L::BAR_VF + i % R), (i / R) & 1, 20000000ull);
+                for (int i = kvn - R < 0 ? 0 : kvn - R; i < kvn; ++i) mbar_wait(bar(L::BAR_KV + i % R), (i / R) & 1, 20000000ull);
                 if (asked) mbar_wait(bar(L::BAR_CLC), (asked - 1) & 1, 20000000ull);
             }
-        } else if (warp < L::TMA_WARP) {
-            // ------------- MMA issuer of query tiles w0 .. w0 + U - 1 (the second may not exist)
+        } else if (warp - L::MMA_WARP < NT) {
+            // ------------------------------------- MMA issuer of query tile w
             // (the whole warp in step, one elected lane issues)
-            constexpr int U = (NT + 1) / 2;
-            const int w0 = (warp - L::MMA_WARP) * U;
+            const int w = warp - L::MMA_WARP;
             const uint32_t e = elect_one();
             constexpr uint32_t idesc_s = idesc_bf16_f32(BQ, BKV);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(BQ, HD) | (1u << 16);   // B MN-major
             const uint64_t kd = smem_desc_sw128(sb + L::K_OFF);
-            const uint64_t vd = smem_desc_mn_sw128(sb + L::V_OFF, L::BOX);
+            const uint64_t vd = smem_desc_mn_sw128(sb + L::K_OFF + L::TILE, L::BOX);
             const uint64_t qd = smem_desc_sw128(sb + L::Q_OFF);
-            uint32_t sc[U], pc[U], items[U], qn[U];      // S and PV issued, items begun (as PV, as Q see them)
-#pragma unroll
-            for (int u = 0; u < U; ++u) sc[u] = pc[u] = items[u] = qn[u] = 0;
-            Ring kr = {0, 0}, vr = {0, 0};               // the K tile whose S, the V tile whose PV comes next
-            auto lane_arrive = [&](int b) {
-                asm volatile(
-                    "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar(b)),
-                    "r"(e)
-                    : "memory");
-            };
-            // S = Q K^T of the next K tile, key tile t, for the query tiles that see it
-            auto step_s = [&](const KeyTiles (&kw)[U], int t) -> bool {
-                if (!wait(L::BAR_KF + kr.at, kr.phase)) return false;
-                const uint64_t k0 = kd + (uint64_t)(kr.at * (L::TILE >> 4));
-                bool any = false;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (!kw[u].has(t)) continue;
-                    const int w = w0 + u;
-                    // the softmax has the last S in registers
-                    if (sc[u] > 0 && !wait(L::BAR_SFREE + w, sc[u] - 1)) return false;
+            const uint32_t stm = tbase + w * L::TILE_COLS;
+            uint32_t sc = 0, pc = 0;                     // S and PV issued
+            uint32_t items = 0, qn = 0;                  // items with rows, as PV and as Q see them
+            Ring sr = {0, 0}, pr = {0, 0};               // the K whose S, the V whose PV comes next
+            uint64_t q0 = qd;                            // this item's Q
+            // S = Q K^T of the next K tile (mine: this query tile sees it)
+            auto step_s = [&](bool mine) -> bool {
+                const bool kv_there = test(L::BAR_KV + sr.at, sr.phase);
+                // the softmax has the last S in registers (before the first there is nothing to wait for)
+                const bool s_free = mine ? test(L::BAR_SFREE + w, sc + 1) : true;
+                if (!__all_sync(0xFFFFFFFFu, kv_there && s_free) &&
+                    !(wait(L::BAR_KV + sr.at, sr.phase) && (!mine || wait(L::BAR_SFREE + w, sc + 1))))
+                    return false;
+                if (mine) {
                     tc_fence_after();
-                    const int qb = L::NQ == 2 ? NT * ((qn[u] - 1) & 1) + w : w;
-                    const uint64_t q0 = qd + (uint64_t)(qb * (L::QTILE >> 4));
+                    const uint64_t k0 = kd + (uint64_t)(sr.at * (2 * L::TILE >> 4));
 #pragma unroll
                     for (int k = 0; k < HD / 16; ++k)
-                        mma_ss_bf16_e(tbase + w * L::TILE_COLS, q0 + (((k >> 2) * L::QBOX + (k & 3) * 32) >> 4),
+                        mma_ss_bf16_e(stm, q0 + (((k >> 2) * L::QBOX + (k & 3) * 32) >> 4),
                                       k0 + (((k >> 2) * L::BOX + (k & 3) * 32) >> 4), idesc_s, k > 0, e);
                     mma_commit_e(bar(L::BAR_SF + w), e);
-                    ++sc[u];
-                    any = true;
+                    ++sc;
                 }
-                if (any) mma_commit_e(bar(L::BAR_KE + kr.at), e);
-                else lane_arrive(L::BAR_KE + kr.at);
-                kr.step();
+                sr.step();
                 return true;
             };
-            // O += P V of the next V tile, key tile t; `fresh`: query tiles whose item has had none
-            auto step_pv = [&](const KeyTiles (&kw)[U], int t, uint32_t &fresh) -> bool {
-                if (!wait(L::BAR_VF + vr.at, vr.phase)) return false;
-                const uint64_t v0 = vd + (uint64_t)(vr.at * (L::TILE >> 4));
-                bool any = false;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (!kw[u].has(t)) continue;
-                    const int w = w0 + u;
-                    const bool first = fresh >> u & 1;
+            // O += P V of the next V tile (its K's S was waited for, so it is there); more: not the item's first
+            auto step_pv = [&](bool mine, bool more) -> bool {
+                if (mine) {
+                    const bool p_there = test(L::BAR_PF + w, pc);
                     // an item's first overwrites O, whose last rows have been read
-                    if (first && items[u] > 0 && !wait(L::BAR_OFREE + w, items[u] - 1)) return false;
-                    if (first) ++items[u];
-                    fresh &= ~(1u << u);
-                    if (!wait(L::BAR_PF + w, pc[u])) return false;
+                    const bool o_free = more ? true : test(L::BAR_OFREE + w, items + 1);
+                    if (!__all_sync(0xFFFFFFFFu, p_there && o_free) &&
+                        !((more || wait(L::BAR_OFREE + w, items + 1)) && wait(L::BAR_PF + w, pc)))
+                        return false;
+                    if (!more) ++items;
                     tc_fence_after();
+                    const uint64_t v0 = vd + (uint64_t)(pr.at * (2 * L::TILE >> 4));
 #pragma unroll
                     for (int k = 0; k < BKV / 16; ++k)
-                        mma_ts_bf16_e(tbase + w * L::TILE_COLS + L::O_COL, tbase + w * L::TILE_COLS + L::P_COL + 8 * k,
-                                      v0 + (uint64_t)(128 * k), idesc_pv, !first || k != 0, e);
+                        mma_ts_bf16_e(stm + L::O_COL, stm + L::P_COL + 8 * k, v0 + (uint64_t)(128 * k), idesc_pv,
+                                      more || k != 0, e);
                     mma_commit_e(bar(L::BAR_PV + w), e);
-                    ++pc[u];
-                    any = true;
+                    ++pc;
+                    mma_commit_e(bar(L::BAR_KVE + pr.at), e);
+                } else {
+                    arrive_if(bar(L::BAR_KVE + pr.at), e != 0);
                 }
-                if (any) mma_commit_e(bar(L::BAR_VE + vr.at), e);
-                else lane_arrive(L::BAR_VE + vr.at);
-                vr.step();
+                pr.step();
                 return true;
             };
-            KeyTiles all = {0, 0, 0}, kw[U];
-            // every S of the item is issued: its Q may be overwritten behind them
-            auto q_read = [&]() {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (kw[u].end > 0) mma_commit_e(bar(L::BAR_QE + (L::NQ == 2 ? NT * ((qn[u] - 1) & 1) : 0) + w0 + u), e);
-            };
+            KeyTiles all = {0, 0, 0}, kw = {0, 0, 0};
+            int qbar = 0;                                // the Q buffer's barrier
             // takes item number it: waits for its Q, issues its first S
             auto begin = [&](int it) -> bool {
                 Item r;
                 if (!read_record(it, r)) return false;
-                all = {0, 0, 0};
-#pragma unroll
-                for (int u = 0; u < U; ++u) kw[u] = {0, 0, 0};
+                all = kw = {0, 0, 0};
                 if (r.len == 0) return true;
                 all = tiles_of(r);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int w = w0 + u;
-                    if (w < NT) kw[u] = tiles_of_w(r, w);
-                    if (kw[u].end > 0) {
-                        if (!wait(L::BAR_Q + (L::NQ == 2 ? NT * (qn[u] & 1) : 0) + w, L::NQ == 2 ? qn[u] >> 1 : qn[u])) return false;
-                        ++qn[u];
-                    }
+                kw = tiles_of_w(r, w);
+                if (kw.end > 0) {
+                    qbar = L::NQ == 2 ? NT * (qn & 1) + w : w;
+                    if (!wait(L::BAR_Q + qbar, L::NQ == 2 ? qn >> 1 : qn)) return false;
+                    q0 = qd + (uint64_t)(qbar * (L::QTILE >> 4));
+                    ++qn;
                 }
-                if (!step_s(kw, all.tile(0))) return false;
-                if (all.count() == 1) q_read();
-                return true;
+                return step_s(kw.has(all.tile(0)));
             };
             ok = begin(0);
             for (int it = 0; ok && all.end > 0; ++it) {
-                const KeyTiles now = all;
-                KeyTiles mine[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) mine[u] = kw[u];
+                const KeyTiles now = all, mine = kw;
                 const int n = now.count();
-                uint32_t fresh = ~0u;
+                bool more = false, see = mine.has(now.tile(0));
                 for (int j = 0; j < n && ok; ++j) {
                     // S of the next key tile, or the next item's first, then this one's PV
-                    if (j + 1 == n) {
-                        ok = begin(it + 1);
+                    bool see_next = false;
+                    if (j + 1 < n) {
+                        see_next = mine.has(now.tile(j + 1));
+                        ok = step_s(see_next);
                     } else {
-                        ok = step_s(mine, now.tile(j + 1));
-                        if (j + 2 == n) q_read();
+                        // every S of the item is issued: its Q may be overwritten behind them
+                        if (mine.end > 0) mma_commit_e(bar(L::BAR_QE + qbar), e);
+                        ok = begin(it + 1);
                     }
-                    ok = ok && step_pv(mine, now.tile(j), fresh);
+                    ok = ok && step_pv(see, more);
+                    more = more || see;
+                    see = see_next;
                 }
             }
             // nothing of ours may still be running when TMEM is given back
-            mma_commit_e(bar(L::BAR_FIN + warp - L::MMA_WARP), e);
-            mbar_wait(bar(L::BAR_FIN + warp - L::MMA_WARP), 0, 20000000ull);
-        } else if (BIAS) {
-            // -------------------------------- the heads' biases, ahead of their items
-            int head = -1, built = 0;
-            for (int it = 0; ok; ++it) {
-                Item r;
-                if (!(ok = read_record(it, r)) || r.len == 0) break;
-                if (r.h == head) continue;
-                head = r.h;
-                const int buf = p.nbuf == 2 ? built & 1 : 0, use = p.nbuf == 2 ? built >> 1 : built;
-                if (!(ok = wait(L::BAR_BE + buf, use ^ 1))) break;
-                for (int b = lane; b < nb; b += 32) {
-                    // log2 units; a finite bias stays finite (the type's lowest value still masks softly)
-                    const float v = p.table[(long long)b * p.ldt + head], v2 = v * 1.4426950408889634f;
-                    tab[b] = fabsf(v) <= FLT_MAX ? fminf(fmaxf(v2, -FLT_MAX), FLT_MAX) : v;
-                }
-                __syncwarp();
-                float *spread = spread_of(buf);
-#pragma unroll 4
-                for (int d = lane - width; d <= width; d += 32)
-                    spread[d] = bias_of(p, tab, d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::BAR_BF + buf));
-                ++built;
-            }
+            mma_commit_e(bar(L::BAR_FIN + w), e);
+            mbar_wait(bar(L::BAR_FIN + w), 0, 20000000ull);
         }
     } else {
         // ---------------------------------------- softmax, one query per thread
@@ -673,7 +669,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
         const float c = p.scale_log2;
         uint32_t done = 0;                               // key tiles of this query tile, of all items
         uint32_t vbase = 0;                              // key tiles of the CTA's items before this one
-        int head = -1, built = 0;                        // as in the bias warp
+        int head = -1, built = 0;                        // as where they are spread
         const float *bias = nullptr;                     // bias[d]: distance d, -(reach + PAD) .. reach + PAD
         for (int it = 0; ok; ++it) {
             if (!(ok = wait(L::BAR_REC + (it & 3), it >> 2))) break;
@@ -683,11 +679,10 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             if constexpr (BIAS) {
                 if (r.h != head) {
                     // let go of the last head's bias, take this one's
-                    if (head >= 0 && lane == 0) mbar_arrive(bar(L::BAR_BE + (p.nbuf == 2 ? (built - 1) & 1 : 0)));
+                    if (head >= 0 && lane == 0) mbar_arrive(bar(L::BAR_BE + ((built - 1) & 1)));
                     head = r.h;
-                    const int buf = p.nbuf == 2 ? built & 1 : 0;
-                    if (!(ok = wait(L::BAR_BF + buf, p.nbuf == 2 ? built >> 1 : built))) break;
-                    bias = spread_of(buf);
+                    if (!(ok = wait(L::BAR_BF + (built & 1), built >> 1))) break;
+                    bias = spread_of(built & 1);
                     ++built;
                 }
             }
@@ -700,10 +695,8 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             }
             const int qi = r0 + lane;
             const KeyTiles mine = tiles_of_w(r, w);
-            float m_used = -INFINITY;
-            uint64_t r4[4];                              // partial row sums
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r4[i] = f2_pack(0.f, 0.f);
+            float m_used = -INFINITY, nm0 = 0.f;         // nm0 = -m_used, 0 while there is none
+            uint64_t r2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};   // partial row sums
             // Tiles whose first key is in [whole_from, whole_to], or which end within
             // the sinks, are seen whole by every row of the warp.  Near tiles begin
             // in (near_from, near_to); the others have one bias for all pairs.
@@ -715,139 +708,155 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 far_before = bias[-p.reach];
                 far_behind = bias[p.reach];
             }
-            // what the tile that begins at key kv0 needs: its mask, its bias
-            bool whole, add, each;
-            float cb;
+            // what the tile that begins at key kv0 needs: a mask or a bias of each pair
+            // (special), else one bias cb for all its pairs
+            bool special;
+            float cb = 0.f;
             auto look = [&](int kv0) {
-                whole = kv0 <= whole_to && (kv0 >= whole_from || kv0 + BKV <= p.sinks);
-                add = false;
-                each = false;
-                cb = 0.f;
+                special = kv0 > whole_to || (kv0 < whole_from && kv0 + BKV > p.sinks);
                 if constexpr (BIAS) {
-                    each = kv0 > near_from && kv0 < near_to;
                     cb = kv0 <= near_from ? far_before : far_behind;
-                    // so large that it takes the scores' own digits, as it does in a near tile
-                    add = each || !(fabsf(cb) <= 8192.f);
+                    // a bias so large that it takes the scores' own digits is added to each, as in a near tile
+                    special = special || (kv0 > near_from && kv0 < near_to) || !(fabsf(cb) <= 8192.f);
                 }
             };
             int t = mine.sink > 0 ? 0 : mine.first;
             look(t * BKV);
-            bool begun = false, s_there = false, more = true;
+            bool begun = false, more = true;
+            // the S row of a tile in two halves of 32 keys
+            uint32_t va[32], vb[32];
+            if (!(ok = wait(L::BAR_SF + w, done))) break;
+            tc_fence_after();
+            tmem_ld32(scol, va);
+            tmem_ld32(scol + 32, vb);
             while (more) {
-                if (!(ok = settle(s_there, L::BAR_SF + w, done))) break;
-                tc_fence_after();
-                const int kv0 = t * BKV;
-                // the S row once into registers for all passes
-                uint32_t v[64];
-                tmem_ld64(scol, v);
-                tmem_wait_ld();
+                wait_loaded(va);
+                wait_loaded(vb);
                 // the tensor core may compute the next S
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::BAR_SFREE + w));
+                arrive_if(bar(L::BAR_SFREE + w), lane == 0);
                 // scores in log2 units are s * cs + cb
                 float cs = c;
-                if constexpr (BIAS) {
-                    if (add) {
-                        const uint64_t c2 = f2_pack(c, c);
-                        if (each) add_bias<false>(v, c2, bias + (kv0 - qi), 0.f);
-                        else add_bias<true>(v, c2, nullptr, cb);
-                        cs = 1.f;
-                        cb = 0.f;
+                if (special) {
+                    const int kv0 = t * BKV;
+                    if constexpr (BIAS) {
+                        const bool each = kv0 > near_from && kv0 < near_to;
+                        if (each || !(fabsf(cb) <= 8192.f)) {
+                            const uint64_t c2 = f2_pack(c, c);
+                            if (each) {
+                                add_bias<false>(va, c2, bias + (kv0 - qi), 0.f);
+                                add_bias<false>(vb, c2, bias + (kv0 - qi) + 32, 0.f);
+                            } else {
+                                add_bias<true>(va, c2, nullptr, cb);
+                                add_bias<true>(vb, c2, nullptr, cb);
+                            }
+                            cs = 1.f;
+                            cb = 0.f;
+                        }
+                    }
+                    if (kv0 > whole_to || (kv0 < whole_from && kv0 + BKV > p.sinks)) {
+                        const int hi = (qi + p.right < len ? qi + p.right + 1 : len) - kv0;   // keys below it are not too far
+                        const int lo = qi - p.left - kv0, sk = p.sinks - kv0;
+                        hide(va, bits_below(hi) & (~bits_below(lo) | bits_below(sk)));
+                        hide(vb, bits_below(hi - 32) & (~bits_below(lo - 32) | bits_below(sk - 32)));
+                    }
+                    if (kv0 + BKV > len) {
+                        // the last tile: V's rows behind the sequence become zeros, each
+                        // warp its share of them (a row is 128 bytes of each box)
+                        const uint32_t slot = vlast % R;
+                        if (!(ok = wait(L::BAR_KV + slot, vlast / R))) break;
+                        for (int x = len - kv0 + 4 * wq + (lane >> 3); x < BKV; x += 16)
+#pragma unroll
+                            for (int cc = 0; cc < L::NB; ++cc)
+                                *reinterpret_cast<uint4 *>(smem + L::K_OFF + (2 * slot + 1) * L::TILE + cc * L::BOX + x * 128 +
+                                                           (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
                     }
                 }
-                if (!whole) {
-                    const int hi = (qi + p.right < len ? qi + p.right + 1 : len) - kv0;   // keys below it are not too far
-                    const int lo = qi - p.left - kv0, sk = p.sinks - kv0;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t see =
-                            bits_below(hi - 32 * x) & (~bits_below(lo - 32 * x) | bits_below(sk - 32 * x));
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(see >> e & 1)) v[32 * x + e] = 0xFF800000u;   // -inf
-                    }
-                }
-                // pass 1: the row maximum, eight partial ones
+                // P is free once its last PV is done (there is none before the first)
+                const bool p_free = test(L::BAR_PV + w, done - 1);
+                // pass 1: the row maximum, eight partial ones; and beside it P = 2^(s cs + cb - m)
+                // of the first half by the reference so far, which nearly always stays
                 float m8[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m8[i] = fmaxf(__uint_as_float(v[i]), __uint_as_float(v[8 + i]));
+                for (int i = 0; i < 8; ++i) m8[i] = fmaxf(__uint_as_float(va[i]), __uint_as_float(vb[i]));
 #pragma unroll
-                for (int i = 16; i < 64; i += 2)
-                    m8[(i >> 1) & 7] = fmax3(m8[(i >> 1) & 7], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                for (int i = 8; i < 32; ++i) m8[i & 7] = fmax3(m8[i & 7], __uint_as_float(va[i]), __uint_as_float(vb[i]));
                 const float mx = fmaf(fmaxf(fmax3(fmax3(m8[0], m8[1], m8[2]), m8[3], m8[4]), fmax3(m8[5], m8[6], m8[7])), cs, cb);
-                // the reference moves when a row grew by more than 2^8
+                // it moves when a row grew by more than 2^8
                 const bool resc = mx > m_used + 8.f;
-                if (__any_sync(0xFFFFFFFFu, resc)) {
-                    const float alpha = resc ? hw_exp2(m_used - mx) : 1.f;
-                    if (resc) m_used = mx;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) r4[i] = f2_mul(r4[i], f2_pack(alpha, alpha));
-                    if (begun) {
-                        // O is whole once the PV before is done
-                        if (!(ok = wait(L::BAR_PV + w, done - 1))) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int cc = 0; cc < HD / 16; ++cc) {   // (few columns at once: S holds the registers)
-                            uint32_t o[16];
-                            tmem_ld16(scol + L::O_COL + 16 * cc, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st16(scol + L::O_COL + 16 * cc, o);
+                const uint64_t c2 = f2_pack(cs, cs);
+                uint64_t nm2 = f2_pack(cb + nm0, cb + nm0);
+                uint64_t rt[2] = {r2[0], r2[1]};
+                uint32_t pk[16];
+                exp_pass(va, c2, nm2, rt, pk);
+                if (!__all_sync(0xFFFFFFFFu, !resc && p_free)) {
+                    if (__any_sync(0xFFFFFFFFu, resc)) {
+                        const float alpha = resc ? hw_exp2(m_used - mx) : 1.f;
+                        if (resc) {
+                            m_used = mx;
+                            nm0 = -mx;
                         }
-                        tmem_wait_st();
-                    }
-                }
-                if (kv0 + BKV > len) {
-                    // the last tile: V's rows behind the sequence become zeros, each
-                    // warp its share of them (a row is 128 bytes of each box)
-                    const uint32_t slot = vlast % R;
-                    if (!(ok = wait(L::BAR_VF + slot, vlast / R))) break;
-                    for (int x = len - kv0 + 4 * wq + (lane >> 3); x < BKV; x += 16)
+                        rt[0] = f2_mul(r2[0], f2_pack(alpha, alpha));
+                        rt[1] = f2_mul(r2[1], f2_pack(alpha, alpha));
+                        nm2 = f2_pack(cb + nm0, cb + nm0);
+                        exp_pass(va, c2, nm2, rt, pk);
+                        if (begun) {
+                            // O is whole once the PV before is done
+                            if (!(ok = wait(L::BAR_PV + w, done - 1))) break;
+                            tc_fence_after();
 #pragma unroll
-                        for (int cc = 0; cc < L::NB; ++cc)
-                            *reinterpret_cast<uint4 *>(smem + L::V_OFF + slot * L::TILE + cc * L::BOX + x * 128 + (lane & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                    fence_async_smem();
+                            for (int cc = 0; cc < HD / 16; ++cc) {   // (few columns at once: S holds the registers)
+                                uint32_t o[16];
+                                tmem_ld16(scol + L::O_COL + 16 * cc, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st16(scol + L::O_COL + 16 * cc, o);
+                            }
+                        }
+                    }
+                    if (!(ok = wait(L::BAR_PV + w, done - 1))) break;
                 }
-                // pass 2: P = 2^(s cs + cb - m) as bf16 and its row sum over the f32
-                // values.  What the next tile needs is worked out beside it.
-                const float nm = cb - (m_used == -INFINITY ? 0.f : m_used);
-                const uint64_t c2 = f2_pack(cs, cs), nm2 = f2_pack(nm, nm);
-                // P is free once its last PV is done
-                const bool p_free = begun ? test(L::BAR_PV + w, done - 1) : true;
+                tc_fence_after();
+                tmem_st16(scol + L::P_COL, pk);
+                // the second half; what the next tile needs is worked out beside it
+                const bool s_there = test(L::BAR_SF + w, done + 1);
+                exp_pass(vb, c2, nm2, rt, pk);
+                r2[0] = rt[0];
+                r2[1] = rt[1];
                 t = t + 1 == mine.sink ? mine.first : t + 1;
                 more = t < mine.end;
                 look(t * BKV);
-                uint32_t pk[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float a0, a1;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), c2, nm2), a0, a1);
-                    const float p0 = hw_exp2(a0), p1 = hw_exp2(a1);
-                    r4[e & 3] = f2_add(r4[e & 3], f2_pack(p0, p1));
-                    pk[e] = pack_bf16x2(p0, p1);
-                }
-                if (begun) {
-                    if (!(ok = settle(p_free, L::BAR_PV + w, done - 1))) break;
+                tmem_st16(scol + L::P_COL + 16, pk);
+                begun = true;
+                ++done;
+                // the next S while P is on its way to TMEM (not waited for yet: it may come
+                // only behind this tile's PV)
+                const bool ahead = __all_sync(0xFFFFFFFFu, s_there) && more;
+                if (ahead) {
                     tc_fence_after();
+                    tmem_ld32(scol, va);
+                    tmem_ld32(scol + 32, vb);
                 }
-                tmem_st32(scol + L::P_COL, pk);
-                s_there = test(L::BAR_SF + w, done + 1);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::BAR_PF + w));
-                begun = true;
-                ++done;
+                arrive_if(bar(L::BAR_PF + w), lane == 0);
+                if (more && !ahead) {
+                    if (!(ok = wait(L::BAR_SF + w, done))) break;
+                    tc_fence_after();
+                    tmem_ld32(scol, va);
+                    tmem_ld32(scol + 32, vb);
+                }
             }
             if (!ok) break;
             // ---- epilogue: O / l, one row per thread (0 where nothing is visible)
-            float r8[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f2_unpack(r4[i], r8[2 * i], r8[2 * i + 1]);
-            const float l = ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
+            float s0, s1, s2, s3;
+            f2_unpack(r2[0], s0, s1);
+            f2_unpack(r2[1], s2, s3);
+            const float l = (s0 + s1) + (s2 + s3);
             const float inv = 1.f / l;
             float finite = l;                            // NaN once a value of the row is not finite
             r = get_record(it);
@@ -868,7 +877,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                     // O is in registers: the next item's first PV may overwrite it
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(L::BAR_OFREE + w));
+                    arrive_if(bar(L::BAR_OFREE + w), lane == 0);
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) finite = fmaf(__uint_as_float(o[e]), 0.f, finite);
@@ -909,17 +918,11 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
 }
 
 template <int HD, bool BIAS>
-te_status launch(SpanParams &p, cudaStream_t stream) {
+te_status launch(const SpanParams &p, cudaStream_t stream) {
     using L = SLayout<HD>;
     constexpr int most = BIAS ? 227 * 1024 : L::TAB_OFF + 1024;
-    int smem = L::TAB_OFF + 1024;
-    if (BIAS) {
-        // two spread biases, the next head's beside this one's, where they fit
-        const int nb = p.two_sided ? 2 * p.side : p.side, spread = 4 * (2 * (p.reach + PAD) + 1);
-        smem += 4 * nb + spread;
-        p.nbuf = smem + spread <= most ? 2 : 1;
-        if (p.nbuf == 2) smem += spread;
-    }
+    const int nb = p.two_sided ? 2 * p.side : p.side;
+    const int smem = L::TAB_OFF + 1024 + (BIAS ? 4 * (nb + 2 * (2 * (p.reach + PAD) + 1)) : 0);
     static std::atomic<bool> ready[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
