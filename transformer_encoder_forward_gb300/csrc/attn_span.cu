@@ -78,12 +78,14 @@ template <int HD>
 struct SLayout {
     static constexpr int NB = HD / 64;              // 64-column boxes per tile row
     static constexpr int NT = HD == 64 ? 3 : 2;     // query tiles
-    static constexpr int NQ = HD == 64 ? 2 : 1;     // Q buffers: the next item's Q beside this one's
-    static constexpr int R = HD == 64 ? 4 : 3;      // pairs of a K and a V tile in flight
+    // pairs of a K and a V tile in flight: as many as fit.  Where there is a window the
+    // first query tile is done with an item's keys while the last still needs
+    // some; the ring lets it go on to the next item.
+    static constexpr int R = HD == 64 ? 7 : 3;
     static constexpr int QTILE = BQ * HD * 2, TILE = BKV * HD * 2;
     static constexpr int QBOX = BQ * 128, BOX = BKV * 128;   // 64 columns of them
-    static constexpr int Q_OFF = 0;                 // Q[NQ][NT]
-    static constexpr int K_OFF = NQ * NT * QTILE;   // [R] K, V
+    static constexpr int Q_OFF = 0;                 // Q[NT]
+    static constexpr int K_OFF = NT * QTILE;        // [R] K, V
     static constexpr int STG_OFF = K_OFF + R * 2 * TILE;     // a softmax warp's 32 rows of 32 outputs
     static constexpr int STG_WARP = 32 * 64;
     // warps: softmax (4 a query tile), one a query tile that issues its MMAs, and in
@@ -95,9 +97,9 @@ struct SLayout {
     static_assert(NT * SOFTMAX_REGS + OTHER_REGS <= (NT + 1) * LAUNCH_REGS && LAUNCH_REGS * NTHREADS <= 65536, "register split");
     static constexpr int BAR_OFF = STG_OFF + SOFTMAX_WARPS * STG_WARP;
     // barriers
-    static constexpr int BAR_Q = 0;                      // [NQ][NT] Q loaded, per buffer and query tile
-    static constexpr int BAR_QE = BAR_Q + NT * NQ;       // [NQ][NT] Q read by the item's last S
-    static constexpr int BAR_KV = BAR_QE + NT * NQ;      // [R] K and V loaded
+    static constexpr int BAR_Q = 0;                      // [NT] Q loaded
+    static constexpr int BAR_QE = BAR_Q + NT;            // [NT] Q read by the item's last S
+    static constexpr int BAR_KV = BAR_QE + NT;      // [R] K and V loaded
     static constexpr int BAR_KVE = BAR_KV + R;           // [R] K and V read by every query tile
     static constexpr int BAR_SF = BAR_KVE + R;           // [NT] S ready
     static constexpr int BAR_SFREE = BAR_SF + NT;        // [NT] S is in registers
@@ -128,8 +130,9 @@ struct KeyTiles {
     int sink, first, end;
     __device__ __forceinline__ bool has(int t) const { return t < end && (t >= first || t < sink); }
     __device__ __forceinline__ int count() const { return sink + end - first; }
-    // the j-th of them
+    // the j-th of them, and the place of a tile among them
     __device__ __forceinline__ int tile(int j) const { return j < sink ? j : j + first - sink; }
+    __device__ __forceinline__ int place(int t) const { return t < sink ? t : t - first + sink; }
 };
 __device__ __forceinline__ KeyTiles key_tiles(const SpanParams &p, int r0, int r1, int len) {
     const int lo = r0 > p.left ? r0 - p.left : 0;
@@ -162,6 +165,49 @@ __device__ __forceinline__ float bias_of(const SpanParams &p, const float *col, 
 __device__ __forceinline__ void arrive_if(uint32_t bar, bool on) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
                  "r"((uint32_t)on)
+                 : "memory");
+}
+
+// Shared-memory descriptors of the 128-byte swizzle differ in their low words
+// alone (address, leading offset); the high word is the same for both operand forms.
+constexpr uint32_t DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
+
+// Four MMAs along K = 64 as one block, issued by the lane whose e is set: the
+// predicates are made once and the descriptors by adds to their low words.  First S = Q K^T, then O += P V.
+__device__ __forceinline__ void mma_s4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint32_t e) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %6};\n\tmov.b64 b, {y, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a, {x, %6};\n\tmov.b64 b, {y, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %6};\n\tmov.b64 b, {y, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(e), "n"(DESC_HI)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pv4(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint32_t e) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 b, {y, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n\t"
+        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 b, {y, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n\t"
+        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 b, {y, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, 1;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(e), "n"(DESC_HI)
+        : "memory");
+}
+
+__device__ __forceinline__ void arrive_n(uint32_t bar, int n, uint32_t e) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+                 "r"(n), "r"(e)
                  : "memory");
 }
 
@@ -359,7 +405,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == L::TMA_WARP && lane == 0) {
         tma_prefetch_desc(&p.map);
-        for (int i = 0; i < 2 * NT * L::NQ; ++i) mbar_init(bar(L::BAR_Q + i), 1);
+        for (int i = 0; i < 2 * NT; ++i) mbar_init(bar(L::BAR_Q + i), 1);
         for (int i = 0; i < R; ++i) {
             mbar_init(bar(L::BAR_KV + i), 1);
             mbar_init(bar(L::BAR_KVE + i), NT);
@@ -426,8 +472,8 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
     struct Ring {
         int at;
         uint32_t phase;
-        __device__ __forceinline__ void step() {
-            if (++at == R) { at = 0; phase ^= 1; }
+        __device__ __forceinline__ void step(int k = 1) {
+            for (at += k; at >= R; at -= R) phase ^= 1;
         }
     };
 
@@ -508,22 +554,29 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 const int g = r.h / p.group;
                 const KeyTiles tiles = tiles_of(r);
                 const int n = tiles.count();
+                KeyTiles kw[NT];
 #pragma unroll
-                for (int w = 0; w < NT; ++w) {
-                    if (!ok || r.q0 + w * BQ >= r.len) break;
-                    const int qb = L::NQ == 2 ? NT * (qn[w] & 1) + w : w;
-                    if (!wait(L::BAR_QE + qb, (L::NQ == 2 ? qn[w] >> 1 : qn[w]) ^ 1)) { ok = false; break; }
-                    ++qn[w];
-                    mbar_arrive_expect_tx_e(bar(L::BAR_Q + qb), L::QTILE, e);
-                    for (int c = 0; c < 2 * L::NB; ++c)   // 64 columns, 64 rows a box
-                        tma_load_2d_e(sb + L::Q_OFF + qb * L::QTILE + c * L::BOX, &p.map, bar(L::BAR_Q + qb),
-                                      p.q_off + r.h * HD + 64 * (c >> 1), r.off + r.q0 + w * BQ + BKV * (c & 1), e);
-                }
+                for (int w = 0; w < NT; ++w) kw[w] = tiles_of_w(r, w);
                 Item r2 = {0, 0, 0, 0};
                 for (int j = 0; j < n && ok; ++j) {
-                    if (!(ok = wait(L::BAR_KVE + kv.at, kv.phase ^ 1))) break;
+                    const int t = tiles.tile(j);
+                    int idle = 0;                        // query tiles that do not see this key tile
+#pragma unroll
+                    for (int w = 0; w < NT; ++w) {
+                        idle += kw[w].has(t) ? 0 : 1;
+                        // a query tile's Q comes with the first key tile that it sees
+                        if (!ok || kw[w].end == 0 || t != kw[w].tile(0)) continue;
+                        if (!wait(L::BAR_QE + w, qn[w] ^ 1)) { ok = false; continue; }
+                        ++qn[w];
+                        mbar_arrive_expect_tx_e(bar(L::BAR_Q + w), L::QTILE, e);
+#pragma unroll
+                        for (int c = 0; c < 2 * L::NB; ++c)   // 64 columns, 64 rows a box
+                            tma_load_2d_e(sb + L::Q_OFF + w * L::QTILE + c * L::BOX, &p.map, bar(L::BAR_Q + w),
+                                          p.q_off + r.h * HD + 64 * (c >> 1), r.off + r.q0 + w * BQ + BKV * (c & 1), e);
+                    }
+                    if (!ok || !(ok = wait(L::BAR_KVE + kv.at, kv.phase ^ 1))) break;
                     const uint32_t to = sb + L::K_OFF + kv.at * 2 * L::TILE, b = bar(L::BAR_KV + kv.at);
-                    const int row = r.off + tiles.tile(j) * BKV;
+                    const int row = r.off + t * BKV;
                     mbar_arrive_expect_tx_e(b, 2 * L::TILE, e);
 #pragma unroll
                     for (int c = 0; c < L::NB; ++c)
@@ -531,16 +584,17 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
 #pragma unroll
                     for (int c = 0; c < L::NB; ++c)
                         tma_load_2d_e(to + L::TILE + c * L::BOX, &p.map, b, p.v_off + g * HD + 64 * c, row, e);
+                    // those that do not see it have no need to say that they read it
+                    if (idle) arrive_n(bar(L::BAR_KVE + kv.at), idle, e);
                     kv.step();
                     ++kvn;
-                    if (j == 0) {
-                        if (BIAS && it == 0) spread_bias(r.h);
-                        // the next item, well before this one ends
+                    if (BIAS && it == 0 && j == 0) spread_bias(r.h);
+                    // the next item and its bias, once the ring is full or the item's loads are out
+                    if (j == R - 1 || (j < R - 1 && j + 1 == n)) {
                         if (ok) next = answer();
                         if (ok) publish(it + 1, r2);
+                        if (BIAS && ok && r2.len > 0) spread_bias(r2.h);
                     }
-                    // its bias once some tiles are on their way
-                    if (BIAS && ok && r2.len > 0 && (j == 2 || (j < 2 && j + 1 == n))) spread_bias(r2.h);
                 }
                 r = r2;
             }
@@ -548,11 +602,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 // no copy of ours may still be landing when the CTA exits
 #pragma unroll
                 for (int w = 0; w < NT; ++w)
-                    for (int x = 0; x < L::NQ; ++x)
-                        if ((int)qn[w] > x) {
-                            const uint32_t u = qn[w] - 1 - x;
-                            mbar_wait(bar(L::BAR_Q + (L::NQ == 2 ? NT * (u & 1) + w : w)), (L::NQ == 2 ? u >> 1 : u) & 1, 20000000ull);
-                        }
+                    if (qn[w]) mbar_wait(bar(L::BAR_Q + w), (qn[w] - 1) & 1, 20000000ull);
                 for (int i = kvn - R < 0 ? 0 : kvn - R; i < kvn; ++i) mbar_wait(bar(L::BAR_KV + i % R), (i / R) & 1, 20000000ull);
                 if (asked) mbar_wait(bar(L::BAR_CLC), (asked - 1) & 1, 20000000ull);
             }
@@ -563,98 +613,79 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             const uint32_t e = elect_one();
             constexpr uint32_t idesc_s = idesc_bf16_f32(BQ, BKV);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(BQ, HD) | (1u << 16);   // B MN-major
-            const uint64_t kd = smem_desc_sw128(sb + L::K_OFF);
-            const uint64_t vd = smem_desc_mn_sw128(sb + L::K_OFF + L::TILE, L::BOX);
-            const uint64_t qd = smem_desc_sw128(sb + L::Q_OFF);
+            const uint32_t kd = (uint32_t)smem_desc_sw128(sb + L::K_OFF);
+            const uint32_t vd = (uint32_t)smem_desc_mn_sw128(sb + L::K_OFF + L::TILE, L::BOX);
+            const uint32_t q0 = (uint32_t)smem_desc_sw128(sb + L::Q_OFF) + w * (L::QTILE >> 4);
             const uint32_t stm = tbase + w * L::TILE_COLS;
             uint32_t sc = 0, pc = 0;                     // S and PV issued
-            uint32_t items = 0, qn = 0;                  // items with rows, as PV and as Q see them
-            Ring sr = {0, 0}, pr = {0, 0};               // the K whose S, the V whose PV comes next
-            uint64_t q0 = qd;                            // this item's Q
-            // S = Q K^T of the next K tile (mine: this query tile sees it)
-            auto step_s = [&](bool mine) -> bool {
-                const bool kv_there = test(L::BAR_KV + sr.at, sr.phase);
+            uint32_t items = 0;                          // items with rows before this one
+            Ring kv = {0, 0};                            // the pair of K and V whose S comes next
+            // S = Q K^T of the next key tile that this query tile sees
+            auto step_s = [&]() -> bool {
+                const bool there = test(L::BAR_KV + kv.at, kv.phase);
                 // the softmax has the last S in registers (before the first there is nothing to wait for)
-                const bool s_free = mine ? test(L::BAR_SFREE + w, sc + 1) : true;
-                if (!__all_sync(0xFFFFFFFFu, kv_there && s_free) &&
-                    !(wait(L::BAR_KV + sr.at, sr.phase) && (!mine || wait(L::BAR_SFREE + w, sc + 1))))
+                const bool s_free = test(L::BAR_SFREE + w, sc + 1);
+                if (!__all_sync(0xFFFFFFFFu, there && s_free) &&
+                    !(wait(L::BAR_KV + kv.at, kv.phase) && wait(L::BAR_SFREE + w, sc + 1)))
                     return false;
-                if (mine) {
-                    tc_fence_after();
-                    const uint64_t k0 = kd + (uint64_t)(sr.at * (2 * L::TILE >> 4));
+                tc_fence_after();
+                const uint32_t k0 = kd + kv.at * (2 * L::TILE >> 4);
 #pragma unroll
-                    for (int k = 0; k < HD / 16; ++k)
-                        mma_ss_bf16_e(stm, q0 + (((k >> 2) * L::QBOX + (k & 3) * 32) >> 4),
-                                      k0 + (((k >> 2) * L::BOX + (k & 3) * 32) >> 4), idesc_s, k > 0, e);
-                    mma_commit_e(bar(L::BAR_SF + w), e);
-                    ++sc;
-                }
-                sr.step();
+                for (int c = 0; c < L::NB; ++c)
+                    mma_s4(stm, q0 + c * (L::QBOX >> 4), k0 + c * (L::BOX >> 4), idesc_s, c > 0, e);
+                mma_commit_e(bar(L::BAR_SF + w), e);
+                ++sc;
                 return true;
             };
-            // O += P V of the next V tile (its K's S was waited for, so it is there); more: not the item's first
-            auto step_pv = [&](bool mine, bool more) -> bool {
-                if (mine) {
-                    const bool p_there = test(L::BAR_PF + w, pc);
-                    // an item's first overwrites O, whose last rows have been read
-                    const bool o_free = more ? true : test(L::BAR_OFREE + w, items + 1);
-                    if (!__all_sync(0xFFFFFFFFu, p_there && o_free) &&
-                        !((more || wait(L::BAR_OFREE + w, items + 1)) && wait(L::BAR_PF + w, pc)))
-                        return false;
-                    if (!more) ++items;
-                    tc_fence_after();
-                    const uint64_t v0 = vd + (uint64_t)(pr.at * (2 * L::TILE >> 4));
-#pragma unroll
-                    for (int k = 0; k < BKV / 16; ++k)
-                        mma_ts_bf16_e(stm + L::O_COL, stm + L::P_COL + 8 * k, v0 + (uint64_t)(128 * k), idesc_pv,
-                                      more || k != 0, e);
-                    mma_commit_e(bar(L::BAR_PV + w), e);
-                    ++pc;
-                    mma_commit_e(bar(L::BAR_KVE + pr.at), e);
-                } else {
-                    arrive_if(bar(L::BAR_KVE + pr.at), e != 0);
-                }
-                pr.step();
+            // O += P V of the pair in ring place `at` (its S was waited for, so it is there); more: not the item's first
+            auto step_pv = [&](int at, bool more) -> bool {
+                const bool p_there = test(L::BAR_PF + w, pc);
+                // an item's first overwrites O, whose last rows have been read
+                const bool o_free = more ? true : test(L::BAR_OFREE + w, items + 1);
+                if (!__all_sync(0xFFFFFFFFu, p_there && o_free) &&
+                    !((more || wait(L::BAR_OFREE + w, items + 1)) && wait(L::BAR_PF + w, pc)))
+                    return false;
+                tc_fence_after();
+                mma_pv4(stm + L::O_COL, stm + L::P_COL, vd + at * (2 * L::TILE >> 4), idesc_pv, more, e);
+                mma_commit_e(bar(L::BAR_PV + w), e);
+                mma_commit_e(bar(L::BAR_KVE + at), e);
+                ++pc;
                 return true;
             };
-            KeyTiles all = {0, 0, 0}, kw = {0, 0, 0};
-            int qbar = 0;                                // the Q buffer's barrier
-            // takes item number it: waits for its Q, issues its first S
-            auto begin = [&](int it) -> bool {
+            for (int it = 0; ok; ++it) {
                 Item r;
-                if (!read_record(it, r)) return false;
-                all = kw = {0, 0, 0};
-                if (r.len == 0) return true;
-                all = tiles_of(r);
-                kw = tiles_of_w(r, w);
-                if (kw.end > 0) {
-                    qbar = L::NQ == 2 ? NT * (qn & 1) + w : w;
-                    if (!wait(L::BAR_Q + qbar, L::NQ == 2 ? qn >> 1 : qn)) return false;
-                    q0 = qd + (uint64_t)(qbar * (L::QTILE >> 4));
-                    ++qn;
+                if (!(ok = read_record(it, r)) || r.len == 0) break;
+                const KeyTiles all = tiles_of(r), mine = tiles_of_w(r, w);
+                const int n = all.count(), m = mine.count();
+                if (m == 0) {                            // the item has no rows of this query tile
+                    kv.step(n);
+                    continue;
                 }
-                return step_s(kw.has(all.tile(0)));
-            };
-            ok = begin(0);
-            for (int it = 0; ok && all.end > 0; ++it) {
-                const KeyTiles now = all, mine = kw;
-                const int n = now.count();
-                bool more = false, see = mine.has(now.tile(0));
-                for (int j = 0; j < n && ok; ++j) {
-                    // S of the next key tile, or the next item's first, then this one's PV
-                    bool see_next = false;
-                    if (j + 1 < n) {
-                        see_next = mine.has(now.tile(j + 1));
-                        ok = step_s(see_next);
+                int at_list = all.place(mine.tile(0));   // where the next S's key tile is among the item's
+                kv.step(at_list);
+                ok = wait(L::BAR_Q + w, items) && step_s();
+                for (int i = 0; i < m && ok; ++i) {
+                    // S of the next key tile, then this one's PV; the other way round where the
+                    // next is so far on that it waits for this one's place in the ring
+                    const int at = kv.at;
+                    bool pv = false;
+                    if (i + 1 < m) {
+                        const int next = all.place(mine.tile(i + 1));
+                        if (next - at_list >= R) {
+                            pv = true;
+                            ok = step_pv(at, i > 0);
+                        }
+                        kv.step(next - at_list);
+                        at_list = next;
+                        ok = ok && step_s();
                     } else {
                         // every S of the item is issued: its Q may be overwritten behind them
-                        if (mine.end > 0) mma_commit_e(bar(L::BAR_QE + qbar), e);
-                        ok = begin(it + 1);
+                        mma_commit_e(bar(L::BAR_QE + w), e);
                     }
-                    ok = ok && step_pv(see, more);
-                    more = more || see;
-                    see = see_next;
+                    if (!pv) ok = ok && step_pv(at, i > 0);
                 }
+                kv.step(n - at_list);
+                ++items;
             }
             // nothing of ours may still be running when TMEM is given back
             mma_commit_e(bar(L::BAR_FIN + w), e);
@@ -857,8 +888,8 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             f2_unpack(r2[0], s0, s1);
             f2_unpack(r2[1], s2, s3);
             const float l = (s0 + s1) + (s2 + s3);
-            const float inv = 1.f / l;
-            float finite = l;                            // NaN once a value of the row is not finite
+            const float inv = hw_rcp(l);                 // (2^-23 of itself, then rounded to bf16)
+            float fin[4] = {l, 0.f, 0.f, 0.f};           // their sum is NaN once a value of the row is not finite
             r = get_record(it);
             let_record(it);
             // rows go out through shared memory, so that a store of the warp writes 8
@@ -880,7 +911,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                     arrive_if(bar(L::BAR_OFREE + w), lane == 0);
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) finite = fmaf(__uint_as_float(o[e]), 0.f, finite);
+                for (int e = 0; e < 32; ++e) fin[e & 3] = fmaf(__uint_as_float(o[e]), 0.f, fin[e & 3]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint4 u;
@@ -900,6 +931,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 __syncwarp();
             }
             // rows whose sum is 0 or not finite, or that hold a value that is not
+            const float finite = (fin[0] + fin[1]) + (fin[2] + fin[3]);
             uint32_t mend = __ballot_sync(0xFFFFFFFFu, qi < len && !(finite > 0.f && finite <= FLT_MAX));
             while (mend) {
                 const int x = __ffs(mend) - 1;
