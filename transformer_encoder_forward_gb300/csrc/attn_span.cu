@@ -161,6 +161,16 @@ __device__ __forceinline__ float bias_of(const SpanParams &p, const float *col, 
     return col[p.two_sided && d > 0 ? b + p.side : b];
 }
 
+// A whole warp waits for a phase, for 200 ms at most (then false); the loop out of
+// the way of the code around it.
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity) {
+    if (__builtin_expect(__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)), 1)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
+        if (__all_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > 200000000ull)) return false;
+    return true;
+}
+
 // Arrives where `on` is set, without a branch.
 __device__ __forceinline__ void arrive_if(uint32_t bar, bool on) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
@@ -279,6 +289,7 @@ __device__ __forceinline__ void mend_row(const SpanParams &p, const float *bias,
             if (key < end) {
                 const __nv_bfloat16 *k = kb + (long long)key * p.ld;
                 float acc = 0.f;
+#pragma unroll 1
                 for (int c = 0; c < HD; ++c) acc = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), acc);
                 float b = 0.f;
                 if (BIAS) {
@@ -296,6 +307,7 @@ __device__ __forceinline__ void mend_row(const SpanParams &p, const float *bias,
             l = l * alpha + warp_sum(pr);
 #pragma unroll
             for (int c = 0; c < C; ++c) o[c] *= alpha;
+#pragma unroll 1
             for (int t = 0; t < 32 && k0 + t < end; ++t) {
                 const float st = __shfl_sync(0xFFFFFFFFu, s, t), pt = __shfl_sync(0xFFFFFFFFu, pr, t);
                 if (st == -INFINITY) continue;   // a bias of -inf masks too
@@ -439,7 +451,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
     const uint32_t tbase = tmem_slot[0];
     bool ok = true;
     // waits of a whole warp; false: given up
-    auto wait = [&](int b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar(b), parity & 1)) != 0; };
+    auto wait = [&](int b, uint32_t parity) { return wait_on(bar(b), parity & 1); };
     // The same in two parts: test looks without waiting, settle comes once the
     // answer is needed; a look at a barrier costs its latency, which the work
     // between the two hides.
@@ -548,31 +560,52 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 arrive_if(bar(L::BAR_BF + buf), lane == 0);
                 ++built;
             };
-            Item r;
-            publish(0, r);
-            for (int it = 0; ok && r.len > 0; ++it) {
+            // Item number it is r, the one behind it r2; before the first there is an empty one.
+            // The next item is published once the ring is full or the item's loads are out, and its
+            // head's bias spread behind the load that follows.
+            Item r = {0, 0, 0, 0}, r2 = r;
+            int to_spread = -1;
+            for (int it = -1; ok && (it < 0 || r.len > 0); ++it, r = r2) {
                 const int g = r.h / p.group;
-                const KeyTiles tiles = tiles_of(r);
-                const int n = tiles.count();
-                KeyTiles kw[NT];
+                KeyTiles tiles = {0, 0, 0}, kw[NT];
+                if (it >= 0) tiles = tiles_of(r);
 #pragma unroll
-                for (int w = 0; w < NT; ++w) kw[w] = tiles_of_w(r, w);
-                Item r2 = {0, 0, 0, 0};
-                for (int j = 0; j < n && ok; ++j) {
+                for (int w = 0; w < NT; ++w) kw[w] = it >= 0 ? tiles_of_w(r, w) : KeyTiles{0, 0, 0};
+                const int n = it >= 0 ? tiles.count() : 0;
+                int qw = 0;                              // the query tile whose Q comes next
+                for (int j = 0; ok; ++j) {
+                    if (j == (n < R ? n : R)) {
+                        if (it >= 0) next = answer();
+                        if (ok) publish(it + 1, r2);
+                        if (r2.len > 0) to_spread = r2.h;
+                    }
+                    if (!ok || j >= n) break;
                     const int t = tiles.tile(j);
-                    int idle = 0;                        // query tiles that do not see this key tile
+                    int idle = 0, first = -1;            // query tiles that do not see this key tile; qw's first
 #pragma unroll
                     for (int w = 0; w < NT; ++w) {
                         idle += kw[w].has(t) ? 0 : 1;
-                        // a query tile's Q comes with the first key tile that it sees
-                        if (!ok || kw[w].end == 0 || t != kw[w].tile(0)) continue;
-                        if (!wait(L::BAR_QE + w, qn[w] ^ 1)) { ok = false; continue; }
-                        ++qn[w];
-                        mbar_arrive_expect_tx_e(bar(L::BAR_Q + w), L::QTILE, e);
+                        if (w == qw && kw[w].end > 0) first = kw[w].tile(0);
+                    }
+                    // a query tile's Q comes with the first key tile that it sees (later tiles
+                    // see nothing sooner)
+                    while (ok && t == first) {
+                        uint32_t used = 0;
+#pragma unroll
+                        for (int w = 0; w < NT; ++w)
+                            if (w == qw) used = qn[w]++;
+                        if (!(ok = wait(L::BAR_QE + qw, used ^ 1))) break;
+                        const uint32_t to = sb + L::Q_OFF + qw * L::QTILE, b = bar(L::BAR_Q + qw);
+                        mbar_arrive_expect_tx_e(b, L::QTILE, e);
 #pragma unroll
                         for (int c = 0; c < 2 * L::NB; ++c)   // 64 columns, 64 rows a box
-                            tma_load_2d_e(sb + L::Q_OFF + w * L::QTILE + c * L::BOX, &p.map, bar(L::BAR_Q + w),
-                                          p.q_off + r.h * HD + 64 * (c >> 1), r.off + r.q0 + w * BQ + BKV * (c & 1), e);
+                            tma_load_2d_e(to + c * L::BOX, &p.map, b, p.q_off + r.h * HD + 64 * (c >> 1),
+                                          r.off + r.q0 + qw * BQ + BKV * (c & 1), e);
+                        ++qw;
+                        first = -1;
+#pragma unroll
+                        for (int w = 0; w < NT; ++w)
+                            if (w == qw && kw[w].end > 0) first = kw[w].tile(0);
                     }
                     if (!ok || !(ok = wait(L::BAR_KVE + kv.at, kv.phase ^ 1))) break;
                     const uint32_t to = sb + L::K_OFF + kv.at * 2 * L::TILE, b = bar(L::BAR_KV + kv.at);
@@ -588,15 +621,11 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                     if (idle) arrive_n(bar(L::BAR_KVE + kv.at), idle, e);
                     kv.step();
                     ++kvn;
-                    if (BIAS && it == 0 && j == 0) spread_bias(r.h);
-                    // the next item and its bias, once the ring is full or the item's loads are out
-                    if (j == R - 1 || (j < R - 1 && j + 1 == n)) {
-                        if (ok) next = answer();
-                        if (ok) publish(it + 1, r2);
-                        if (BIAS && ok && r2.len > 0) spread_bias(r2.h);
+                    if (BIAS && to_spread >= 0) {
+                        spread_bias(to_spread);
+                        to_spread = -1;
                     }
                 }
-                r = r2;
             }
             if (!ok) {
                 // no copy of ours may still be landing when the CTA exits
@@ -625,7 +654,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 const bool there = test(L::BAR_KV + kv.at, kv.phase);
                 // the softmax has the last S in registers (before the first there is nothing to wait for)
                 const bool s_free = test(L::BAR_SFREE + w, sc + 1);
-                if (!__all_sync(0xFFFFFFFFu, there && s_free) &&
+                if (__builtin_expect(!__all_sync(0xFFFFFFFFu, there && s_free), 0) &&
                     !(wait(L::BAR_KV + kv.at, kv.phase) && wait(L::BAR_SFREE + w, sc + 1)))
                     return false;
                 tc_fence_after();
@@ -642,7 +671,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 const bool p_there = test(L::BAR_PF + w, pc);
                 // an item's first overwrites O, whose last rows have been read
                 const bool o_free = more ? true : test(L::BAR_OFREE + w, items + 1);
-                if (!__all_sync(0xFFFFFFFFu, p_there && o_free) &&
+                if (__builtin_expect(!__all_sync(0xFFFFFFFFu, p_there && o_free), 0) &&
                     !((more || wait(L::BAR_OFREE + w, items + 1)) && wait(L::BAR_PF + w, pc)))
                     return false;
                 tc_fence_after();
@@ -661,28 +690,31 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                     kv.step(n);
                     continue;
                 }
-                int at_list = all.place(mine.tile(0));   // where the next S's key tile is among the item's
-                kv.step(at_list);
-                ok = wait(L::BAR_Q + w, items) && step_s();
-                for (int i = 0; i < m && ok; ++i) {
-                    // S of the next key tile, then this one's PV; the other way round where the
-                    // next is so far on that it waits for this one's place in the ring
-                    const int at = kv.at;
-                    bool pv = false;
-                    if (i + 1 < m) {
-                        const int next = all.place(mine.tile(i + 1));
-                        if (next - at_list >= R) {
-                            pv = true;
-                            ok = step_pv(at, i > 0);
-                        }
+                // S of a key tile, then PV of the one before it; PV first where the next key tile
+                // is so far on that it waits for that one's place in the ring
+                int at_list = 0, si = 0;                 // where kv stands among the item's key tiles, S issued
+                int at_s = 0, at_pv = 0;                 // ring places of the last S and of the PV that comes next
+                ok = wait(L::BAR_Q + w, items);
+                for (int i = 0; i < m && ok;) {
+                    bool s_next = si < m && si <= i + 1;
+                    int next = 0;
+                    if (s_next) {
+                        next = all.place(mine.tile(si));
+                        s_next = si == i || next - at_list < R;
+                    }
+                    if (s_next) {
                         kv.step(next - at_list);
                         at_list = next;
-                        ok = ok && step_s();
-                    } else {
+                        at_pv = si == i ? kv.at : at_s;
+                        at_s = kv.at;
+                        ok = step_s();
                         // every S of the item is issued: its Q may be overwritten behind them
-                        mma_commit_e(bar(L::BAR_QE + w), e);
+                        if (++si == m) mma_commit_e(bar(L::BAR_QE + w), e);
+                    } else {
+                        ok = step_pv(at_pv, i > 0);
+                        at_pv = at_s;
+                        ++i;
                     }
-                    if (!pv) ok = ok && step_pv(at, i > 0);
                 }
                 kv.step(n - at_list);
                 ++items;
@@ -822,7 +854,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 uint64_t rt[2] = {r2[0], r2[1]};
                 uint32_t pk[16];
                 exp_pass(va, c2, nm2, rt, pk);
-                if (!__all_sync(0xFFFFFFFFu, !resc && p_free)) {
+                if (__builtin_expect(!__all_sync(0xFFFFFFFFu, !resc && p_free), 0)) {
                     if (__any_sync(0xFFFFFFFFu, resc)) {
                         const float alpha = resc ? hw_exp2(m_used - mx) : 1.f;
                         if (resc) {
@@ -875,7 +907,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 tc_fence_before();
                 __syncwarp();
                 arrive_if(bar(L::BAR_PF + w), lane == 0);
-                if (more && !ahead) {
+                if (__builtin_expect(more && !ahead, 0)) {
                     if (!(ok = wait(L::BAR_SF + w, done))) break;
                     tc_fence_after();
                     tmem_ld32(scol, va);
