@@ -266,63 +266,46 @@ __device__ __forceinline__ void exp_pass(const uint32_t (&v)[32], uint64_t c2, u
     }
 }
 
-// One output row from its visible keys alone, by one warp in f32: what the
-// tiled form computes, without products of masked values.  It ends at once when
-// all of the row is lost.
+// One output row from its visible keys alone, by one warp in f32, key by key:
+// what the tiled form computes, without products of masked values.  It ends at
+// once when all of the row is lost.  (Short rather than fast: no finite input
+// comes here, and its code lies among the softmax's.)
 template <int HD, bool BIAS>
 __device__ __forceinline__ void mend_row(const SpanParams &p, const float *bias, int off, int len, int h, int qi) {
-    constexpr int C = HD / 32;
-    const int lane = threadIdx.x & 31, g = h / p.group;
-    const __nv_bfloat16 *q = p.qkv + (long long)(off + qi) * p.ld + p.q_off + h * HD;
-    const __nv_bfloat16 *kb = p.qkv + (long long)off * p.ld + p.k_off + g * HD;
-    const __nv_bfloat16 *vb = p.qkv + (long long)off * p.ld + p.v_off + g * HD + lane * C;
+    constexpr int C = HD / 32;                           // channels of a lane
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat16 *row0 = p.qkv + (long long)off * p.ld + lane * C;
+    const __nv_bfloat16 *q = row0 + (long long)qi * p.ld + p.q_off + h * HD;
     const int lo = qi > p.left ? qi - p.left : 0;
     const int hi = qi + p.right + 1 < len ? qi + p.right + 1 : len;
     float m = -INFINITY, l = 0.f, o[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) o[c] = 0.f;
-    for (int part = 0; part < 2; ++part) {
-        const int from = part ? lo : 0, end = part ? hi : (p.sinks < lo ? p.sinks : lo);
-        for (int k0 = from; k0 < end; k0 += 32) {
-            const int key = k0 + lane;
-            float s = -INFINITY;
-            if (key < end) {
-                const __nv_bfloat16 *k = kb + (long long)key * p.ld;
-                float acc = 0.f;
 #pragma unroll 1
-                for (int c = 0; c < HD; ++c) acc = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), acc);
-                float b = 0.f;
-                if (BIAS) {
-                    const int d = key - qi;
-                    b = bias[d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d)];
-                }
-                s = fmaf(acc, p.scale_log2, b);
-            }
-            float wm = s;
+    for (int key = p.sinks > 0 ? 0 : lo; key < hi; key = key + 1 < p.sinks || key + 1 > lo ? key + 1 : lo) {
+        const __nv_bfloat16 *k = row0 + (long long)key * p.ld + (h / p.group) * HD;
+        float s = 0.f;
 #pragma unroll
-            for (int x = 16; x > 0; x >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xFFFFFFFFu, wm, x));
-            const float mn = fmaxf(m, wm), off2 = mn == -INFINITY ? 0.f : mn;
-            const float alpha = hw_exp2(m - off2), pr = hw_exp2(s - off2);
-            m = mn;
-            l = l * alpha + warp_sum(pr);
-#pragma unroll
-            for (int c = 0; c < C; ++c) o[c] *= alpha;
+        for (int c = 0; c < C; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(k[p.k_off + c]), s);
 #pragma unroll 1
-            for (int t = 0; t < 32 && k0 + t < end; ++t) {
-                const float st = __shfl_sync(0xFFFFFFFFu, s, t), pt = __shfl_sync(0xFFFFFFFFu, pr, t);
-                if (st == -INFINITY) continue;   // a bias of -inf masks too
-                const __nv_bfloat16 *v = vb + (long long)(k0 + t) * p.ld;
-#pragma unroll
-                for (int c = 0; c < C; ++c) o[c] = fmaf(pt, __bfloat162float(v[c]), o[c]);
-            }
-            bool lost = true;
-#pragma unroll
-            for (int c = 0; c < C; ++c) lost = lost && isnan(o[c]);
-            if (__all_sync(0xFFFFFFFFu, lost)) {
-                part = 2;
-                break;
-            }
+        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
+        float b = 0.f;
+        if (BIAS) {
+            const int d = key - qi;
+            b = bias[d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d)];
         }
+        s = fmaf(s, p.scale_log2, b);
+        if (s == -INFINITY) continue;                    // a bias of -inf masks too
+        const float mn = fmaxf(m, s), alpha = hw_exp2(m - mn), pr = hw_exp2(s - mn);
+        m = mn;
+        l = l * alpha + pr;
+        bool lost = true;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            o[c] = fmaf(pr, __bfloat162float(k[p.v_off + c]), o[c] * alpha);
+            lost = lost && isnan(o[c]);
+        }
+        if (__all_sync(0xFFFFFFFFu, lost)) break;
     }
     __nv_bfloat16 *orow = p.out + (long long)(off + qi) * p.ldo + h * HD + lane * C;
 #pragma unroll
@@ -829,6 +812,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                         // warp its share of them (a row is 128 bytes of each box)
                         const uint32_t slot = vlast % R;
                         if (!(ok = wait(L::BAR_KV + slot, vlast / R))) break;
+#pragma unroll 1
                         for (int x = len - kv0 + 4 * wq + (lane >> 3); x < BKV; x += 16)
 #pragma unroll
                             for (int cc = 0; cc < L::NB; ++cc)
@@ -965,6 +949,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             // rows whose sum is 0 or not finite, or that hold a value that is not
             const float finite = (fin[0] + fin[1]) + (fin[2] + fin[3]);
             uint32_t mend = __ballot_sync(0xFFFFFFFFu, qi < len && !(finite > 0.f && finite <= FLT_MAX));
+#pragma unroll 1
             while (mend) {
                 const int x = __ffs(mend) - 1;
                 mend &= mend - 1;
