@@ -34,7 +34,8 @@
  *     calls return before it completes.  te_q8_linear, te_q8_gated_linear,
  *     te_attn_varlen_fwd, te_attn_sink_fwd, te_attn_relbias_fwd,
  *     the row ops, te_quant_rows, te_rownorm_quant, te_i8_linear,
- *     te_i8_gated_linear, te_qk_rope_axes and te_encoder_block_fwd are
+ *     te_i8_gated_linear, te_qk_rope_axes, te_encoder_block_fwd and
+ *     te_encoder_block_attn_fwd are
  *     capturable in a CUDA graph (no host synchronisation, no allocation).
  */
 #ifndef TEFWD_H
@@ -592,6 +593,25 @@ size_t te_encoder_block_workspace(const te_block_desc *desc, int32_t t);
 te_status te_encoder_block_fwd(const te_block_desc *desc, float *x, void *a,
                                const int32_t *cu_host, const int32_t *cu_dev, int32_t nseq,
                                void *workspace, size_t ws_bytes, te_stream stream);
+
+/* The attention step of te_encoder_block_attn_fwd: te_attn_sink_fwd's limits
+ * and sinks and, plan != NULL, te_attn_relbias_fwd's bias (its plan on the host;
+ * its table f32 [plan->buckets, n_heads], rows ldt floats apart, on the device). */
+typedef struct {
+    int32_t left, right, sinks;
+    const te_relpos *plan;
+    const float *table;
+    int64_t ldt;
+} te_block_attn;
+
+/* encoder_block_attn_fwd: te_encoder_block_fwd with another attention step, for
+ * encoders of local, causal or relative-position attention.  The descriptor's
+ * window and n_attn_items must be 0; its attn_scale applies.  The workspace is
+ * te_encoder_block_workspace(desc, t). */
+te_status te_encoder_block_attn_fwd(const te_block_desc *desc, const te_block_attn *attn, float *x,
+                                    void *a, const int32_t *cu_host, const int32_t *cu_dev,
+                                    int32_t nseq, void *workspace, size_t ws_bytes,
+                                    te_stream stream);
 
 /* Size of the fixed scratch array of te_encoder_block_fwd_static (bytes). */
 #define TE_STATIC_SCRATCH_BYTES ((size_t)32 << 20)

@@ -111,3 +111,11 @@ def test_the_mask_of_the_reference():
     assert see.int().tolist() == [[1, 0, 0, 0, 0, 0], [1, 1, 0, 0, 0, 0], [1, 1, 1, 0, 0, 0], [1, 1, 1, 1, 0, 0],
                                   [1, 1, 0, 1, 1, 0], [1, 1, 0, 0, 1, 1]]
     assert bool(visible(5, -1, -1, 0).all()) and visible(4, 0, 0, 0).int().sum() == 4
+
+
+def test_block_attention_refusals(L):
+    """What is no descriptor's fault is refused too, before anything is launched."""
+    st, msg = _call(L, "te_encoder_block_attn_fwd", None, None, FAKE, FAKE, None, FAKE, 1, FAKE, 0, None)
+    assert st == te.TE_EINVAL and "attention" in msg
+    a = te.block_attn()
+    assert _call(L, "te_encoder_block_attn_fwd", None, ctypes.byref(a), FAKE, FAKE, None, FAKE, 1, FAKE, 0, None)[0] == te.TE_EINVAL

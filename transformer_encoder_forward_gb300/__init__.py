@@ -71,6 +71,10 @@ class te_block_desc(ctypes.Structure):
                 ("prof_events", c_p)]
 
 
+class te_block_attn(ctypes.Structure):
+    _fields_ = [("left", c_i32), ("right", c_i32), ("sinks", c_i32), ("plan", c_p), ("table", c_p), ("ldt", c_i64)]
+
+
 class te_i8_choice(ctypes.Structure):
     _fields_ = [("kernel", c_i32), ("tile", c_i32), ("split", c_i32)]
 
@@ -145,6 +149,8 @@ EXPORTS = {
     "te_encoder_block_workspace": (ctypes.c_size_t, [ctypes.POINTER(te_block_desc), c_i32]),
     "te_encoder_block_fwd": (ctypes.c_int, [ctypes.POINTER(te_block_desc), c_p, c_p, c_p, c_p, c_i32,
                                             c_p, ctypes.c_size_t, c_p]),
+    "te_encoder_block_attn_fwd": (ctypes.c_int, [ctypes.POINTER(te_block_desc), ctypes.POINTER(te_block_attn), c_p,
+                                                 c_p, c_p, c_p, c_i32, c_p, ctypes.c_size_t, c_p]),
     "te_encoder_block_fwd_static": (ctypes.c_int, [ctypes.POINTER(te_block_desc), c_p, c_p, c_p,
                                                    c_p, c_i32, c_p]),
     "te_check": (ctypes.c_int, [c_p]),
@@ -483,6 +489,26 @@ def encoder_block_fwd(desc: te_block_desc, x, a, cu_host, cu_dev, workspace, str
     _ok(lib().te_encoder_block_fwd(ctypes.byref(desc), x.data_ptr(), a.data_ptr(), hp,
                                    cu_dev.data_ptr(), len(arr) - 1, workspace.data_ptr(),
                                    workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def block_attn(left=-1, right=-1, sinks=0, plan=None, table=None) -> te_block_attn:
+    """The attention step of encoder_block_attn_fwd: limits (-1: none), sinks and,
+    with a relpos_plan and its table (f32 [buckets, heads] on the device), the
+    relative position bias.  Keeps plan and table alive."""
+    if (plan is None) != (table is None):
+        raise ValueError("block_attn: a plan and its table go together")
+    a = te_block_attn(left, right, sinks, ctypes.addressof(plan) if plan is not None else None, _ptr(table),
+                      table.stride(0) if table is not None else 0)
+    a.keep = (plan, table)
+    return a
+
+
+def encoder_block_attn_fwd(desc: te_block_desc, attn: te_block_attn, x, a, cu_host, cu_dev, workspace, stream=None):
+    """encoder_block_fwd with the attention step of `attn` (block_attn)."""
+    arr, hp = _host_i32(cu_host)
+    _ok(lib().te_encoder_block_attn_fwd(ctypes.byref(desc), ctypes.byref(attn), x.data_ptr(), a.data_ptr(), hp,
+                                        cu_dev.data_ptr(), len(arr) - 1, workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def encoder_block_fwd_static(desc: te_block_desc, x, a, cu_host, cu_dev, stream=None):

@@ -1065,36 +1065,10 @@ te_status span_fwd(const char *name, const void *qkv, int64_t ld, int32_t q_off,
                    const int32_t *cu_host, const int32_t *cu_dev, int32_t nseq, int32_t nq, int32_t nkv, int32_t hd,
                    int32_t left, int32_t right, int32_t sinks, float scale, const te_relpos *plan, const float *table,
                    int64_t ldt, void *out, int64_t ldo, te_stream stream) {
-    if (!qkv || !out) return fail(TE_EINVAL, "%s: NULL qkv or out", name);
-    if (hd != 64 && hd != 128) return fail(TE_ESHAPE, "%s: hd=%d (64 or 128)", name, hd);
-    if (nq < 1 || nkv < 1 || nq % nkv || nq > 65535)
-        return fail(TE_ESHAPE, "%s: nq_heads=%d nkv_heads=%d (nq %% nkv == 0, at most 65535)", name, nq, nkv);
-    if (left < -1 || right < -1 || sinks < 0)
-        return fail(TE_EINVAL, "%s: left=%d right=%d sinks=%d (limits >= 0 or -1, sinks >= 0)", name, left, right, sinks);
-    // a power of two to either side of which scores in log2 units stay normal numbers
-    if (!(scale >= 0x1p-100f && scale <= 0x1p100f)) return fail(TE_EINVAL, "%s: scale=%g (2^-100 .. 2^100)", name, (double)scale);
-    if (q_off < 0 || k_off < 0 || v_off < 0 || (int64_t)q_off + (int64_t)nq * hd > ld ||
-        (int64_t)k_off + (int64_t)nkv * hd > ld || (int64_t)v_off + (int64_t)nkv * hd > ld)
-        return fail(TE_ESHAPE, "%s: head columns run past ld=%lld", name, (long long)ld);
-    if (ld > 2147483647) return fail(TE_ESHAPE, "%s: ld=%lld", name, (long long)ld);
-    if (ldo < (int64_t)nq * hd || ldo > 2147483647) return fail(TE_ESHAPE, "%s: ldo=%lld, need nq_heads * hd or more", name, (long long)ldo);
-    if (!aligned16(qkv) || !aligned16(out) || ld % 8 || ldo % 8 || q_off % 8 || k_off % 8 || v_off % 8)
-        return fail(TE_EALIGN, "%s: rows and head offsets must be 16-byte aligned", name);
     int32_t total = 0, max_len = 0;
-    te_status st = check_cu(cu_host, cu_dev, nseq, &total, &max_len);
+    te_status st = check_attn_span(name, qkv, ld, q_off, k_off, v_off, cu_host, cu_dev, nseq, nq, nkv, hd, left, right,
+                                   sinks, scale, plan, table, ldt, out, ldo, &total, &max_len);
     if (st != TE_OK) return st;
-    if (max_len > (1 << 29)) return fail(TE_ESHAPE, "%s: a sequence of %d rows", name, max_len);
-    if (plan) {
-        if ((st = check_relpos(plan, name)) != TE_OK) return st;
-        if (!table) return fail(TE_EINVAL, "%s: NULL table", name);
-        if (ldt < nq) return fail(TE_ESHAPE, "%s: ldt=%lld < nq_heads=%d", name, (long long)ldt, nq);
-        if (reinterpret_cast<uintptr_t>(table) & 3) return fail(TE_EALIGN, "%s: the table must be 4-byte aligned", name);
-    }
-    {
-        const uintptr_t a0 = reinterpret_cast<uintptr_t>(qkv), a1 = a0 + (uintptr_t)total * ld * 2;
-        const uintptr_t b0 = reinterpret_cast<uintptr_t>(out), b1 = b0 + (uintptr_t)total * ldo * 2;
-        if (a0 < b1 && b0 < a1) return fail(TE_EINVAL, "%s: out overlaps qkv", name);
-    }
     SpanParams p;
     memset(&p, 0, sizeof(p));
     st = make_map_2d(&p.map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, qkv, (uint64_t)ld, (uint64_t)total, (uint64_t)ld * 2,
@@ -1141,6 +1115,47 @@ te_status span_fwd(const char *name, const void *qkv, int64_t ld, int32_t q_off,
 }
 
 }  // namespace
+
+// Host validation of te_attn_sink_fwd and (plan != NULL) te_attn_relbias_fwd;
+// writes the row count and the longest sequence.
+te_status check_attn_span(const char *name, const void *qkv, int64_t ld, int32_t q_off, int32_t k_off, int32_t v_off,
+                          const int32_t *cu_host, const int32_t *cu_dev, int32_t nseq, int32_t nq, int32_t nkv, int32_t hd,
+                          int32_t left, int32_t right, int32_t sinks, float scale, const te_relpos *plan, const float *table,
+                          int64_t ldt, const void *out, int64_t ldo, int32_t *total_rows, int32_t *longest) {
+    if (!qkv || !out) return fail(TE_EINVAL, "%s: NULL qkv or out", name);
+    if (hd != 64 && hd != 128) return fail(TE_ESHAPE, "%s: hd=%d (64 or 128)", name, hd);
+    if (nq < 1 || nkv < 1 || nq % nkv || nq > 65535)
+        return fail(TE_ESHAPE, "%s: nq_heads=%d nkv_heads=%d (nq %% nkv == 0, at most 65535)", name, nq, nkv);
+    if (left < -1 || right < -1 || sinks < 0)
+        return fail(TE_EINVAL, "%s: left=%d right=%d sinks=%d (limits >= 0 or -1, sinks >= 0)", name, left, right, sinks);
+    // a power of two to either side of which scores in log2 units stay normal numbers
+    if (!(scale >= 0x1p-100f && scale <= 0x1p100f)) return fail(TE_EINVAL, "%s: scale=%g (2^-100 .. 2^100)", name, (double)scale);
+    if (q_off < 0 || k_off < 0 || v_off < 0 || (int64_t)q_off + (int64_t)nq * hd > ld ||
+        (int64_t)k_off + (int64_t)nkv * hd > ld || (int64_t)v_off + (int64_t)nkv * hd > ld)
+        return fail(TE_ESHAPE, "%s: head columns run past ld=%lld", name, (long long)ld);
+    if (ld > 2147483647) return fail(TE_ESHAPE, "%s: ld=%lld", name, (long long)ld);
+    if (ldo < (int64_t)nq * hd || ldo > 2147483647) return fail(TE_ESHAPE, "%s: ldo=%lld, need nq_heads * hd or more", name, (long long)ldo);
+    if (!aligned16(qkv) || !aligned16(out) || ld % 8 || ldo % 8 || q_off % 8 || k_off % 8 || v_off % 8)
+        return fail(TE_EALIGN, "%s: rows and head offsets must be 16-byte aligned", name);
+    int32_t total = 0, max_len = 0;
+    te_status st = check_cu(cu_host, cu_dev, nseq, &total, &max_len);
+    if (st != TE_OK) return st;
+    if (max_len > (1 << 29)) return fail(TE_ESHAPE, "%s: a sequence of %d rows", name, max_len);
+    if (plan) {
+        if ((st = check_relpos(plan, name)) != TE_OK) return st;
+        if (!table) return fail(TE_EINVAL, "%s: NULL table", name);
+        if (ldt < nq) return fail(TE_ESHAPE, "%s: ldt=%lld < nq_heads=%d", name, (long long)ldt, nq);
+        if (reinterpret_cast<uintptr_t>(table) & 3) return fail(TE_EALIGN, "%s: the table must be 4-byte aligned", name);
+    }
+    {
+        const uintptr_t a0 = reinterpret_cast<uintptr_t>(qkv), a1 = a0 + (uintptr_t)total * ld * 2;
+        const uintptr_t b0 = reinterpret_cast<uintptr_t>(out), b1 = b0 + (uintptr_t)total * ldo * 2;
+        if (a0 < b1 && b0 < a1) return fail(TE_EINVAL, "%s: out overlaps qkv", name);
+    }
+    *total_rows = total;
+    *longest = max_len;
+    return TE_OK;
+}
 
 int read_clear_attn_span_error() {
     int v = 0;

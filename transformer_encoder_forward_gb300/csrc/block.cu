@@ -163,10 +163,10 @@ extern "C" size_t te_encoder_block_workspace(const te_block_desc *desc, int32_t 
     return ws_layout(*desc, t).total;
 }
 
-extern "C" te_status te_encoder_block_fwd(const te_block_desc *desc, float *x, void *a,
-                                          const int32_t *cu_host, const int32_t *cu_dev,
-                                          int32_t nseq, void *workspace, size_t ws_bytes,
-                                          te_stream stream) {
+// The block; at != NULL: with its attention step instead of the descriptor's.
+static te_status block_fwd(const te_block_desc *desc, const te_block_attn *at, float *x, void *a,
+                           const int32_t *cu_host, const int32_t *cu_dev, int32_t nseq, void *workspace,
+                           size_t ws_bytes, te_stream stream) {
     te_status st = check_block_desc(desc);
     if (st != TE_OK) return st;
     const te_block_desc &d = *desc;
@@ -210,6 +210,15 @@ extern "C" te_status te_encoder_block_fwd(const te_block_desc *desc, float *x, v
     float *tmp = reinterpret_cast<float *>(ws + L.tmp);
     __nv_bfloat16 *m = reinterpret_cast<__nv_bfloat16 *>(ws + L.m);
     const bool plain = d.resid_form == TE_RESID_PLAIN;
+    if (at) {
+        if (d.window != 0 || d.n_attn_items != 0)
+            return fail(TE_EINVAL, "block_attn: the descriptor's window and attention items must be 0");
+        int32_t rows, longest;
+        if ((st = check_attn_span("block_attn", qkv, ldqkv, 0, qw, qw + kw, cu_host, cu_dev, nseq, H, KV, hd, at->left,
+                                  at->right, at->sinks, d.attn_scale, at->plan, at->table, at->ldt, o, qw, &rows,
+                                  &longest)) != TE_OK)
+            return st;
+    }
 
     // 1. q|k|v projections, one grouped launch (z = 3)
     te_q8_item it[3] = {};
@@ -228,7 +237,13 @@ extern "C" te_status te_encoder_block_fwd(const te_block_desc *desc, float *x, v
     }
     if ((st = mark(2)) != TE_OK) return st;
     // 3. attention: per sequence, or per two-range item
-    if (d.n_attn_items > 0)
+    if (at && at->plan)
+        st = te_attn_relbias_fwd(qkv, ldqkv, 0, qw, qw + kw, cu_host, cu_dev, nseq, H, KV, hd, at->left, at->right,
+                                 at->sinks, d.attn_scale, at->plan, at->table, at->ldt, o, qw, stream);
+    else if (at)
+        st = te_attn_sink_fwd(qkv, ldqkv, 0, qw, qw + kw, cu_host, cu_dev, nseq, H, KV, hd, at->left, at->right,
+                              at->sinks, d.attn_scale, o, qw, stream);
+    else if (d.n_attn_items > 0)
         st = te_attn_items_fwd(qkv, ldqkv, 0, qw, qw + kw, d.attn_items_host, d.attn_items_dev,
                                d.n_attn_items, t, H, KV, hd, d.window, d.attn_scale, o, qw, stream);
     else
@@ -300,4 +315,18 @@ extern "C" te_status te_encoder_block_fwd(const te_block_desc *desc, float *x, v
                              d.next_norm_w ? a : nullptr, TE_BF16, t, D, stream);
     }
     return st != TE_OK ? st : mark(8);
+}
+
+extern "C" te_status te_encoder_block_fwd(const te_block_desc *desc, float *x, void *a,
+                                          const int32_t *cu_host, const int32_t *cu_dev,
+                                          int32_t nseq, void *workspace, size_t ws_bytes,
+                                          te_stream stream) {
+    return block_fwd(desc, nullptr, x, a, cu_host, cu_dev, nseq, workspace, ws_bytes, stream);
+}
+
+extern "C" te_status te_encoder_block_attn_fwd(const te_block_desc *desc, const te_block_attn *attn, float *x, void *a,
+                                               const int32_t *cu_host, const int32_t *cu_dev, int32_t nseq,
+                                               void *workspace, size_t ws_bytes, te_stream stream) {
+    if (!attn) return fail(TE_EINVAL, "block_attn: NULL attention");
+    return block_fwd(desc, attn, x, a, cu_host, cu_dev, nseq, workspace, ws_bytes, stream);
 }

@@ -29,6 +29,14 @@ te_status check_cu(const int32_t *cu_host, const int32_t *cu_dev, int32_t nseq,
 // Host validation of an encoder block descriptor (block.cu).
 te_status check_block_desc(const te_block_desc *d);
 
+// Host validation of attention with sinks and, plan != NULL, a relative position
+// bias (attn_span.cu); writes the row count and the longest sequence.
+te_status check_attn_span(const char *name, const void *qkv, int64_t ld, int32_t q_off, int32_t k_off, int32_t v_off,
+                          const int32_t *cu_host, const int32_t *cu_dev, int32_t nseq, int32_t nq, int32_t nkv, int32_t hd,
+                          int32_t left, int32_t right, int32_t sinks, float scale, const te_relpos *plan,
+                          const float *table, int64_t ldt, const void *out, int64_t ldo, int32_t *total_rows,
+                          int32_t *longest);
+
 // Encodes a 2-D tiled TMA descriptor (row-major, `inner` elements per row,
 // `outer` rows, `row_bytes` apart) for a box of box_inner x box_outer.
 te_status make_map_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner,

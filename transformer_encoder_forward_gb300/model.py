@@ -15,8 +15,9 @@ from typing import List, Optional
 import numpy as np
 
 from . import (TE_ACT_GELU_TANH, TE_ACT_SILU, TE_NORM_LN, TE_NORM_RMS, TE_RESID_PLAIN,
-               TE_RESID_SANDWICH, block_workspace, cast_bf16, encoder_block_fwd, pool_mean,
-               q4_0_unpack, q8_0_unpack, q8w, rownorm, rownorm_mod, te_block_desc)
+               TE_RESID_SANDWICH, block_attn, block_workspace, cast_bf16, encoder_block_attn_fwd,
+               encoder_block_fwd, pool_mean, q4_0_unpack, q8_0_unpack, q8w, relpos_plan, rownorm, rownorm_mod,
+               te_block_desc)
 
 
 def _dev(a, device, dtype=None):
@@ -64,10 +65,15 @@ class EncoderStack:
 
     def __init__(self, cfg, layers: List[dict], lens, tables: dict,
                  final_norm: Optional[np.ndarray] = None, device="cuda", ple: Optional[dict] = None,
-                 items: Optional[np.ndarray] = None):
+                 items: Optional[np.ndarray] = None, attn=None):
         """items: two-range attention items, int32 [n, 4] = (off1, len1,
         off2, len2) covering every row once (the CFG pair's batch-2 program,
-        zimage.rs); None: attention per sequence of ``lens``."""
+        zimage.rs); None: attention per sequence of ``lens``.
+        attn: the layers' attention steps where they are not the config's: a dict
+        (every layer) or a list of one a layer, each a dict or None (the
+        config's).  A dict may hold left, right (limits; -1 or absent: none),
+        sinks, and relpos = (buckets, max_distance, two_sided) with table, f32
+        [buckets, heads] (layers that share a dict share the device's copy)."""
         import torch
         self.cfg = cfg
         self.device = torch.device(device)
@@ -97,9 +103,34 @@ class EncoderStack:
         if items is not None:
             self.items_host = np.ascontiguousarray(np.asarray(items, dtype=np.int32).reshape(-1, 4))
             self.items_dev = torch.from_numpy(self.items_host).to(self.device)
+        self.attn = self._attn(attn)
         self.descs = [self._desc(i) for i in range(len(self.layers))]
         ws = max(block_workspace(d, self.T) for d in self.descs)
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=self.device)
+
+    def _attn(self, attn):
+        """One te_block_attn a layer (None: the config's attention)."""
+        if attn is None or isinstance(attn, dict):
+            attn = [attn] * len(self.layers)
+        if len(attn) != len(self.layers):
+            raise ValueError("attn: one entry a layer")
+        if self.items_host is not None and any(a is not None for a in attn):
+            raise ValueError("attn: not together with attention items")
+        made = {}
+        for a in attn:
+            if a is None or id(a) in made:
+                continue
+            bad = set(a) - {"left", "right", "sinks", "relpos", "table"}
+            if bad or ("relpos" in a) != ("table" in a):
+                raise ValueError(f"attn: unknown keys {sorted(bad)}" if bad else "attn: relpos and table go together")
+            plan = table = None
+            if "relpos" in a:
+                plan = relpos_plan(*a["relpos"])
+                if np.shape(a["table"]) != (plan.buckets, self.cfg.heads):
+                    raise ValueError(f"attn: table {np.shape(a['table'])}, not {(plan.buckets, self.cfg.heads)}")
+                table = _dev(np.asarray(a["table"], dtype=np.float32), self.device)
+            made[id(a)] = block_attn(a.get("left", -1), a.get("right", -1), a.get("sinks", 0), plan, table)
+        return [None if a is None else made[id(a)] for a in attn]
 
     def _desc(self, i: int) -> te_block_desc:
         cfg, L = self.cfg, self.layers[i]
@@ -111,7 +142,7 @@ class EncoderStack:
         d.resid_form = TE_RESID_SANDWICH if cfg.form == "sandwich" else TE_RESID_PLAIN
         d.act = TE_ACT_SILU if cfg.act == "silu" else TE_ACT_GELU_TANH
         d.gated = 1 if cfg.gated else 0
-        d.window = cfg.window_of(i)
+        d.window = cfg.window_of(i) if self.attn[i] is None else 0
         d.eps, d.attn_scale, d.post, d.q_mul = cfg.eps, cfg.scale, cfg.post, 1.0
         for key in ("wq", "wk", "wv", "wo", "wg", "wd"):
             setattr(d, key, q8w(*L.t[key]))
@@ -168,8 +199,12 @@ class EncoderStack:
         self.input_norm(x, a, stream)
         n = len(self.layers) if layers is None else layers
         for i in range(n):
-            encoder_block_fwd(self.descs[i], x, a, self.cu_host, self.cu_dev, self.workspace,
-                              stream=stream)
+            if self.attn[i] is not None:
+                encoder_block_attn_fwd(self.descs[i], self.attn[i], x, a, self.cu_host, self.cu_dev, self.workspace,
+                                       stream=stream)
+            else:
+                encoder_block_fwd(self.descs[i], x, a, self.cu_host, self.cu_dev, self.workspace,
+                                  stream=stream)
         if out is not None and self.cfg.pool:
             pool_mean(x, self.cu_host, self.cu_dev, self.final_norm, self.cfg.eps, out,
                       stream=stream)
