@@ -349,10 +349,10 @@ __device__ __forceinline__ Item item_of(const SpanParams &p, int b, int lane) {
         seq = lo;
         qblk = slot - (p.cu[seq] / QB + seq);
     }
-    const int off = p.cu[seq], len = p.cu[seq + 1] - off, q0 = qblk * QB;
-    // else: nothing to do, or a device table that is not the host's
-    const bool live = off >= 0 && len >= 1 && (long long)off + len <= p.total && qblk >= 0 && q0 < len;
-    return {off, live ? len : 0, q0, h};
+    // nothing to do, or a device table that is not the host's: an item without rows
+    const long long off = p.cu[seq], len = p.cu[seq + 1] - off, q0 = (long long)qblk * QB;
+    const bool live = off >= 0 && len >= 1 && off + len <= p.total && q0 >= 0 && q0 < len;
+    return {(int)off, live ? (int)len : 0, (int)q0, h};
 }
 
 // Takes over the place of a CTA of this grid that has not started yet; the
