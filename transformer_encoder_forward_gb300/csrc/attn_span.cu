@@ -61,6 +61,7 @@ struct SpanParams {
     int nwork;                 // > 0: work[i] = (sequence << 16) | query block, longest first
     int nq, hgroup;            // heads, and heads per group of the CTA order
     uint32_t work[MAX_WORK];
+    int starts[MAX_WORK + 1];  // with a list: the sequences' offsets (the device's array is not read)
     long long ld, ldo;
     int q_off, k_off, v_off, group;
     int left, right, sinks;    // limits clipped to the longest sequence
@@ -319,6 +320,7 @@ struct Item {
 template <int QB>
 __device__ __forceinline__ Item item_of(const SpanParams &p, int b, int lane) {
     int seq, qblk, h;
+    long long off, len;
     if (p.nwork) {
         // CTAs take the heads in groups of hgroup: within a group, work items in
         // list order (most keys first), the group's heads fastest
@@ -332,6 +334,8 @@ __device__ __forceinline__ Item item_of(const SpanParams &p, int b, int lane) {
         seq = (int)(wv >> 16);
         qblk = (int)(wv & 0xFFFFu);
         h = h0 + (r - wi * gn);
+        off = p.starts[seq];
+        len = p.starts[seq + 1] - off;
     } else {
         // many blocks: sequence s has the slots from cu[s] / QB + s on, at least
         // as many as it has query blocks
@@ -347,10 +351,12 @@ __device__ __forceinline__ Item item_of(const SpanParams &p, int b, int lane) {
             hi = lo + step < hi ? lo + step : hi;
         }
         seq = lo;
-        qblk = slot - (p.cu[seq] / QB + seq);
+        off = p.cu[seq];
+        len = p.cu[seq + 1] - off;
+        qblk = slot - (int)(off / QB + seq);
     }
     // nothing to do, or a device table that is not the host's: an item without rows
-    const long long off = p.cu[seq], len = p.cu[seq + 1] - off, q0 = (long long)qblk * QB;
+    const long long q0 = (long long)qblk * QB;
     const bool live = off >= 0 && len >= 1 && off + len <= p.total && q0 >= 0 && q0 < len;
     return {(int)off, live ? (int)len : 0, (int)q0, h};
 }
@@ -428,9 +434,11 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // from here on global memory is touched
-    prior_wait();
-    next_go();
+    // from here on global memory is touched, by the loading warp once it knows its first item
+    if (warp != L::TMA_WARP) {
+        prior_wait();
+        next_go();
+    }
     const uint32_t tbase = tmem_slot[0];
     bool ok = true;
     // waits of a whole warp; false: given up
@@ -506,10 +514,11 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             // (len 0: no more) as the CTA's item number it.
             auto publish = [&](int it, Item &r) {
                 r = {0, 0, 0, 0};
+                if (!p.nwork) prior_wait();              // the offsets come from global memory
                 while (next >= 0 && ok) {
                     r = item_of<QB>(p, next, lane);
-                    ask();
                     if (r.len > 0) break;
+                    ask();
                     next = answer();
                 }
                 if (!ok || !wait(L::BAR_RECE + (it & 3), (it >> 2) ^ 1)) { ok = false; return; }
@@ -524,14 +533,14 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 __syncwarp();
             };
             // Spreads the head's bias over the distances, in log2 units, ahead of its first item.
-            auto spread_bias = [&](int h) {
+            auto spread_bias = [&](int h, float column) {
                 if (h == head) return;
                 head = h;
                 const int buf = built & 1;
                 if (!wait(L::BAR_BE + buf, (built >> 1) ^ 1)) { ok = false; return; }
                 for (int b = lane; b < nb; b += 32) {
                     // a finite bias stays finite (the type's lowest value still masks softly)
-                    const float v = p.table[(long long)b * p.ldt + h], v2 = v * 1.4426950408889634f;
+                    const float v = b < 32 ? column : p.table[(long long)b * p.ldt + h], v2 = v * 1.4426950408889634f;
                     tab[b] = fabsf(v) <= FLT_MAX ? fminf(fmaxf(v2, -FLT_MAX), FLT_MAX) : v;
                 }
                 __syncwarp();
@@ -548,6 +557,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             // head's bias spread behind the load that follows.
             Item r = {0, 0, 0, 0}, r2 = r;
             int to_spread = -1;
+            float column = 0.f;                          // its first 32 buckets, loaded ahead
             for (int it = -1; ok && (it < 0 || r.len > 0); ++it, r = r2) {
                 const int g = r.h / p.group;
                 KeyTiles tiles = {0, 0, 0}, kw[NT];
@@ -560,7 +570,14 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                     if (j == (n < R ? n : R)) {
                         if (it >= 0) next = answer();
                         if (ok) publish(it + 1, r2);
-                        if (r2.len > 0) to_spread = r2.h;
+                        if (it < 0) {
+                            prior_wait();
+                            next_go();
+                        }
+                        if (BIAS && r2.len > 0) {
+                            to_spread = r2.h;
+                            column = lane < nb ? p.table[(long long)lane * p.ldt + to_spread] : 0.f;
+                        }
                     }
                     if (!ok || j >= n) break;
                     const int t = tiles.tile(j);
@@ -604,8 +621,9 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                     if (idle) arrive_n(bar(L::BAR_KVE + kv.at), idle, e);
                     kv.step();
                     ++kvn;
+                    if (j == 0) ask();
                     if (BIAS && to_spread >= 0) {
-                        spread_bias(to_spread);
+                        spread_bias(to_spread, column);
                         to_spread = -1;
                     }
                 }
@@ -1103,6 +1121,7 @@ te_status span_fwd(const char *name, const void *qkv, int64_t ld, int32_t q_off,
         for (int b = 0; b < p.side; ++b) p.first[b] = (uint16_t)plan->first[b];
     }
     p.nwork = build_work(cu_host, nseq, p, (hd == 64 ? SLayout<64>::NT : SLayout<128>::NT) * BQ, p.work);
+    if (p.nwork) memcpy(p.starts, cu_host, sizeof(int32_t) * (nseq + 1));   // (no more sequences than blocks)
     // heads per group: all when every head's K and V fit in KV_ALL_BYTES
     // together, else the kv heads whose K and V make about KV_GROUP_BYTES
     const int64_t kv_head = (int64_t)total * hd * 4;
