@@ -112,7 +112,8 @@ struct SLayout {
     static constexpr int BAR_CLC = BAR_RECE + 4;         // the next CTA's place taken over, or not
     static constexpr int BAR_BF = BAR_CLC + 1;           // [2] bias spread
     static constexpr int BAR_BE = BAR_BF + 2;            // [2] bias no longer read
-    static constexpr int BAR_FIN = BAR_BE + 2;           // [NT] every MMA and commit of an MMA warp is done
+    static constexpr int BAR_B0 = BAR_BE + 2;            // the first bias spread, by the softmax warps
+    static constexpr int BAR_FIN = BAR_B0 + 1;           // [NT] every MMA and commit of an MMA warp is done
     static constexpr int NBAR = BAR_FIN + NT;
     static constexpr int REC_OFF = (BAR_OFF + 8 * NBAR + 15) / 16 * 16;   // 4 records of 16 bytes, the taken place
     static constexpr int SLOT_OFF = REC_OFF + 80;        // TMEM base
@@ -148,9 +149,10 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
-// The bias of distance d (already clipped to the reach), in the table column col.
-__device__ __forceinline__ float bias_of(const SpanParams &p, const float *col, int d) {
-    const int a = p.two_sided ? (d < 0 ? -d : d) : (d < 0 ? -d : 0);
+// The bucket of distance d, which counts as the reach where it is further.
+__device__ __forceinline__ int bucket_of(const SpanParams &p, int d) {
+    int a = p.two_sided ? (d < 0 ? -d : d) : (d < 0 ? -d : 0);
+    if (a > p.reach) a = p.reach;
     int b = a;
     if (a >= p.exact) {
         // within one of the bucket by the f32 logarithm, then by the exact borders
@@ -159,7 +161,13 @@ __device__ __forceinline__ float bias_of(const SpanParams &p, const float *col, 
         if (b > p.exact && a < p.first[b]) --b;
         else if (b + 1 < p.side && a >= p.first[b + 1]) ++b;
     }
-    return col[p.two_sided && d > 0 ? b + p.side : b];
+    return p.two_sided && d > 0 ? b + p.side : b;
+}
+
+// A bias in log2 units; a finite one stays finite (the type's lowest value still masks softly).
+__device__ __forceinline__ float bias_log2(float v) {
+    const float v2 = v * 1.4426950408889634f;
+    return fabsf(v) <= FLT_MAX ? fminf(fmaxf(v2, -FLT_MAX), FLT_MAX) : v;
 }
 
 // A whole warp waits for a phase, for 200 ms at most (then false); the loop out of
@@ -428,6 +436,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             mbar_init(bar(L::BAR_BE + i), L::SOFTMAX_WARPS);
         }
         mbar_init(bar(L::BAR_CLC), 1);
+        mbar_init(bar(L::BAR_B0), L::SOFTMAX_WARPS);
         fence_mbar_init();
     }
     if (warp == L::MMA_WARP) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -490,7 +499,7 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
             next = __shfl_sync(0xFFFFFFFFu, next, 0);
             Ring kv = {0, 0};
             int kvn = 0;                                 // pairs of K and V issued in all
-            int head = -1, built = 0;                    // the head whose bias was spread last, biases spread
+            int head = -1, built = 1;                    // the head whose bias was spread last, biases spread
             int asked = 0;                               // places asked for
             uint32_t qn[NT];                             // Q loads of each query tile
 #pragma unroll
@@ -532,22 +541,18 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                 }
                 __syncwarp();
             };
-            // Spreads the head's bias over the distances, in log2 units, ahead of its first item.
+            // Spreads a head's bias over the distances, in log2 units, ahead of its first item.
             auto spread_bias = [&](int h, float column) {
                 if (h == head) return;
                 head = h;
                 const int buf = built & 1;
                 if (!wait(L::BAR_BE + buf, (built >> 1) ^ 1)) { ok = false; return; }
-                for (int b = lane; b < nb; b += 32) {
-                    // a finite bias stays finite (the type's lowest value still masks softly)
-                    const float v = b < 32 ? column : p.table[(long long)b * p.ldt + h], v2 = v * 1.4426950408889634f;
-                    tab[b] = fabsf(v) <= FLT_MAX ? fminf(fmaxf(v2, -FLT_MAX), FLT_MAX) : v;
-                }
+                for (int b = lane; b < nb; b += 32)
+                    tab[b] = bias_log2(b < 32 ? column : p.table[(long long)b * p.ldt + h]);
                 __syncwarp();
                 float *spread = spread_of(buf);
 #pragma unroll 4
-                for (int d = lane - width; d <= width; d += 32)
-                    spread[d] = bias_of(p, tab, d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d));
+                for (int d = lane - width; d <= width; d += 32) spread[d] = tab[bucket_of(p, d)];
                 __syncwarp();
                 arrive_if(bar(L::BAR_BF + buf), lane == 0);
                 ++built;
@@ -574,7 +579,8 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                             prior_wait();
                             next_go();
                         }
-                        if (BIAS && r2.len > 0) {
+                        if (BIAS && it < 0) head = r2.h;     // the softmax warps spread the first themselves
+                        if (BIAS && it >= 0 && r2.len > 0) {
                             to_spread = r2.h;
                             column = lane < nb ? p.table[(long long)lane * p.ldt + to_spread] : 0.f;
                         }
@@ -745,8 +751,18 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
                     // let go of the last head's bias, take this one's
                     if (head >= 0 && lane == 0) mbar_arrive(bar(L::BAR_BE + ((built - 1) & 1)));
                     head = r.h;
-                    if (!(ok = wait(L::BAR_BF + (built & 1), built >> 1))) break;
                     bias = spread_of(built & 1);
+                    if (built == 0) {
+                        // the CTA's first: by all softmax warps at once, while Q and K are on their way
+                        prior_wait();
+                        for (int d = (int)threadIdx.x - width; d <= width; d += 32 * L::SOFTMAX_WARPS)
+                            spread_of(0)[d] = bias_log2(p.table[(long long)bucket_of(p, d) * p.ldt + head]);
+                        __syncwarp();
+                        arrive_if(bar(L::BAR_B0), lane == 0);
+                        if (!(ok = wait(L::BAR_B0, 0))) break;
+                    } else if (!(ok = wait(L::BAR_BF + (built & 1), (built - 1) >> 1))) {
+                        break;
+                    }
                     ++built;
                 }
             }
