@@ -865,8 +865,9 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
 #pragma unroll
                 for (int i = 8; i < 32; ++i) m8[i & 7] = fmax3(m8[i & 7], __uint_as_float(va[i]), __uint_as_float(vb[i]));
                 const float mx = fmaf(fmaxf(fmax3(fmax3(m8[0], m8[1], m8[2]), m8[3], m8[4]), fmax3(m8[5], m8[6], m8[7])), cs, cb);
-                // it moves when a row grew by more than 2^8
-                const bool resc = mx > m_used + 8.f;
+                // it moves when a row grew by more than 2^20 (P, sums and O have f32's exponents to spare;
+                // moves cost a pass over O: by 2^8 grouped causal heads take 138 us instead of 131)
+                const bool resc = mx > m_used + 20.f;
                 const uint64_t c2 = f2_pack(cs, cs);
                 uint64_t nm2 = f2_pack(cb + nm0, cb + nm0);
                 uint64_t rt[2] = {r2[0], r2[1]};
