@@ -89,6 +89,21 @@ def test_relative_bias(rel, lens, hd, nq, nkv):
     compare(f"bias {lens} {rel} {hd}", out, ref, mag)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("reach", [960, 970, 980, 990, 1000, 1024, 2048])
+def test_bias_of_a_wide_reach(reach, hd):
+    """Spread biases that leave shared memory for more, and for fewer, keys and values in flight."""
+    import torch
+    ln, nq, nkv = [2200, 1100, 700], 8, 4
+    rel = (512, reach, True)
+    qkv = panel(sum(ln), (nq + 2 * nkv) * hd, 20)
+    table = 3 * torch.randn(rel[0], nq, device="cuda", generator=torch.Generator(device="cuda").manual_seed(21))
+    span = (-1, -1, 0)
+    ref, mag = attention(qkv, ln, nq, nkv, hd, *span, hd ** -0.5, table=table, rel=rel)
+    out = call(qkv, ln, nq, nkv, hd, *span, hd ** -0.5, table=table, rel=rel)
+    compare(f"bias of reach {reach} {hd}", out, ref, mag)
+
+
 @pytest.mark.parametrize("hd,nq,nkv", HEADS)
 @pytest.mark.parametrize("span", SPANS, ids=lambda s: "l%d_r%d_s%d" % s)
 @pytest.mark.parametrize("rel", [(32, 128, True), (32, 128, False), (64, 300, True)], ids=lambda r: "b%d_d%d_%d" % r)

@@ -45,6 +45,7 @@ namespace {
 constexpr int BQ = 128;     // queries per tile (= TMEM lanes)
 constexpr int BKV = 64;     // keys per tile
 constexpr int MAX_WORK = 640;   // work list entries carried in the launch parameters
+constexpr int MAX_SMEM = 227 * 1024;
 constexpr int PAD = 96;     // distances past `reach` that 32 rows and 64 keys near it can still touch (94)
 // as in attn.cu: K and V bytes that the CTA order treats as one group of heads
 constexpr long long KV_ALL_BYTES = 48ll << 20;
@@ -75,14 +76,14 @@ struct SpanParams {
 };
 
 // Several query tiles a CTA, four softmax warps each, and four warps that feed them.
-template <int HD>
+template <int HD, int RING = HD == 64 ? 7 : 3>
 struct SLayout {
     static constexpr int NB = HD / 64;              // 64-column boxes per tile row
     static constexpr int NT = HD == 64 ? 3 : 2;     // query tiles
     // pairs of a K and a V tile in flight: as many as fit.  Where there is a window the
     // first query tile is done with an item's keys while the last still needs
     // some; the ring lets it go on to the next item.
-    static constexpr int R = HD == 64 ? 7 : 3;
+    static constexpr int R = RING;
     static constexpr int QTILE = BQ * HD * 2, TILE = BKV * HD * 2;
     static constexpr int QBOX = BQ * 128, BOX = BKV * 128;   // 64 columns of them
     static constexpr int Q_OFF = 0;                 // Q[NT]
@@ -121,9 +122,9 @@ struct SLayout {
     // TMEM columns of a query tile: S (64 f32), P (64 bf16), O (HD f32)
     static constexpr int P_COL = 64, O_COL = 96, TILE_COLS = 96 + HD;
     static_assert(NT * TILE_COLS <= 512, "TMEM budget");
-    // the widest bias: every distance to TE_RELPOS_MAX_DISTANCE to either side
-    static_assert(TAB_OFF + 4 * (TE_RELPOS_MAX_BUCKETS + 2 * (2 * (TE_RELPOS_MAX_DISTANCE + PAD) + 1)) + 1024 <= 227 * 1024,
-                  "shared memory per CTA");
+    // shared memory besides the bias: nb of the table's column and two of 2 (reach + PAD) + 1 distances
+    static constexpr int bytes(int nb, int reach) { return TAB_OFF + 1024 + 4 * (nb + 2 * (2 * (reach + PAD) + 1)); }
+    static_assert(RING > (HD == 64 ? 7 : 3) || bytes(TE_RELPOS_MAX_BUCKETS, TE_RELPOS_MAX_DISTANCE) <= MAX_SMEM, "shared memory per CTA");
 };
 
 // Key tiles that rows [r0, r1] of a sequence of `len` see: tiles [0, sink) and
@@ -395,9 +396,9 @@ __device__ __forceinline__ int taken(uint32_t src) {
     return got ? (int)x : -1;
 }
 
-template <int HD, bool BIAS>
-__global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(const __grid_constant__ SpanParams p) {
-    using L = SLayout<HD>;
+template <int HD, bool BIAS, int RING>
+__global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kernel(const __grid_constant__ SpanParams p) {
+    using L = SLayout<HD, RING>;
     constexpr int NT = L::NT, QB = NT * BQ, R = L::R;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -1001,25 +1002,36 @@ __global__ void __launch_bounds__(SLayout<HD>::NTHREADS, 1) attn_span_kernel(con
     }
 }
 
-template <int HD, bool BIAS>
+template <int HD, bool BIAS, int RING>
 te_status launch(const SpanParams &p, cudaStream_t stream) {
-    using L = SLayout<HD>;
-    constexpr int most = BIAS ? 227 * 1024 : L::TAB_OFF + 1024;
-    const int nb = p.two_sided ? 2 * p.side : p.side;
-    const int smem = L::TAB_OFF + 1024 + (BIAS ? 4 * (nb + 2 * (2 * (p.reach + PAD) + 1)) : 0);
+    using L = SLayout<HD, RING>;
+    constexpr int most = BIAS ? MAX_SMEM : L::TAB_OFF + 1024;
+    const int smem = BIAS ? L::bytes(p.two_sided ? 2 * p.side : p.side, p.reach) : most;
     static std::atomic<bool> ready[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess || dev < 0 || dev >= 64) return cuda_fail(e, "attn: device");
     if (!ready[dev]) {
-        e = cudaFuncSetAttribute(attn_span_kernel<HD, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        e = cudaFuncSetAttribute(attn_span_kernel<HD, BIAS, RING>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return cuda_fail(e, "attn: set shared memory size");
         ready[dev] = true;
     }
     const int64_t slots = p.nwork ? p.nwork : (int64_t)p.total / (L::NT * BQ) + p.nseq;
     if (slots * p.nq > 2147483647) return fail(TE_ESHAPE, "attn: too many query blocks and heads");
-    e = launch_close(attn_span_kernel<HD, BIAS>, dim3((unsigned)(slots * p.nq)), L::NTHREADS, smem, stream, 1, p);
+    e = launch_close(attn_span_kernel<HD, BIAS, RING>, dim3((unsigned)(slots * p.nq)), L::NTHREADS, smem, stream, 1, p);
     return e == cudaSuccess ? TE_OK : cuda_fail(e, "attn launch");
+}
+
+// The deeper ring wherever the bias leaves room for it: with 4 pairs of K and V instead
+// of 3 (hd 128) two images take 417 us instead of 423, with sinks 206 instead of 212; at hd 64 9
+// instead of 7 change nothing.
+template <int HD>
+te_status launch(const SpanParams &p, const te_relpos *plan, cudaStream_t stream) {
+    constexpr int DEEP = HD == 64 ? 7 : 4, WIDE = HD == 64 ? 7 : 3;
+    if (!plan) return launch<HD, false, DEEP>(p, stream);
+    if (SLayout<HD, DEEP>::bytes(p.two_sided ? 2 * p.side : p.side, p.reach) <= MAX_SMEM)
+        return launch<HD, true, DEEP>(p, stream);
+    return launch<HD, true, WIDE>(p, stream);
 }
 
 // --------------------------------------------- buckets of relative positions
@@ -1146,8 +1158,7 @@ te_status span_fwd(const char *name, const void *qkv, int64_t ld, int32_t q_off,
     if (kv_head * nkv > KV_ALL_BYTES) hg = std::min<int64_t>(nq, std::max<int64_t>(1, KV_GROUP_BYTES / kv_head) * p.group);
     p.hgroup = (int)hg;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (hd == 64) return plan ? launch<64, true>(p, s) : launch<64, false>(p, s);
-    return plan ? launch<128, true>(p, s) : launch<128, false>(p, s);
+    return hd == 64 ? launch<64>(p, plan, s) : launch<128>(p, plan, s);
 }
 
 }  // namespace
