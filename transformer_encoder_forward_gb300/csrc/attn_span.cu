@@ -6,28 +6,67 @@
 // over the keys j of i's own sequence with
 //     j <= i + right  and  (j >= i - left  or  j < sinks).
 //
-// The kernel is the flash form of attn.cu (128-query tiles, 128-key tiles, S
-// and O in TMEM, one query row a softmax thread, the maximum moved lazily);
-// what differs is the list of key tiles, the mask and the bias:
+// One pass over the keys: with m a reference that is moved to the row's maximum
+// when there was none, or when the maximum grew by more than 2^20, P = 2^(s - m),
+// l = sum P and O = P V are kept in f32 (P itself rounds to bf16, as the operand
+// of its product; l adds the P before they round), and o = O / l at the end.
+//
+// What bounds it.  A key costs 4 hd multiply-adds on the tensor core and one
+// exponential; bytes are few (q, k, v read once, o written: 30 % of the copy rate
+// where windows are short, 9 % where they are not).  A step of 64 keys and all
+// query tiles of a CTA takes the tensor core 1200 (hd 64, 3 tiles) and 1250 (hd
+// 128, 2 tiles) clocks; alone, the softmax takes 1286 and 993 for it.  Both run
+// at once and take 1600 to 1750 together: two pipes that wait on one another
+// through barriers of about 100 clocks.  Without a window, 4 x 4096 rows with 12
+// heads of 64 run at 890 TFLOP/s and 2 x 4096 with 30 heads of 128 at 1480; with
+// one, partly seen tiles and the masks and biases of their pairs cost the rest.
+//
+// The form, and why:
+//   * a CTA holds an SM and NT query tiles (128 rows, a row a softmax thread), as
+//     many as TMEM, registers and shared memory hold: 3 at hd 64, 2 at hd 128.
+//     The tiles share the K and V that are loaded, and one's softmax runs while
+//     another's products do.  Key tiles are 64 keys: a row's scores of a tile are
+//     64 registers, and a window is covered with less beside it than by 128
+//     (two images with sinks: 268 us by 128, 222 by 64);
+//   * each query tile has a warp that issues its products, a further warp
+//     schedules, loads and spreads biases.  S of the next key tile is issued once
+//     the softmax has this one's in registers; P goes to TMEM, half at a time;
+//   * a CTA that is done takes over the place of one that has not started
+//     (cluster launch control), so that the next item's loads and first products
+//     run under the last one's softmax and stores.  Items with the most keys go
+//     first (up to MAX_WORK blocks; beyond that a CTA finds its block by a search
+//     in the device's offsets).  Smaller items at the end would even out the last
+//     turn, and cost what they gain: fewer query tiles in a step take longer each;
 //   * key tiles: those that hold one of the first `sinks` keys, then those of
-//     the window of the CTA's queries.  With two query tiles a CTA (hd = 128)
-//     each tile takes part only in the key tiles that its own rows see: its S
-//     and PV are not issued for the others and its softmax warps skip them;
-//   * mask: a row's visible keys of a tile are four 32-bit words (a bit below
+//     the window of the item's queries; a query tile takes part only in those
+//     that its own rows see;
+//   * mask: a row's visible keys of a tile are two 32-bit words (a bit below
 //     the last key and not below the first one, or below `sinks`), applied to
 //     the scores in one pass; tiles that every row of a warp sees whole skip it;
-//   * bias: a head's column of the table is spread over the distances once a
-//     CTA, in shared memory, scaled by log2 e.  A row's thread then adds the
-//     float at (key - row), neighbouring rows neighbouring words (no bank
-//     conflicts), in the same FMA that scales the score.  Beyond `reach` all
-//     distances of a side share one bucket: there the bias is one number for
-//     the tile and goes into the exponent's offset, at no cost a key.
+//   * bias: a head's column of the table is spread over the distances, in shared
+//     memory, scaled by log2 e: the CTA's first by all softmax warps while Q and K
+//     are on their way (two texts: 4.6 us instead of 6.8 by one warp), later ones
+//     by the loading warp, ahead.  A row's thread then adds the float at (key -
+//     row), neighbouring rows neighbouring words (no bank conflicts), in an FMA
+//     that scales the score; reading the words costs 2 % (two or four at once, from
+//     shifted copies, gain nothing).  Beyond `reach` all distances of a side share
+//     one bucket: there the bias is one number for the tile and goes into the
+//     exponent's offset, at no cost a key;
+//   * one copy of each role's code, rare cases short rather than fast: the
+//     instruction caches bound it (5 to 10 %).
 // A masked key has weight 0, but 0 x inf is not 0: the tensor core would spread
 // a value that is not finite from a masked place.  So the rows of V behind a
 // sequence's end (its neighbour's) are zeroed in shared memory, and an output
 // row that comes out not finite all the same is computed again from its visible
-// keys alone (mend_row), which finite inputs never reach.
+// keys alone (mend_row), which finite inputs of ordinary size never reach.
 // Every mbarrier wait is bounded, as in attn.cu.
+//
+// Measured (a call among others): packed texts (32, 19 .. 955 rows, 8
+// heads of 64) with a window of 512 and 4 sinks 36.8 us, with a bias 44.6; 30001
+// rows, 12 heads of 64, window 256, 64 sinks 89.6 us (590 TFLOP/s of the visible
+// pairs); grouped causal heads (8191 rows, 32 over 8 of 128, window 1023) 128 us
+// (1010); two images of 4224 rows, 30 heads of 128: window 1056 and 32 sinks 207 us
+// (1170), bias 417 us (1310, 70 % of the measured bf16 rate).
 #include <cuda.h>
 #include <float.h>
 #include <math.h>
@@ -35,7 +74,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "common.cuh"
 
@@ -453,11 +491,8 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
     bool ok = true;
     // waits of a whole warp; false: given up
     auto wait = [&](int b, uint32_t parity) { return wait_on(bar(b), parity & 1); };
-    // The same in two parts: test looks without waiting, settle comes once the
-    // answer is needed; a look at a barrier costs its latency, which the work
-    // between the two hides.
+    // looks without waiting; what the look costs (its latency) the work up to its use hides
     auto test = [&](int b, uint32_t parity) { return mbar_test(bar(b), parity & 1); };
-    auto settle = [&](bool there, int b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, there) || wait(b, parity); };
     // the record of the CTA's item number it, read by a whole warp
     auto get_record = [&](int it) {
         const volatile int4 *q = rec + (it & 3);
@@ -755,7 +790,6 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
                     bias = spread_of(built & 1);
                     if (built == 0) {
                         // the CTA's first: by all softmax warps at once, while Q and K are on their way
-                        prior_wait();
                         for (int d = (int)threadIdx.x - width; d <= width; d += 32 * L::SOFTMAX_WARPS)
                             spread_of(0)[d] = bias_log2(p.table[(long long)bucket_of(p, d) * p.ldt + head]);
                         __syncwarp();
