@@ -773,6 +773,12 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
         const int wq = warp & 3;                         // TMEM lane quadrant: rows 32 wq ..
         const uint32_t scol = tbase + ((uint32_t)(32 * wq) << 16) + w * L::TILE_COLS;
         const float c = p.scale_log2;
+        // Partial maxima of a row, and whether S is given back behind them or as soon as it is
+        // in registers.  Both only order the same work; measured: 2 and 3 maxima at hd 64 217 and
+        // 225 us (4 x 4096 rows, 12 heads), at hd 128 with bias 405 and 399 (two images); S given
+        // back late and at once 217 and 226, hd 128 341 and 347 (2 x 4096, 30 heads), with bias 434 and 399.
+        constexpr int NM = HD == 64 ? 2 : 3;
+        constexpr bool FREE_LATE = HD == 64 || !BIAS;
         uint32_t done = 0;                               // key tiles of this query tile, of all items
         uint32_t vbase = 0;                              // key tiles of the CTA's items before this one
         int head = -1, built = 0;                        // as where they are spread
@@ -838,6 +844,12 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
             int t = mine.sink > 0 ? 0 : mine.first;
             look(t * BKV);
             bool begun = false, more = true;
+            // the tensor core may compute the next S
+            auto free_s = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                arrive_if(bar(L::BAR_SFREE + w), lane == 0);
+            };
             // the S row of a tile in two halves of 32 keys
             uint32_t va[32], vb[32];
             if (!(ok = wait(L::BAR_SF + w, done))) break;
@@ -847,10 +859,7 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
             while (more) {
                 wait_loaded(va);
                 wait_loaded(vb);
-                // the tensor core may compute the next S
-                tc_fence_before();
-                __syncwarp();
-                arrive_if(bar(L::BAR_SFREE + w), lane == 0);
+                if (!FREE_LATE) free_s();
                 // scores in log2 units are s * cs + cb
                 float cs = c;
                 if (special) {
@@ -890,16 +899,17 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
                         fence_async_smem();
                     }
                 }
+                if (FREE_LATE) free_s();
                 // P is free once its last PV is done (there is none before the first)
                 const bool p_free = test(L::BAR_PV + w, done - 1);
-                // pass 1: the row maximum, eight partial ones; and beside it P = 2^(s cs + cb - m)
+                // pass 1: the row maximum, a few partial ones; and beside it P = 2^(s cs + cb - m)
                 // of the first half by the reference so far, which nearly always stays
-                float m8[8];
+                float mp[NM];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m8[i] = fmaxf(__uint_as_float(va[i]), __uint_as_float(vb[i]));
+                for (int i = 0; i < NM; ++i) mp[i] = fmaxf(__uint_as_float(va[i]), __uint_as_float(vb[i]));
 #pragma unroll
-                for (int i = 8; i < 32; ++i) m8[i & 7] = fmax3(m8[i & 7], __uint_as_float(va[i]), __uint_as_float(vb[i]));
-                const float mx = fmaf(fmaxf(fmax3(fmax3(m8[0], m8[1], m8[2]), m8[3], m8[4]), fmax3(m8[5], m8[6], m8[7])), cs, cb);
+                for (int i = NM; i < 32; ++i) mp[i % NM] = fmax3(mp[i % NM], __uint_as_float(va[i]), __uint_as_float(vb[i]));
+                const float mx = fmaf(NM == 3 ? fmax3(mp[0], mp[1], mp[NM - 1]) : fmaxf(mp[0], mp[1]), cs, cb);
                 // it moves when a row grew by more than 2^20 (P, sums and O have f32's exponents to spare;
                 // moves cost a pass over O: by 2^8 grouped causal heads take 138 us instead of 131)
                 const bool resc = mx > m_used + 20.f;
