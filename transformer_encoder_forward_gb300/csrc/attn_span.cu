@@ -13,12 +13,12 @@
 //
 // What bounds it.  A key costs 4 hd multiply-adds on the tensor core and one
 // exponential; bytes are few (q, k, v read once, o written: 30 % of the copy rate
-// where windows are short, 9 % where they are not).  A step of 64 keys and all
+// where windows are short, 10 % where they are not).  A step of 64 keys and all
 // query tiles of a CTA takes the tensor core 1200 (hd 64, 3 tiles) and 1250 (hd
 // 128, 2 tiles) clocks; alone, the softmax takes 1286 and 993 for it.  Both run
-// at once and take 1600 to 1750 together: two pipes that wait on one another
+// at once and take 1500 to 1700 together: two pipes that wait on one another
 // through barriers of about 100 clocks.  Without a window, 4 x 4096 rows with 12
-// heads of 64 run at 890 TFLOP/s and 2 x 4096 with 30 heads of 128 at 1480; with
+// heads of 64 run at 950 TFLOP/s and 2 x 4096 with 30 heads of 128 at 1520; with
 // one, partly seen tiles and the masks and biases of their pairs cost the rest.
 //
 // The form, and why:
@@ -52,8 +52,10 @@
 //     shifted copies, gain nothing).  Beyond `reach` all distances of a side share
 //     one bucket: there the bias is one number for the tile and goes into the
 //     exponent's offset, at no cost a key;
-//   * one copy of each role's code, rare cases short rather than fast: the
-//     instruction caches bound it (5 to 10 %).
+//   * one copy of each role's code, rare cases short rather than fast, no branch in
+//     the softmax's loop that saves work only sometimes: the instruction caches and
+//     the loop's one long schedule bound it (5 to 15 %: leaving out the exponentials
+//     of tiles that a warp sees nothing of made even calls without any slower).
 // A masked key has weight 0, but 0 x inf is not 0: the tensor core would spread
 // a value that is not finite from a masked place.  So the rows of V behind a
 // sequence's end (its neighbour's) are zeroed in shared memory, and an output
@@ -61,12 +63,12 @@
 // keys alone (mend_row), which finite inputs of ordinary size never reach.
 // Every mbarrier wait is bounded, as in attn.cu.
 //
-// Measured (a call among others): packed texts (32, 19 .. 955 rows, 8
-// heads of 64) with a window of 512 and 4 sinks 36.8 us, with a bias 44.6; 30001
-// rows, 12 heads of 64, window 256, 64 sinks 89.6 us (590 TFLOP/s of the visible
-// pairs); grouped causal heads (8191 rows, 32 over 8 of 128, window 1023) 128 us
-// (1010); two images of 4224 rows, 30 heads of 128: window 1056 and 32 sinks 207 us
-// (1170), bias 417 us (1310, 70 % of the measured bf16 rate).
+// Measured (a call among others): packed texts (32, 19 .. 955 rows, 8 heads of 64)
+// with a window of 512 and 4 sinks 35.4 us, with a bias 43.7; 30001 rows, 12 heads
+// of 64, window 256, 64 sinks 86.6 us (611 TFLOP/s of the visible pairs); grouped
+// causal heads (8191 rows, 32 over 8 of 128, window 1023) 125 us (1030); two images
+// of 4224 rows, 30 heads of 128: window 1056 and 32 sinks 202 us (1200), bias 403 us
+// (1360, 72 % of the measured bf16 rate).
 #include <cuda.h>
 #include <float.h>
 #include <math.h>
@@ -269,12 +271,11 @@ __device__ __forceinline__ void arrive_n(uint32_t bar, int n, uint32_t e) {
                  : "memory");
 }
 
-// Scores of 32 keys to log2 units with their bias: v = v c + b[e] (ONE: + one).
-template <bool ONE>
-__device__ __forceinline__ void add_bias(uint32_t (&v)[32], uint64_t c2, const float *b, float one) {
+// Scores of 32 keys to log2 units with their bias: v = v c + b[e].
+__device__ __forceinline__ void add_bias(uint32_t (&v)[32], uint64_t c2, const float *b) {
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
-        const uint64_t b2 = ONE ? f2_pack(one, one) : f2_pack(b[e], b[e + 1]);
+        const uint64_t b2 = f2_pack(b[e], b[e + 1]);
         float x, y;
         f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2, b2), x, y);
         v[e] = __float_as_uint(x);
@@ -865,16 +866,13 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
                 if (special) {
                     const int kv0 = t * BKV;
                     if constexpr (BIAS) {
-                        const bool each = kv0 > near_from && kv0 < near_to;
-                        if (each || !(fabsf(cb) <= 8192.f)) {
+                        const bool near = kv0 > near_from && kv0 < near_to;
+                        if (near || !(fabsf(cb) <= 8192.f)) {
+                            // (64 distances past the reach hold a side's far bias)
+                            const float *b = bias + (near ? kv0 - qi : kv0 <= near_from ? -p.reach - (BKV - 1) : p.reach);
                             const uint64_t c2 = f2_pack(c, c);
-                            if (each) {
-                                add_bias<false>(va, c2, bias + (kv0 - qi), 0.f);
-                                add_bias<false>(vb, c2, bias + (kv0 - qi) + 32, 0.f);
-                            } else {
-                                add_bias<true>(va, c2, nullptr, cb);
-                                add_bias<true>(vb, c2, nullptr, cb);
-                            }
+                            add_bias(va, c2, b);
+                            add_bias(vb, c2, b + 32);
                             cs = 1.f;
                             cb = 0.f;
                         }
