@@ -119,3 +119,17 @@ def test_block_attention_refusals(L):
     assert st == te.TE_EINVAL and "attention" in msg
     a = te.block_attn()
     assert _call(L, "te_encoder_block_attn_fwd", None, ctypes.byref(a), FAKE, FAKE, None, FAKE, 1, FAKE, 0, None)[0] == te.TE_EINVAL
+
+
+def test_block_attn_checks_its_table():
+    torch = pytest.importorskip("torch")
+    plan = te.relpos_plan(32, 128)
+    for table, err in ((torch.zeros(32, 4), ValueError),                    # not on the device
+                       (torch.zeros(32, 4, dtype=torch.float64), TypeError), (torch.zeros(31, 4), ValueError),
+                       (torch.zeros(32), ValueError), (torch.zeros(4, 32).T, ValueError)):
+        with pytest.raises(err):
+            te.block_attn(plan=plan, table=table)
+    with pytest.raises(TypeError):
+        te.block_attn(plan=object(), table=torch.zeros(32, 4))
+    with pytest.raises(ValueError):
+        te.block_attn(table=torch.zeros(32, 4))

@@ -128,3 +128,12 @@ def test_refusals_touch_nothing():
             make("c1", 1, (37, 64), wrong)
     with pytest.raises(ValueError):
         make("c1", 2, (37, 64), [None])
+
+
+def test_a_table_of_too_few_heads_is_refused():
+    import torch
+    cfg, ps, tables, st = make("c1", 1, (37, 64), dict(left=8, right=8))
+    x, a, _ = st.buffers()
+    at = te.block_attn(plan=te.relpos_plan(32, 128), table=torch.zeros(32, cfg.heads, device="cuda")[:, :cfg.heads - 1])
+    with pytest.raises(ValueError, match="heads"):
+        te.encoder_block_attn_fwd(st.descs[0], at, x, a, st.cu_host, st.cu_dev, st.workspace)

@@ -497,6 +497,14 @@ def block_attn(left=-1, right=-1, sinks=0, plan=None, table=None) -> te_block_at
     relative position bias.  Keeps plan and table alive."""
     if (plan is None) != (table is None):
         raise ValueError("block_attn: a plan and its table go together")
+    if plan is not None:
+        import torch
+        if not isinstance(plan, te_relpos) or table.dtype != torch.float32:
+            raise TypeError("block_attn: a relpos_plan and an f32 table")
+        if table.dim() != 2 or table.shape[0] < plan.buckets or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError(f"block_attn: table {tuple(table.shape)}, strides {table.stride()}, for {plan.buckets} buckets")
+        if not table.is_cuda:
+            raise ValueError("block_attn: the table is not on the device")
     a = te_block_attn(left, right, sinks, ctypes.addressof(plan) if plan is not None else None, _ptr(table),
                       table.stride(0) if table is not None else 0)
     a.keep = (plan, table)
@@ -505,6 +513,9 @@ def block_attn(left=-1, right=-1, sinks=0, plan=None, table=None) -> te_block_at
 
 def encoder_block_attn_fwd(desc: te_block_desc, attn: te_block_attn, x, a, cu_host, cu_dev, workspace, stream=None):
     """encoder_block_fwd with the attention step of `attn` (block_attn)."""
+    table = getattr(attn, "keep", (None, None))[1]
+    if table is not None and (table.shape[1] < desc.n_heads or table.device != x.device):
+        raise ValueError(f"block_attn: a table of {table.shape[1]} heads on {table.device}, the block has {desc.n_heads} on {x.device}")
     arr, hp = _host_i32(cu_host)
     _ok(lib().te_encoder_block_attn_fwd(ctypes.byref(desc), ctypes.byref(attn), x.data_ptr(), a.data_ptr(), hp,
                                         cu_dev.data_ptr(), len(arr) - 1, workspace.data_ptr(),
