@@ -372,8 +372,8 @@ def _marshalling():
             raise RuntimeError(f"_marshal.so is not built, or for another PyTorch or Python ({e}); run "
                                "python -m transformer_encoder_forward_gb300.build") from e
         mod.bind(*(ctypes.cast(f, c_p).value for f in (L.te_quant_rows, L.te_rownorm_quant, L.te_i8_linear,
-                                                       L.te_i8_gated_linear, L.te_qk_rope_axes,
-                                                       L.te_attn_sink_fwd, L.te_attn_relbias_fwd)))
+                                                       L.te_i8_gated_linear, L.te_qk_rope_axes)))
+        mod.bind_attn(*(ctypes.cast(f, c_p).value for f in (L.te_attn_sink_fwd, L.te_attn_relbias_fwd)))
         _m = mod
     return _m
 

@@ -391,29 +391,43 @@ PyObject *attn_span(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// bind(addresses of te_quant_rows, te_rownorm_quant, te_i8_linear, te_i8_gated_linear, te_qk_rope_axes,
-//      te_attn_sink_fwd, te_attn_relbias_fwd)
+// A function's address, from a Python int.
+void *address(PyObject *o) {
+    void *f = PyLong_AsVoidPtr(o);
+    if (!f) raise(PyExc_ValueError, "bind: not a function's address");
+    return f;
+}
+
+// bind(addresses of te_quant_rows, te_rownorm_quant, te_i8_linear, te_i8_gated_linear, te_qk_rope_axes)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&] {
-        count(n, 7);
-        void *f[7];
-        for (int i = 0; i < 7; ++i) {
-            f[i] = PyLong_AsVoidPtr(a[i]);
-            if (!f[i]) raise(PyExc_ValueError, "bind: not a function's address");
-        }
+        count(n, 5);
+        void *f[5];
+        for (int i = 0; i < 5; ++i) f[i] = address(a[i]);
         abi.quant_rows = reinterpret_cast<decltype(abi.quant_rows)>(f[0]);
         abi.rownorm_quant = reinterpret_cast<decltype(abi.rownorm_quant)>(f[1]);
         abi.i8_linear = reinterpret_cast<decltype(abi.i8_linear)>(f[2]);
         abi.i8_gated_linear = reinterpret_cast<decltype(abi.i8_gated_linear)>(f[3]);
         abi.qk_rope_axes = reinterpret_cast<decltype(abi.qk_rope_axes)>(f[4]);
-        abi.attn_sink_fwd = reinterpret_cast<decltype(abi.attn_sink_fwd)>(f[5]);
-        abi.attn_relbias_fwd = reinterpret_cast<decltype(abi.attn_relbias_fwd)>(f[6]);
+        return TE_OK;
+    });
+}
+
+// bind_attn(addresses of te_attn_sink_fwd, te_attn_relbias_fwd)
+PyObject *bind_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&] {
+        count(n, 2);
+        void *f[2];
+        for (int i = 0; i < 2; ++i) f[i] = address(a[i]);
+        abi.attn_sink_fwd = reinterpret_cast<decltype(abi.attn_sink_fwd)>(f[0]);
+        abi.attn_relbias_fwd = reinterpret_cast<decltype(abi.attn_relbias_fwd)>(f[1]);
         return TE_OK;
     });
 }
 
 PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, nullptr},
+    {"bind_attn", (PyCFunction)(void (*)(void))bind_attn, METH_FASTCALL, nullptr},
     {"quant_rows", (PyCFunction)(void (*)(void))quant_rows, METH_FASTCALL, nullptr},
     {"rownorm_quant", (PyCFunction)(void (*)(void))rownorm_quant, METH_FASTCALL, nullptr},
     {"i8_linear", (PyCFunction)(void (*)(void))i8_linear, METH_FASTCALL, nullptr},
