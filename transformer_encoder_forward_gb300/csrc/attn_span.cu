@@ -774,12 +774,15 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
         const int wq = warp & 3;                         // TMEM lane quadrant: rows 32 wq ..
         const uint32_t scol = tbase + ((uint32_t)(32 * wq) << 16) + w * L::TILE_COLS;
         const float c = p.scale_log2;
-        // Partial maxima of a row, and whether S is given back behind them or as soon as it is
-        // in registers.  Both only order the same work; measured: 2 and 3 maxima at hd 64 217 and
-        // 225 us (4 x 4096 rows, 12 heads), at hd 128 with bias 405 and 399 (two images); S given
-        // back late and at once 217 and 226, hd 128 341 and 347 (2 x 4096, 30 heads), with bias 434 and 399.
-        constexpr int NM = HD == 64 ? 2 : 3;
+        // Partial maxima of a row; whether S is given back behind them or as soon as it is in
+        // registers; whether the next tile is looked over behind P or beside the second half.  All
+        // only order the same work.  Measured, us (full attention, 4 x 4096 rows of 12 heads of 64;
+        // 2 x 4096 of 30 of 128; two images with bias): maxima 2 204 341 412, 3 201 335 407, 8 (before
+        // the others) 231 347 415; S given back late 217 341 434 (before), at once 226 347 399; looked
+        // over late 205 347 406, beside the second half 205 337 410 (packed texts with bias 41.8, 44.0).
+        constexpr int NM = 3;
         constexpr bool FREE_LATE = HD == 64 || !BIAS;
+        constexpr bool LOOK_LATE = HD == 64 || BIAS;
         uint32_t done = 0;                               // key tiles of this query tile, of all items
         uint32_t vbase = 0;                              // key tiles of the CTA's items before this one
         int head = -1, built = 0;                        // as where they are spread
@@ -907,7 +910,7 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
                 for (int i = 0; i < NM; ++i) mp[i] = fmaxf(__uint_as_float(va[i]), __uint_as_float(vb[i]));
 #pragma unroll
                 for (int i = NM; i < 32; ++i) mp[i % NM] = fmax3(mp[i % NM], __uint_as_float(va[i]), __uint_as_float(vb[i]));
-                const float mx = fmaf(NM == 3 ? fmax3(mp[0], mp[1], mp[NM - 1]) : fmaxf(mp[0], mp[1]), cs, cb);
+                const float mx = fmaf(fmax3(mp[0], mp[1], mp[2]), cs, cb);
                 // it moves when a row grew by more than 2^20 (P, sums and O have f32's exponents to spare;
                 // moves cost a pass over O: by 2^8 grouped causal heads take 138 us instead of 131)
                 const bool resc = mx > m_used + 20.f;
@@ -953,24 +956,19 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
                 r2[1] = rt[1];
                 t = t + 1 == mine.sink ? mine.first : t + 1;
                 more = t < mine.end;
-                look(t * BKV);
+                if (!LOOK_LATE) look(t * BKV);
                 tmem_st16(scol + L::P_COL + 16, pk);
                 begun = true;
                 ++done;
-                // the next S while P is on its way to TMEM (not waited for yet: it may come
-                // only behind this tile's PV)
-                const bool ahead = __all_sync(0xFFFFFFFFu, s_there) && more;
-                if (ahead) {
-                    tc_fence_after();
-                    tmem_ld32(scol, va);
-                    tmem_ld32(scol + 32, vb);
-                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 arrive_if(bar(L::BAR_PF + w), lane == 0);
-                if (__builtin_expect(more && !ahead, 0)) {
-                    if (!(ok = wait(L::BAR_SF + w, done))) break;
+                if (LOOK_LATE) look(t * BKV);
+                // (the next S may come only behind this tile's PV: P is out before it is waited for)
+                if (more) {
+                    if (!__all_sync(0xFFFFFFFFu, s_there))
+                        if (!(ok = wait(L::BAR_SF + w, done))) break;
                     tc_fence_after();
                     tmem_ld32(scol, va);
                     tmem_ld32(scol + 32, vb);
