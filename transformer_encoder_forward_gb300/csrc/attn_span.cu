@@ -16,9 +16,9 @@
 // where windows are short, 10 % where they are not).  A step of 64 keys and all
 // query tiles of a CTA takes the tensor core 1200 (hd 64, 3 tiles) and 1250 (hd
 // 128, 2 tiles) clocks; alone, the softmax takes 1286 and 993 for it.  Both run
-// at once and take 1500 to 1700 together: two pipes that wait on one another
+// at once and take about 1500 together: two pipes that wait on one another
 // through barriers of about 100 clocks.  Without a window, 4 x 4096 rows with 12
-// heads of 64 run at 950 TFLOP/s and 2 x 4096 with 30 heads of 128 at 1520; with
+// heads of 64 run at 1020 TFLOP/s and 2 x 4096 with 30 heads of 128 at 1530; with
 // one, partly seen tiles and the masks and biases of their pairs cost the rest.
 //
 // The form, and why:
@@ -30,7 +30,9 @@
 //     (two images with sinks: 268 us by 128, 222 by 64);
 //   * each query tile has a warp that issues its products, a further warp
 //     schedules, loads and spreads biases.  S of the next key tile is issued once
-//     the softmax has this one's in registers; P goes to TMEM, half at a time;
+//     the softmax has this one's in registers; P goes to TMEM, half at a time, and
+//     the next scores are taken up behind it (before its stores were waited for
+//     they cost 4 x 4096 rows of 12 heads of 64 217 us instead of 205);
 //   * a CTA that is done takes over the place of one that has not started
 //     (cluster launch control), so that the next item's loads and first products
 //     run under the last one's softmax and stores.  Items with the most keys go
@@ -55,7 +57,7 @@
 //   * one copy of each role's code, rare cases short rather than fast, no branch in
 //     the softmax's loop that saves work only sometimes: the instruction caches and
 //     the loop's one long schedule bound it (5 to 15 %: leaving out the exponentials
-//     of tiles that a warp sees nothing of made even calls without any slower).
+//     of tiles that a warp sees nothing of made even calls without such tiles slower).
 // A masked key has weight 0, but 0 x inf is not 0: the tensor core would spread
 // a value that is not finite from a masked place.  So the rows of V behind a
 // sequence's end (its neighbour's) are zeroed in shared memory, and an output
@@ -64,11 +66,11 @@
 // Every mbarrier wait is bounded, as in attn.cu.
 //
 // Measured (a call among others): packed texts (32, 19 .. 955 rows, 8 heads of 64)
-// with a window of 512 and 4 sinks 35.4 us, with a bias 43.7; 30001 rows, 12 heads
-// of 64, window 256, 64 sinks 86.6 us (611 TFLOP/s of the visible pairs); grouped
+// with a window of 512 and 4 sinks 33.4 us, with a bias 41.7; 30001 rows, 12 heads
+// of 64, window 256, 64 sinks 81 us (653 TFLOP/s of the visible pairs); grouped
 // causal heads (8191 rows, 32 over 8 of 128, window 1023) 125 us (1030); two images
-// of 4224 rows, 30 heads of 128: window 1056 and 32 sinks 202 us (1200), bias 403 us
-// (1360, 72 % of the measured bf16 rate).
+// of 4224 rows, 30 heads of 128: window 1056 and 32 sinks 201 us (1210), bias 407 us
+// (1350, 71 % of the measured bf16 rate).
 #include <cuda.h>
 #include <float.h>
 #include <math.h>
@@ -1076,10 +1078,10 @@ te_status launch(const SpanParams &p, const te_relpos *plan, cudaStream_t stream
 
 // --------------------------------------------- buckets of relative positions
 
-// Whole numbers below 2^3072, for the borders of the buckets: products and
+// Whole numbers below 2^2880, for the borders of the buckets: products and
 // comparisons only.
 struct Whole {
-    uint32_t w[96];
+    uint32_t w[90];
     int n;
     explicit Whole(uint32_t v) : n(1) { w[0] = v; }
     void times(uint32_t f) {
