@@ -31,8 +31,8 @@
 //   * each query tile has a warp that issues its products, a further warp
 //     schedules, loads and spreads biases.  S of the next key tile is issued once
 //     the softmax has this one's in registers; P goes to TMEM, half at a time, and
-//     the next scores are taken up behind it (before its stores were waited for
-//     they cost 4 x 4096 rows of 12 heads of 64 217 us instead of 205);
+//     the next scores are read behind it (read before P's stores are waited for,
+//     4 x 4096 rows of 12 heads of 64 take 217 us instead of 205);
 //   * a CTA that is done takes over the place of one that has not started
 //     (cluster launch control), so that the next item's loads and first products
 //     run under the last one's softmax and stores.  Items with the most keys go
