@@ -334,19 +334,20 @@ __device__ __forceinline__ void mend_row(const SpanParams &p, const float *bias,
     for (int c = 0; c < C; ++c) o[c] = 0.f;
 #pragma unroll 1
     for (int key = p.sinks > 0 ? 0 : lo; key < hi; key = key + 1 < p.sinks || key + 1 > lo ? key + 1 : lo) {
+        float b = 0.f;
+        if (BIAS) {
+            const int d = key - qi;
+            b = bias[d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d)];
+            if (b == -INFINITY) continue;                // it masks, whatever the score (which may be NaN)
+        }
         const __nv_bfloat16 *k = row0 + (long long)key * p.ld + (h / p.group) * HD;
         float s = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(k[p.k_off + c]), s);
 #pragma unroll 1
         for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-        float b = 0.f;
-        if (BIAS) {
-            const int d = key - qi;
-            b = bias[d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d)];
-        }
         s = fmaf(s, p.scale_log2, b);
-        if (s == -INFINITY) continue;                    // a bias of -inf masks too
+        if (s == -INFINITY) continue;
         const float mn = fmaxf(m, s), alpha = hw_exp2(m - mn), pr = hw_exp2(s - mn);
         m = mn;
         l = l * alpha + pr;
