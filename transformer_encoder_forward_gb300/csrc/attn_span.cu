@@ -354,14 +354,15 @@ __device__ __forceinline__ void mend_row(const SpanParams &p, const float *bias,
         bool lost = true;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            o[c] = fmaf(pr, __bfloat162float(k[p.v_off + c]), o[c] * alpha);
+            // (2^-29: no sum of at most 2^29 values passes the largest of them)
+            o[c] = fmaf(pr * 0x1p-29f, __bfloat162float(k[p.v_off + c]), o[c] * alpha);
             lost = lost && isnan(o[c]);
         }
         if (__all_sync(0xFFFFFFFFu, lost)) break;
     }
     __nv_bfloat16 *orow = p.out + (long long)(off + qi) * p.ldo + h * HD + lane * C;
 #pragma unroll
-    for (int c = 0; c < C; ++c) orow[c] = __float2bfloat16_rn(l == 0.f ? 0.f : o[c] / l);
+    for (int c = 0; c < C; ++c) orow[c] = __float2bfloat16_rn(l == 0.f ? 0.f : o[c] / l * 0x1p29f);
 }
 
 // The work of CTA `b` of the grid: which rows of which sequence, and the head.
