@@ -1026,9 +1026,11 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
                 }
                 __syncwarp();
             }
-            // rows whose sum is 0 or not finite, or that hold a value that is not
+            // rows that hold a value that is not finite, or whose sum is out of range: it is 1
+            // to 2^49 but for scores past 2^24, which f32 holds so coarsely that a row's
+            // weights are all off by one power of two (hw_rcp ends at 2^126)
             const float finite = (fin[0] + fin[1]) + (fin[2] + fin[3]);
-            uint32_t mend = __ballot_sync(0xFFFFFFFFu, qi < len && !(finite > 0.f && finite <= FLT_MAX));
+            uint32_t mend = __ballot_sync(0xFFFFFFFFu, qi < len && !(finite >= 0x1p-64f && finite <= 0x1p80f));
 #pragma unroll 1
             while (mend) {
                 const int x = __ffs(mend) - 1;
