@@ -63,7 +63,8 @@
 // sequence's end (its neighbour's) are zeroed in shared memory, and an output
 // row that comes out not finite all the same is computed again from its visible
 // keys alone (mend_row), which finite inputs of ordinary size never reach.
-// Every mbarrier wait is bounded, as in attn.cu.
+// Every mbarrier wait is bounded, as in attn.cu; the limit grows with the keys that a row
+// sees, as what is waited for does.
 //
 // Measured (a call among others): packed texts (32, 19 .. 955 rows, 8 heads of 64)
 // with a window of 512 and 4 sinks 33.4 us, with a bias 41.7; 30001 rows, 12 heads
@@ -88,6 +89,10 @@ constexpr int BQ = 128;     // queries per tile (= TMEM lanes)
 constexpr int BKV = 64;     // keys per tile
 constexpr int MAX_WORK = 640;   // work list entries carried in the launch parameters
 constexpr int MAX_SMEM = 227 * 1024;
+// A wait's limit, ns: far above what any takes, which is the steps of an item's key
+// tiles (0.8 us for 64 keys) and, where rows have to be computed again, 32 rows one
+// after another (18 us a key).
+constexpr unsigned long long WAIT_NS = 200000000, WAIT_KEY_NS = 64000;
 constexpr int PAD = 96;     // distances past `reach` that 32 rows and 64 keys near it can still touch (94)
 // as in attn.cu: K and V bytes that the CTA order treats as one group of heads
 constexpr long long KV_ALL_BYTES = 48ll << 20;
@@ -108,6 +113,7 @@ struct SpanParams {
     long long ld, ldo;
     int q_off, k_off, v_off, group;
     int left, right, sinks;    // limits clipped to the longest sequence
+    unsigned long long wait_ns;   // limit of a wait
     float scale_log2;
     // relative position bias
     const float *table;        // [buckets, ldt]
@@ -213,13 +219,13 @@ __device__ __forceinline__ float bias_log2(float v) {
     return fabsf(v) <= FLT_MAX ? fminf(fmaxf(v2, -FLT_MAX), FLT_MAX) : v;
 }
 
-// A whole warp waits for a phase, for 200 ms at most (then false); the loop out of
+// A whole warp waits for a phase, for limit_ns at most (then false); the loop out of
 // the way of the code around it.
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
     if (__builtin_expect(__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)), 1)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
-        if (__all_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > 200000000ull)) return false;
+        if (__all_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > limit_ns)) return false;
     return true;
 }
 
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
     const uint32_t tbase = tmem_slot[0];
     bool ok = true;
     // waits of a whole warp; false: given up
-    auto wait = [&](int b, uint32_t parity) { return wait_on(bar(b), parity & 1); };
+    auto wait = [&](int b, uint32_t parity) { return wait_on(bar(b), parity & 1, p.wait_ns); };
     // looks without waiting; what the look costs (its latency) the work up to its use hides
     auto test = [&](int b, uint32_t parity) { return mbar_test(bar(b), parity & 1); };
     // the record of the CTA's item number it, read by a whole warp
@@ -1183,6 +1189,8 @@ te_status span_fwd(const char *name, const void *qkv, int64_t ld, int32_t q_off,
     p.left = left < 0 || left > max_len ? max_len : left;
     p.right = right < 0 || right > max_len ? max_len : right;
     p.sinks = std::min(sinks, max_len);
+    // the keys that a row may see bound what a wait can take
+    p.wait_ns = WAIT_NS + WAIT_KEY_NS * (unsigned long long)std::min<int64_t>(max_len, (int64_t)p.left + p.right + 1 + p.sinks);
     p.scale_log2 = scale * 1.4426950408889634f;
     if (plan) {
         p.table = table;
