@@ -1037,6 +1037,16 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
             // weights are all off by one power of two (hw_rcp ends at 2^126)
             const float finite = (fin[0] + fin[1]) + (fin[2] + fin[3]);
             uint32_t mend = __ballot_sync(0xFFFFFFFFu, qi < len && !(finite >= 0x1p-64f && finite <= 0x1p80f));
+            if (mend) {
+                // no key was visible: a score of any would have set the reference, a NaN the sum
+                const bool none = qi < len && l == 0.f && m_used == -INFINITY;
+                mend &= ~__ballot_sync(0xFFFFFFFFu, none);
+                if (none) {
+                    uint4 *row = reinterpret_cast<uint4 *>(p.out + (long long)(r.off + qi) * p.ldo + r.h * HD);
+#pragma unroll 1
+                    for (int i = 0; i < HD / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+                }
+            }
 #pragma unroll 1
             while (mend) {
                 const int x = __ffs(mend) - 1;
