@@ -61,8 +61,8 @@
 // A masked key has weight 0, but 0 x inf is not 0: the tensor core would spread
 // a value that is not finite from a masked place.  So the rows of V behind a
 // sequence's end (its neighbour's) are zeroed in shared memory, and an output
-// row that comes out not finite all the same is computed again from its visible
-// keys alone (mend_row), which finite inputs of ordinary size never reach.
+// row that comes out not finite all the same is settled on its own (mend_rows), which
+// finite inputs of ordinary size never reach.
 // Every mbarrier wait is bounded, as in attn.cu; the limit grows with the keys that a row
 // sees, as what is waited for does.
 //
@@ -90,9 +90,9 @@ constexpr int BKV = 64;     // keys per tile
 constexpr int MAX_WORK = 640;   // work list entries carried in the launch parameters
 constexpr int MAX_SMEM = 227 * 1024;
 // A wait's limit, ns: far above what any takes, which is the steps of an item's key
-// tiles (0.8 us for 64 keys) and, where rows have to be computed again, 32 rows one
-// after another (18 us a key).
-constexpr unsigned long long WAIT_NS = 200000000, WAIT_KEY_NS = 64000;
+// tiles (0.8 us for 64 keys) and, where rows have to be computed again, the 32 rows of
+// a warp (1.8 us a key).
+constexpr unsigned long long WAIT_NS = 200000000, WAIT_KEY_NS = 16000;
 constexpr int PAD = 96;     // distances past `reach` that 32 rows and 64 keys near it can still touch (94)
 // as in attn.cu: K and V bytes that the CTA order treats as one group of heads
 constexpr long long KV_ALL_BYTES = 48ll << 20;
@@ -323,52 +323,229 @@ __device__ __forceinline__ void exp_pass(const uint32_t (&v)[32], uint64_t c2, u
     }
 }
 
-// One output row from its visible keys alone, by one warp in f32, key by key:
-// what the tiled form computes, without products of masked values.  It ends at
-// once when all of the row is lost.  (Short rather than fast: no finite input
-// comes here, and its code lies among the softmax's.)
-template <int HD, bool BIAS>
-__device__ __forceinline__ void mend_row(const SpanParams &p, const float *bias, int off, int len, int h, int qi) {
-    constexpr int C = HD / 32;                           // channels of a lane
-    const int lane = threadIdx.x & 31;
-    const __nv_bfloat16 *row0 = p.qkv + (long long)off * p.ld + lane * C;
-    const __nv_bfloat16 *q = row0 + (long long)qi * p.ld + p.q_off + h * HD;
-    const int lo = qi > p.left ? qi - p.left : 0;
-    const int hi = qi + p.right + 1 < len ? qi + p.right + 1 : len;
-    float m = -INFINITY, l = 0.f, o[C];
+// Is one of a lane's bf16 values infinite or NaN?
+template <int N>
+__device__ __forceinline__ bool odd(const uint32_t (&w)[N]) {
+    bool r = false;
 #pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = 0.f;
-#pragma unroll 1
-    for (int key = p.sinks > 0 ? 0 : lo; key < hi; key = key + 1 < p.sinks || key + 1 > lo ? key + 1 : lo) {
-        float b = 0.f;
-        if (BIAS) {
-            const int d = key - qi;
-            b = bias[d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d)];
-            if (b == -INFINITY) continue;                // it masks, whatever the score (which may be NaN)
-        }
-        const __nv_bfloat16 *k = row0 + (long long)key * p.ld + (h / p.group) * HD;
-        float s = 0.f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(k[p.k_off + c]), s);
-#pragma unroll 1
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-        s = fmaf(s, p.scale_log2, b);
-        if (s == -INFINITY) continue;
-        const float mn = fmaxf(m, s), alpha = hw_exp2(m - mn), pr = hw_exp2(s - mn);
-        m = mn;
-        l = l * alpha + pr;
-        bool lost = true;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            // (2^-29: no sum of at most 2^29 values passes the largest of them)
-            o[c] = fmaf(pr * 0x1p-29f, __bfloat162float(k[p.v_off + c]), o[c] * alpha);
-            lost = lost && isnan(o[c]);
-        }
-        if (__all_sync(0xFFFFFFFFu, lost)) break;
+    for (int i = 0; i < N; ++i) r |= ((w[i] & 0x7F80u) == 0x7F80u) | ((w[i] & 0x7F800000u) == 0x7F800000u);
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void load_words(const __nv_bfloat16 *from, uint32_t (&w)[N]) {
+    if constexpr (N == 1)
+        w[0] = *reinterpret_cast<const uint32_t *>(from);
+    else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(from);
+        w[0] = u.x;
+        w[1] = u.y;
     }
-    __nv_bfloat16 *orow = p.out + (long long)(off + qi) * p.ldo + h * HD + lane * C;
+}
+
+// Eight bf16 as f32.
+__device__ __forceinline__ void widen(const uint4 &u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int c = 0; c < C; ++c) orow[c] = __float2bfloat16_rn(l == 0.f ? 0.f : o[c] / l * 0x1p29f);
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+}
+
+// Output rows that the tiled form cannot give, by the warp that has them (bits of
+// `rows`, from row r0 on).  Where a row's sum is good (bits of `good`) its finite
+// channels are, too: a channel is lost to a value of V that is not finite, either one
+// that the row sees, and then it is that infinity (NaN: both or a NaN), or one in a
+// masked place of a tile (0 x inf).  One pass over the values that the warp's rows
+// see tells which; a lane has the same channels of all of them, and for each channel
+// the rows that see +inf and -inf.  Rows that this does not explain, and those
+// whose sum is not good, are computed again from their visible keys alone, four at
+// once, 32 keys at a time.
+// No finite input of ordinary size comes here.  2048 rows, 12 heads of 64 (45 us): an
+// infinite value that every row sees 162 us, a key of NaN 280; 256 keys to either side
+// (22 us) and a NaN beside the sinks, in a tile of every row, 920 (36, 18 and 9 ms by a
+// key at a time; one row at once 2.0 ms).  Not inlined, and the lane read anew: what is
+// worked out from it would be kept through the loop over key tiles, whose registers are
+// full (30001 rows, 12 heads of 64: 82 us, inlined 88).
+template <int HD, bool BIAS>
+__device__ __noinline__ void mend_rows(const SpanParams &p, const float *bias, int off, int len, int h, int r0, uint32_t rows,
+                                          uint32_t good) {
+    constexpr int C = HD / 32, W = C / 2;                // channels of a lane, words of them
+    constexpr uint32_t ALL = 0xFFFFFFFFu;
+    int lane;
+    asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+    const int g = (h / p.group) * HD;
+    const __nv_bfloat16 *panel = p.qkv + (long long)off * p.ld;
+    __nv_bfloat16 *out = p.out + (long long)(off + r0) * p.ldo + h * HD + lane * C;
+    auto bias_of = [&](int d) { return BIAS ? bias[d < -p.reach ? -p.reach : (d > p.reach ? p.reach : d)] : 0.f; };
+    // the keys of rows qa to qb: the first ns, and lo up to hi
+    int lo, hi, ns;
+    auto keys_of = [&](int qa, int qb) {
+        lo = qa > p.left ? qa - p.left : 0;
+        hi = qb + p.right + 1 < len ? qb + p.right + 1 : len;
+        ns = p.sinks < lo ? p.sinks : lo;
+    };
+    auto key_of = [&](int j) { return j < ns ? j : j - ns + lo; };
+    auto sees = [&](int qi, int key) {
+        return key <= qi + p.right && (key >= qi - p.left || key < p.sinks) && (!BIAS || bias_of(key - qi) != -INFINITY);
+    };
+
+    if (good) {
+        uint32_t plus[C] = {}, minus[C] = {}, again = 0;
+        keys_of(r0 + __ffs(good) - 1, r0 + 31 - __clz(good));
+        const int n = ns + hi - lo;
+        const __nv_bfloat16 *v = panel + p.v_off + g + lane * C;
+        bool known = false;                              // no later value changes anything
+#pragma unroll 1
+        for (int j = 0; j < n && !known; j += 8) {
+            uint32_t eight[8 * W];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t w[W];
+                load_words<W>(v + key_of(j + i < n ? j + i : n - 1) * p.ld, w);
+#pragma unroll
+                for (int y = 0; y < W; ++y) eight[i * W + y] = w[y];
+            }
+            if (!__any_sync(ALL, odd<8 * W>(eight))) continue;
+#pragma unroll 1
+            for (int i = j; i < j + 8 && i < n; ++i) {
+                const int key = key_of(i);
+                uint32_t w[W], k[W];
+                load_words<W>(v + key * p.ld, w);
+                if (!__any_sync(ALL, odd<W>(w))) continue;
+                const uint32_t who = __ballot_sync(ALL, sees(r0 + lane, key)) & good;
+                // (a key that is not finite may have scores of -inf, and then no weight)
+                load_words<W>(panel + key * p.ld + p.k_off + g + lane * C, k);
+                if (__any_sync(ALL, odd<W>(k))) again |= who;
+                known = true;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t x = w[c / 2] >> 16 * (c & 1);
+                    if ((x & 0x7F80u) == 0x7F80u) {
+                        const bool nan = x & 0x7Fu, neg = x & 0x8000u;
+                        if (nan || !neg) plus[c] |= who;
+                        if (nan || neg) minus[c] |= who;
+                    }
+                    known = known && (plus[c] & minus[c]) == good;
+                }
+                known = __all_sync(ALL, known);
+            }
+        }
+#pragma unroll 1
+        for (uint32_t left = good; left; left &= left - 1) {
+            const int x = __ffs(left) - 1;
+            __nv_bfloat16 *o = out + (long long)x * p.ldo;
+            uint32_t w[W];
+            load_words<W>(o, w);
+            bool lost = again >> x & 1;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int at = 16 * (c & 1);
+                if ((w[c / 2] >> at & 0x7F80u) == 0x7F80u) {
+                    const bool a = plus[c] >> x & 1, b = minus[c] >> x & 1;
+                    w[c / 2] = (w[c / 2] & ~(0xFFFFu << at)) | (a && b ? 0x7FFFu : b ? 0xFF80u : 0x7F80u) << at;
+                    lost = lost || !(a || b);
+                }
+            }
+            if (__any_sync(ALL, lost)) continue;
+#pragma unroll
+            for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t *>(o)[i] = w[i];
+            rows &= ~(1u << x);
+        }
+    }
+
+    // R rows at once: they share their keys' loads and hide one another's latency
+    constexpr int R = 4, G = HD / 8;                     // G lanes have a key's channels together, eight each
+    const int at = lane % G * 8;
+    int hint = -1;                                       // a key whose score lost the rows before
+#pragma unroll 1
+    while (rows) {
+        int qi[R];
+        float q[R][8], m[R], l[R], o[R][C];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {                    // (the last one again where there are fewer)
+            qi[r] = rows ? r0 + __ffs(rows) - 1 : qi[r > 0 ? r - 1 : 0];
+            rows &= rows - 1;
+            widen(*reinterpret_cast<const uint4 *>(panel + qi[r] * p.ld + p.q_off + h * HD + at), q[r]);
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) o[r][c] = 0.f;
+        }
+        keys_of(qi[0], qi[R - 1]);
+        const int n = ns + hi - lo;
+        uint32_t lost = 0;                               // a bit a row
+#pragma unroll 1
+        for (int j = hint >= 0 ? -32 : 0; j < n && lost != (1u << R) - 1; j += 32) {
+            const int key = j < 0 ? hint : key_of(j + lane < n ? j + lane : n - 1);
+            float s[R];
+#pragma unroll 4
+            for (int i = 0; i < G; ++i) {
+                float k[8];
+                widen(*reinterpret_cast<const uint4 *>(panel + __shfl_sync(ALL, key, lane / G * G + i) * p.ld + p.k_off + g + at), k);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float d = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d = fmaf(q[r][e], k[e], d);
+#pragma unroll
+                    for (int y = 1; y < G; y <<= 1) d += __shfl_xor_sync(ALL, d, y);
+                    if (lane % G == i) s[r] = d;
+                }
+            }
+            uint32_t take[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                // (a key that is masked takes nothing, whatever the score)
+                s[r] = j + lane < n && sees(qi[r], key) ? fmaf(s[r], p.scale_log2, bias_of(key - qi[r])) : -INFINITY;
+                // a score that is NaN or +inf loses the row, whatever else it sees
+                const uint32_t bad = __ballot_sync(ALL, isnan(s[r]) || s[r] == INFINITY);
+                if (bad) {
+                    hint = __shfl_sync(ALL, key, __ffs(bad) - 1);
+                    lost |= 1u << r;
+                }
+                take[r] = j < 0 ? 0 : __ballot_sync(ALL, s[r] > -INFINITY);
+            }
+            if (j < 0) continue;
+            float pr[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float mn = s[r];
+#pragma unroll
+                for (int y = 16; y > 0; y >>= 1) mn = fmaxf(mn, __shfl_xor_sync(ALL, mn, y));
+                mn = fmaxf(m[r], mn);
+                const float ref = mn == -INFINITY ? 0.f : mn, alpha = hw_exp2(m[r] - ref);
+                pr[r] = hw_exp2(s[r] - ref);
+                m[r] = mn;
+                l[r] = l[r] * alpha + pr[r];
+                pr[r] *= 0x1p-29f;                       // no sum of at most 2^29 values passes the largest of them
+#pragma unroll
+                for (int c = 0; c < C; ++c) o[r][c] *= alpha;
+            }
+#pragma unroll 8
+            for (int e = 0; e < 32; ++e) {
+                uint32_t w[W];
+                load_words<W>(panel + __shfl_sync(ALL, key, e) * p.ld + p.v_off + g + lane * C, w);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float we = __shfl_sync(ALL, pr[r], e);
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        if (take[r] >> e & 1)
+                            o[r][c] = fmaf(we, __uint_as_float(c & 1 ? w[c / 2] & 0xFFFF0000u : w[c / 2] << 16), o[r][c]);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int y = 16; y > 0; y >>= 1) l[r] += __shfl_xor_sync(ALL, l[r], y);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                out[(long long)(qi[r] - r0) * p.ldo + c] =
+                    __float2bfloat16_rn(lost >> r & 1 ? NAN : l[r] == 0.f ? 0.f : o[r][c] / l[r] * 0x1p29f);
+        }
+    }
 }
 
 // The work of CTA `b` of the grid: which rows of which sequence, and the head.
@@ -1039,19 +1216,15 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
             uint32_t mend = __ballot_sync(0xFFFFFFFFu, qi < len && !(finite >= 0x1p-64f && finite <= 0x1p80f));
             if (mend) {
                 // no key was visible: a score of any would have set the reference, a NaN the sum
-                const bool none = qi < len && l == 0.f && m_used == -INFINITY;
+                const bool none = qi < len && l == 0.f && nm0 == 0.f;
                 mend &= ~__ballot_sync(0xFFFFFFFFu, none);
                 if (none) {
                     uint4 *row = reinterpret_cast<uint4 *>(p.out + (long long)(r.off + qi) * p.ldo + r.h * HD);
 #pragma unroll 1
                     for (int i = 0; i < HD / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
                 }
-            }
-#pragma unroll 1
-            while (mend) {
-                const int x = __ffs(mend) - 1;
-                mend &= mend - 1;
-                mend_row<HD, BIAS>(p, bias, r.off, len, r.h, r0 + x);
+                const uint32_t good = __ballot_sync(0xFFFFFFFFu, l >= 0x1p-64f && l <= 0x1p80f);
+                if (mend) mend_rows<HD, BIAS>(p, bias, r.off, len, r.h, r0, mend, mend & good);
             }
         }
     }
