@@ -880,13 +880,23 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
             uint32_t sc = 0, pc = 0;                     // S and PV issued
             uint32_t items = 0;                          // items with rows before this one
             Ring kv = {0, 0};                            // the pair of K and V whose S comes next
-            // S = Q K^T of the next key tile that this query tile sees
+            // S = Q K^T of the next key tile that this query tile sees.  A look at a parity tells a
+            // phase from the one before it alone, and a pair that this warp passed unseen may, in
+            // principle, still be landing when its place comes round; so first its release is looked for,
+            // as by the loading warp: someone read it, so it landed, and the next cannot be released
+            // without this warp.  (The passed pair was issued: an item's Q, which was waited for, comes
+            // behind what was passed before it, and within an item fewer than R pairs are
+            // passed.  So the pair before it was released, and the look is not off by two phases.
+            // This warp's own part of the release is under way: the PV that is still to come
+            // is of one of the last R - 1 pairs.)
+            static_assert((NT - 1) * (BQ / BKV) + 1 <= R, "a query tile skips more than the ring holds");
             auto step_s = [&]() -> bool {
+                const bool released = test(L::BAR_KVE + kv.at, kv.phase ^ 1);
                 const bool there = test(L::BAR_KV + kv.at, kv.phase);
                 // the softmax has the last S in registers (before the first there is nothing to wait for)
                 const bool s_free = test(L::BAR_SFREE + w, sc + 1);
-                if (__builtin_expect(!__all_sync(0xFFFFFFFFu, there && s_free), 0) &&
-                    !(wait(L::BAR_KV + kv.at, kv.phase) && wait(L::BAR_SFREE + w, sc + 1)))
+                if (__builtin_expect(!__all_sync(0xFFFFFFFFu, released && there && s_free), 0) &&
+                    !(wait(L::BAR_KVE + kv.at, kv.phase ^ 1) && wait(L::BAR_KV + kv.at, kv.phase) && wait(L::BAR_SFREE + w, sc + 1)))
                     return false;
                 tc_fence_after();
                 const uint32_t k0 = kd + kv.at * (2 * L::TILE >> 4);
