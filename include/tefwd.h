@@ -596,7 +596,8 @@ te_status te_encoder_block_fwd(const te_block_desc *desc, float *x, void *a,
 
 /* The attention step of te_encoder_block_attn_fwd: te_attn_sink_fwd's limits
  * and sinks and, plan != NULL, te_attn_relbias_fwd's bias (its plan on the host;
- * its table f32 [plan->buckets, n_heads], rows ldt floats apart, on the device). */
+ * its table f32 [plan->buckets, n_heads], rows ldt floats apart, on the device).
+ * Without a plan the table must be NULL. */
 typedef struct {
     int32_t left, right, sinks;
     const te_relpos *plan;

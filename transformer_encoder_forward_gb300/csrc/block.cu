@@ -328,5 +328,6 @@ extern "C" te_status te_encoder_block_attn_fwd(const te_block_desc *desc, const 
                                                const int32_t *cu_host, const int32_t *cu_dev, int32_t nseq,
                                                void *workspace, size_t ws_bytes, te_stream stream) {
     if (!attn) return fail(TE_EINVAL, "block_attn: NULL attention");
+    if (attn->table && !attn->plan) return fail(TE_EINVAL, "block_attn: a table without its plan");
     return block_fwd(desc, attn, x, a, cu_host, cu_dev, nseq, workspace, ws_bytes, stream);
 }
