@@ -199,9 +199,14 @@ te_status te_attn_items_fwd(const void *qkv, int64_t ld, int32_t q_off, int32_t 
  * no limit (right = 0: causal); sinks >= 0.  A row always sees itself.
  * Values in masked places have no influence, not even where they are infinite
  * or NaN (a row with such a key of its own sequence next to its window is summed
- * in another order and takes longer).  scale in [2^-100, 2^100]; a sequence has at most 2^29 rows; rows of
- * out behind the last sequence are not touched.  Otherwise as
- * te_attn_varlen_fwd.  [EG2] att_plan's windowed span, extended. */
+ * in another order and takes longer).  An infinite value that a row sees makes
+ * that channel infinite, or NaN beside one of the other sign.  scale in
+ * [2^-100, 2^100]; a sequence has at most 2^29 rows; rows of out behind the
+ * last sequence are not touched.  cu_dev is read by calls of more than 640 blocks
+ * of 384 rows (hd 64) or 256 (hd 128), each sequence's last one counted whole;
+ * the offsets of smaller calls travel with the launch.  So a captured call is
+ * replayed with the offsets that it was captured with, and cu_dev keeps them.
+ * Otherwise as te_attn_varlen_fwd.  [EG2] att_plan's windowed span, extended. */
 te_status te_attn_sink_fwd(const void *qkv, int64_t ld, int32_t q_off, int32_t k_off, int32_t v_off,
                            const int32_t *cu_host, const int32_t *cu_dev, int32_t nseq,
                            int32_t nq_heads, int32_t nkv_heads, int32_t hd, int32_t left,
