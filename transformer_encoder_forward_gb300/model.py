@@ -72,8 +72,9 @@ class EncoderStack:
         attn: the layers' attention steps where they are not the config's: a dict
         (every layer) or a list of one a layer, each a dict or None (the
         config's).  A dict may hold left, right (limits; -1 or absent: none),
-        sinks, and relpos = (buckets, max_distance, two_sided) with table, f32
-        [buckets, heads] (layers that share a dict share the device's copy)."""
+        sinks, scale (of the scores; absent: the config's), and relpos =
+        (buckets, max_distance, two_sided) with table, f32 [buckets, heads]
+        (layers that share a dict share the device's copy)."""
         import torch
         self.cfg = cfg
         self.device = torch.device(device)
@@ -120,7 +121,7 @@ class EncoderStack:
         for a in attn:
             if a is None or id(a) in made:
                 continue
-            bad = set(a) - {"left", "right", "sinks", "relpos", "table"}
+            bad = set(a) - {"left", "right", "sinks", "scale", "relpos", "table"}
             if bad or ("relpos" in a) != ("table" in a):
                 raise ValueError(f"attn: unknown keys {sorted(bad)}" if bad else "attn: relpos and table go together")
             plan = table = None
@@ -130,6 +131,7 @@ class EncoderStack:
                     raise ValueError(f"attn: table {np.shape(a['table'])}, not {(plan.buckets, self.cfg.heads)}")
                 table = _dev(np.asarray(a["table"], dtype=np.float32), self.device)
             made[id(a)] = block_attn(a.get("left", -1), a.get("right", -1), a.get("sinks", 0), plan, table)
+            made[id(a)].scale = float(a.get("scale", self.cfg.scale))
         return [None if a is None else made[id(a)] for a in attn]
 
     def _desc(self, i: int) -> te_block_desc:
@@ -143,7 +145,8 @@ class EncoderStack:
         d.act = TE_ACT_SILU if cfg.act == "silu" else TE_ACT_GELU_TANH
         d.gated = 1 if cfg.gated else 0
         d.window = cfg.window_of(i) if self.attn[i] is None else 0
-        d.eps, d.attn_scale, d.post, d.q_mul = cfg.eps, cfg.scale, cfg.post, 1.0
+        d.eps, d.post, d.q_mul = cfg.eps, cfg.post, 1.0
+        d.attn_scale = cfg.scale if self.attn[i] is None else self.attn[i].scale
         for key in ("wq", "wk", "wv", "wo", "wg", "wd"):
             setattr(d, key, q8w(*L.t[key]))
         if L.t["wu"] is not None:
