@@ -150,3 +150,57 @@ def test_lost_queries_and_keys(hd):
         keep = ~lost[:, h]
         compare(f"beside lost rows {hd}", o[keep], ref[keep, h * hd:(h + 1) * hd], mag[keep, h * hd:(h + 1) * hd])
     assert torch.equal(out[700:], clean[700:])
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("bias", [False, True])
+def test_among_many_sequences(hd, bias):
+    """More blocks than travel with the launch; a wide panel with its heads in another order."""
+    import torch
+    rng = torch.Generator().manual_seed(124)
+    ln = [int(n) for n in torch.randint(1, 40, (690,), generator=rng)] + [600, 1, 257]
+    nq, nkv = 4, 2
+    w, kw = nq * hd, nkv * hd
+    plain = panel(sum(ln), w + 2 * kw, 125)
+    rows = torch.randint(0, sum(ln), (200,), generator=rng).cuda()
+    plain[rows, w + kw + (rows * 7) % kw] = INF
+    plain[rows[:20] // 2 * 2, w + kw + 3] = NAN
+    table = torch.randn(REL[0], nq, device="cuda") if bias else None
+    if bias:
+        table[2:4, 0] = -INF
+    span = (20, 5, 2)
+    o, mag = expected(plain, ln, nq, nkv, hd, span, table)
+    wide = torch.full((sum(ln), w + 2 * kw + 72), NAN, dtype=torch.bfloat16, device="cuda")
+    offs = (kw + 8, kw + w + 24, 0)
+    for at, (a, b) in zip(offs, ((0, w), (w, w + kw), (w + kw, w + 2 * kw))):
+        wide[:, at:at + b - a] = plain[:, a:b]
+    out = torch.full((sum(ln) + 3, w + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+    call(wide, ln, nq, nkv, hd, *span, hd ** -0.5, table=table, rel=REL if bias else None, offs=offs, out=out)
+    te.check()
+    same(f"many sequences {hd} bias={bias}", out[:sum(ln), :w], o, mag)
+    assert bool((out[sum(ln):] == 7).all()) and bool((out[:, w:] == 7).all())
+
+
+def test_offsets_past_32_bits():
+    """Panels of more than 2^31 values: rows at their end."""
+    import torch
+    hd, nq, ld = 64, 2, 8200
+    rows = (1 << 31) // ld + 3000
+    w = nq * hd
+    tail = [700, 300, 5]
+    lens, start = [rows - 1005] + tail, rows - 1005
+    off = ld - 3 * w - 8
+    qkv = torch.zeros(rows, ld, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(rows, ld, dtype=torch.bfloat16, device="cuda")
+    small = panel(1005, 3 * w, 126)
+    small[[100, 130, 800], [2 * w + 5, 2 * w + 70, 2 * w + 9]] = INF
+    small[40, 2 * w:] = NAN
+    qkv[start:, off:off + 3 * w] = small
+    qkv[start - 50, off + 2 * w:off + 3 * w] = NAN    # of the long sequence
+    span = (64, 64, 2)
+    call(qkv, lens, nq, nq, hd, *span, hd ** -0.5, offs=(off, off + w, off + 2 * w), out=out)
+    te.check()
+    o, mag = expected(small, tail, nq, nq, hd, span, None)
+    same("rows past 2^31 values", out[start:, :w], o, mag)
+    seen = torch.isnan(out[:start, :w].float()).all(1).nonzero()[:, 0]
+    assert seen.tolist() == list(range(start - 114, start))
