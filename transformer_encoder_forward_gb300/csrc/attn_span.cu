@@ -17,9 +17,9 @@
 // query tiles of a CTA takes the tensor core 1200 (hd 64, 3 tiles) and 1250 (hd
 // 128, 2 tiles) clocks; alone, the softmax takes 1286 and 993 for it.  Both run
 // at once and take about 1500 together: two pipes that wait on one another
-// through barriers of about 100 clocks.  Without a window, 4 x 4096 rows with 12
-// heads of 64 run at 1020 TFLOP/s and 2 x 4096 with 30 heads of 128 at 1530; with
-// one, partly seen tiles and the masks and biases of their pairs cost the rest.
+// through barriers of about 100 clocks.  Without a window or bias, 2 x 4224 rows with
+// 30 heads of 128 run at 1420 TFLOP/s; with a window, partly seen tiles and the masks of
+// their pairs cost the rest.
 //
 // The form, and why:
 //   * a CTA holds an SM and NT query tiles (128 rows, a row a softmax thread), as
@@ -32,7 +32,7 @@
 //     schedules, loads and spreads biases.  S of the next key tile is issued once
 //     the softmax has this one's in registers; P goes to TMEM, half at a time, and
 //     the next scores are read behind it (read before P's stores are waited for,
-//     4 x 4096 rows of 12 heads of 64 take 217 us instead of 205);
+//     the long document takes 87 us instead of 81);
 //   * a CTA that is done takes over the place of one that has not started
 //     (cluster launch control), so that the next item's loads and first products
 //     run under the last one's softmax and stores.  Items with the most keys go
@@ -50,10 +50,12 @@
 //     are on their way (two texts: 4.6 us instead of 6.8 by one warp), later ones
 //     by the loading warp, ahead.  A row's thread then adds the float at (key -
 //     row), neighbouring rows neighbouring words (no bank conflicts), in an FMA
-//     that scales the score; reading the words costs 2 % (two or four at once, from
-//     shifted copies, gain nothing).  Beyond `reach` all distances of a side share
-//     one bucket: there the bias is one number for the tile and goes into the
-//     exponent's offset, at no cost a key;
+//     that scales the score: a pass of its own, some 800 clocks a step of three tiles.
+//     Where every tile is near (4 x 1024 rows of 12 heads of 64, 320 buckets to 800)
+//     the call takes 25.7 us instead of the 18.2 without a bias.  Beyond `reach`
+//     all distances of a side share one bucket: there the bias is one number for the tile
+//     and goes into the exponent's offset, at no cost a key (32 buckets to 128: 19.9 us
+//     there; two images 412 instead of 387; packed texts 42.3 instead of 35);
 //   * one copy of each role's code, rare cases short rather than fast, no branch in
 //     the softmax's loop that saves work only sometimes: the instruction caches and
 //     the loop's one long schedule bound it (5 to 15 %: leaving out the exponentials
@@ -66,12 +68,12 @@
 // Every mbarrier wait is bounded, as in attn.cu; the limit grows with the keys that a row
 // sees, as what is waited for does.
 //
-// Measured (a call among others): packed texts (32, 19 .. 955 rows, 8 heads of 64)
-// with a window of 512 and 4 sinks 33.4 us, with a bias 41.7; 30001 rows, 12 heads
-// of 64, window 256, 64 sinks 81 us (653 TFLOP/s of the visible pairs); grouped
-// causal heads (8191 rows, 32 over 8 of 128, window 1023) 125 us (1030); two images
-// of 4224 rows, 30 heads of 128: window 1056 and 32 sinks 201 us (1210), bias 407 us
-// (1350, 71 % of the measured bf16 rate).
+// Measured (a call among others; those of heads of 128 vary by 3 % with the clock):
+// packed texts (32, 19 .. 955 rows, 8 heads of 64) with a window of 512 and 4 sinks 33.6
+// us, with a bias 42.2; 30001 rows, 12 heads of 64, window 256, 64 sinks 82 us (645
+// TFLOP/s of the visible pairs); grouped causal heads (8191 rows, 32 over 8 of 128, window
+// 1023) 128 us (1010); two images of 4224 rows, 30 heads of 128: window 1056 and 32 sinks
+// 209 us (1160), bias 416 us (1320, 70 % of the measured bf16 rate).
 #include <cuda.h>
 #include <float.h>
 #include <math.h>
@@ -973,10 +975,10 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
         const float c = p.scale_log2;
         // Partial maxima of a row; whether S is given back behind them or as soon as it is in
         // registers; whether the next tile is looked over behind P or beside the second half.  All
-        // only order the same work.  Measured, us (full attention, 4 x 4096 rows of 12 heads of 64;
-        // 2 x 4096 of 30 of 128; two images with bias): maxima 2 204 341 412, 3 201 335 407, 8 (before
-        // the others) 231 347 415; S given back late 217 341 434 (before), at once 226 347 399; looked
-        // over late 205 347 406, beside the second half 205 337 410 (packed texts with bias 41.8, 44.0).
+        // only order the same work.  Measured, us (packed texts, images with sinks, the wide
+        // reach, images with bias, causal window with bias): as here 33.6 204 25.5 407 92.9; two maxima
+        // 33.7 204 26.1 406 92.5; S given back the other way 34.1 206 25.0 409 94.3; looked
+        // over the other way 34.6 208 25.9 407 93.0.
         constexpr int NM = 3;
         constexpr bool FREE_LATE = HD == 64 || !BIAS;
         constexpr bool LOOK_LATE = HD == 64 || BIAS;
@@ -1109,7 +1111,8 @@ __global__ void __launch_bounds__(SLayout<HD, RING>::NTHREADS, 1) attn_span_kern
                 for (int i = NM; i < 32; ++i) mp[i % NM] = fmax3(mp[i % NM], __uint_as_float(va[i]), __uint_as_float(vb[i]));
                 const float mx = fmaf(fmax3(mp[0], mp[1], mp[2]), cs, cb);
                 // it moves when a row grew by more than 2^20 (P, sums and O have f32's exponents to spare;
-                // moves cost a pass over O: by 2^8 grouped causal heads take 138 us instead of 131)
+                // moves cost a pass over O: by 2^8 grouped causal heads take 129 us instead of 125, the causal
+                // window with bias 102 instead of 93)
                 const bool resc = mx > m_used + 20.f;
                 const uint64_t c2 = f2_pack(cs, cs);
                 uint64_t nm2 = f2_pack(cb + nm0, cb + nm0);
