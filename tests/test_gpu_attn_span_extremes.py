@@ -25,3 +25,23 @@ def test_values_whose_sum_passes_the_type(hd, bias):
     out = call(qkv, ln, nq, nq, hd, 60, -1, 2, hd ** -0.5, table=table, rel=rel)
     compare(f"large values {hd} bias={bias}", out, ref, mag)
     te.check()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("bias", [False, True])
+def test_tiny_values_beside_a_lost_one(hd, bias):
+    """Rows that are computed again because a tile of theirs holds a NaN keep values near
+    the type's smallest (a product of a weight and such a value may not be taken down by 2^29)."""
+    import torch
+    ln, nq, span = [400, 90], 2, (60, 20, 3)
+    w = nq * hd
+    qkv = panel(sum(ln), 3 * w, 93)
+    qkv[:, 2 * w:] = (qkv[:, 2 * w:].float() * 2.0 ** -116).to(torch.bfloat16)
+    rel = (32, 128, True) if bias else None
+    table = torch.randn(32, nq, device="cuda") if bias else None
+    ref, mag = attention(qkv, ln, nq, nq, hd, *span, hd ** -0.5, table=table, rel=rel)
+    qkv[30, w:] = float("nan")                        # beside the sinks: in a tile of every row
+    out = call(qkv, ln, nq, nq, hd, *span, hd ** -0.5, table=table, rel=rel)
+    hidden = list(range(91, 490)) + list(range(0, 10))
+    compare(f"tiny values {hd} bias={bias}", out[hidden], ref[hidden], mag[hidden])
+    te.check()

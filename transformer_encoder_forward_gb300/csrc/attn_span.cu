@@ -476,6 +476,9 @@ __device__ __noinline__ void mend_rows(const SpanParams &p, const float *bias, i
         }
         keys_of(qi[0], qi[R - 1]);
         const int n = ns + hi - lo;
+        // weights are taken down by a power of two above n, so that no sum of n values passes
+        // the largest of them (by no more: tiny values would be lost)
+        const int down = 32 - __clz(n);
         uint32_t lost = 0;                               // a bit a row
 #pragma unroll 1
         for (int j = hint >= 0 ? -32 : 0; j < n && lost != (1u << R) - 1; j += 32) {
@@ -520,7 +523,7 @@ __device__ __noinline__ void mend_rows(const SpanParams &p, const float *bias, i
                 pr[r] = hw_exp2(s[r] - ref);
                 m[r] = mn;
                 l[r] = l[r] * alpha + pr[r];
-                pr[r] *= 0x1p-29f;                       // no sum of at most 2^29 values passes the largest of them
+                pr[r] *= __int_as_float((127 - down) << 23);
 #pragma unroll
                 for (int c = 0; c < C; ++c) o[r][c] *= alpha;
             }
@@ -545,7 +548,7 @@ __device__ __noinline__ void mend_rows(const SpanParams &p, const float *bias, i
 #pragma unroll
             for (int c = 0; c < C; ++c)
                 out[(long long)(qi[r] - r0) * p.ldo + c] =
-                    __float2bfloat16_rn(lost >> r & 1 ? NAN : l[r] == 0.f ? 0.f : o[r][c] / l[r] * 0x1p29f);
+                    __float2bfloat16_rn(lost >> r & 1 ? NAN : l[r] == 0.f ? 0.f : o[r][c] / l[r] * __int_as_float((127 + down) << 23));
         }
     }
 }
